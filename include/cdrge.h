@@ -210,6 +210,175 @@ cdrge_status cdrge_step_noalloc(const cdrge_config* cfg, void* params, const int
 /* Size in bytes of the static per-device scratch cdrge_step_noalloc uses. */
 size_t cdrge_noalloc_max_workspace_bytes(void);
 
+/* ============================================================================================
+ * Operators of a population of language models.
+ *
+ * A step of the path above evaluates many models that share their weights. The calls below give
+ * the same evaluation to models that differ by a low-rank term instead of a full sign probe, that
+ * recur through a state space instead of an LSTM cell, and that learn from a teacher instead of
+ * the next token: a projection shared by all rows with a low-rank adapter by row, a selective
+ * scan with its short causal convolution, and a distillation loss whose mean by model is what
+ * cdrge_update takes as a model's loss.
+ *
+ * They need no context. Every call enqueues on `stream` (a hipStream_t; NULL is the default
+ * stream) and returns; pointers are device memory of the current device, which must be the
+ * stream's. Nothing is allocated, no call waits, and every call may be captured into a graph.
+ * dtype is CDRGE_F32 or CDRGE_BF16 and types the tensors written below as `T`; strides count
+ * elements between consecutive rows, whose own elements are adjacent. Sums, running maxima,
+ * decays and states are float32 or wider; results are rounded to T once, to nearest even.
+ * Inputs and outputs must not overlap unless a call says so. Index arrays are read on the
+ * device: an entry out of range never reads or writes out of bounds, its effect is stated below.
+ * A workspace serves one call at a time: calls that may overlap (two streams, two graphs
+ * replayed at once) need one each. Its contents need no preparation.
+ * ============================================================================================ */
+
+/* ---- Selective scan -------------------------------------------------------------------------
+ * Per token, a row of xbc holds n_heads * head_dim inputs, then n_groups * state_dim entries B,
+ * then as many entries C (`channels` in all); dt holds n_heads step sizes before their bias and
+ * softplus. Head h belongs to group h / (n_heads / n_groups). With q the token's place in its
+ * sequence (positions + index within the call), e = conv_width and sequences starting at zero:
+ *
+ *   u_q     = silu(conv_bias + sum_{j < e} conv_weight[:, j] xbc_{q - e + 1 + j})     (x, B, C = u)
+ *   step_q  = softplus(dt_q + dt_bias)                                               (by head)
+ *   S_q     = exp(step_q decay) S_{q-1} + step_q x_q B_q^T                           [head_dim][state_dim]
+ *   y_q     = S_q C_q + skip x_q, times silu(z_q) when z is given
+ */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* CDRGE_F32 or CDRGE_BF16 */
+  int32_t n_heads;
+  int32_t head_dim;     /* 1 .. 256 */
+  int32_t n_groups;     /* divides n_heads */
+  int32_t state_dim;    /* 1 .. 256 */
+  int32_t conv_width;   /* 2 .. 4 */
+} cdrge_scan_config;
+
+typedef struct {
+  const void* conv_weight; /* T [channels][conv_width], the last column meets the newest token */
+  const void* conv_bias;   /* T [channels], or NULL */
+  const float* decay;      /* [n_heads], negative for a state that fades */
+  const float* skip;       /* [n_heads], or NULL */
+  const float* dt_bias;    /* [n_heads], or NULL */
+} cdrge_scan_weights;
+
+/* Carried state. Slot s of a cache of n_slots holds one sequence's ring of the last conv_width
+ * rows of xbc (row q at entry q mod conv_width) and its S of every head. conv_in and ssm_in are
+ * read, conv_out and ssm_out written; an output may be its input's own pointer (update in place),
+ * and otherwise gets the slot's whole contents, while slots that no sequence of the call names
+ * are left as they are. All four are given, or none (every sequence starts at zero, nothing is
+ * kept; slots and positions must be NULL then). */
+typedef struct {
+  const void* xbc;          /* T [n_tokens][channels] */
+  int64_t xbc_stride;
+  const void* dt;           /* T [n_tokens][n_heads] */
+  int64_t dt_stride;
+  const void* z;            /* T [n_tokens][n_heads * head_dim], or NULL */
+  int64_t z_stride;
+  void* y;                  /* T [n_tokens][n_heads * head_dim] */
+  int64_t y_stride;
+  int64_t n_tokens;         /* 0 .. 2^30 */
+  int32_t n_seqs;           /* 1 .. 2^20 */
+  int32_t n_slots;
+  const int32_t* offsets;   /* [n_seqs + 1]: sequence i has the rows offsets[i] .. offsets[i+1] - 1
+                               (may be none); NULL: n_tokens / n_seqs rows each, exactly */
+  const int32_t* slots;     /* [n_seqs]; NULL: sequence i has slot i */
+  const int32_t* positions; /* [n_seqs]: tokens that the slot has seen before this call; zero (or
+                               less) starts the sequence at zero whatever the slot holds */
+  const void* conv_in;      /* T [n_slots][conv_width][channels], 16-byte aligned */
+  void* conv_out;
+  const float* ssm_in;      /* [n_slots][n_heads][head_dim][state_dim], 16-byte aligned */
+  float* ssm_out;
+} cdrge_scan_io;
+
+/* Workspace, in bytes, of cdrge_scan_prompt for n_tokens tokens in n_seqs sequences (256-byte
+ * aligned base required). */
+cdrge_status cdrge_scan_workspace_bytes(const cdrge_scan_config* cfg, int64_t n_tokens, int32_t n_seqs,
+                                        size_t* bytes_out);
+
+/* Whole prompts, or continued ones. positions NULL: every sequence starts at zero. Rows of y
+ * outside every sequence are left as they are. Offsets that fall or leave [0, n_tokens] are
+ * clamped into a rising row. A sequence whose slot is negative keeps no state (and starts at
+ * zero). One whose slot is n_slots or more, or is named by an earlier sequence of the call, gets
+ * NaN rows and touches no state. A token that is not finite may spoil outputs of its own sequence
+ * from up to 63 tokens before it; other sequences are not affected. */
+cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_weights* weights,
+                               const cdrge_scan_io* io, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of n_seqs = n_tokens sequences (offsets must be NULL, the state and positions
+ * given). A row with a negative slot is padding: its y row and every state are left as they are.
+ * Slots out of range or named twice: as for cdrge_scan_prompt. */
+cdrge_status cdrge_scan_step(const cdrge_scan_config* cfg, const cdrge_scan_weights* weights,
+                             const cdrge_scan_io* io, void* stream);
+
+/* ---- Low-rank adapters beside a shared projection --------------------------------------------
+ *   y_r = weight x_r + bias + scale_r up_a (down_a x_r),   a = row_adapter[r], scale_r = row_scale[r]
+ * The rows of one antithetic pair of low-rank probes name the same adapter with scales of either
+ * sign; the rows of requests name their own. */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* CDRGE_F32 or CDRGE_BF16 */
+  int32_t in_features;  /* K, 1 .. 2^20 */
+  int32_t out_features; /* O, 1 .. 2^20 */
+  int32_t n_adapters;   /* A, 0 .. 2^20 */
+  int32_t max_rank;     /* R, 1 .. 128 */
+} cdrge_adapter_config;
+
+typedef struct {
+  const void* weight;   /* T [O][K] */
+  int64_t weight_stride;
+  const void* bias;     /* T [O], or NULL */
+  const void* down;     /* T [A][R][K] */
+  const void* up;       /* T [A][O][R] */
+  const int32_t* ranks; /* [A]: the rank in use of each adapter (entries past it are not used,
+                           whatever they hold; clamped into [0, R]), or NULL: R each */
+} cdrge_adapter_weights;
+
+/* Workspace, in bytes, of cdrge_adapter_project for n_rows rows (256-byte aligned base required). */
+cdrge_status cdrge_adapter_workspace_bytes(const cdrge_adapter_config* cfg, int64_t n_rows, size_t* bytes_out);
+
+/* x: T [n_rows][K]; row_adapter: int32 [n_rows], negative for no adapter, or NULL (no row has
+ * one); row_scale: float32 [n_rows] or NULL (1); y: T [n_rows][O]. n_rows may be 0, up to 2^30. A row
+ * whose adapter is A or more gets NaN. A row's result does not depend on what other rows' inputs
+ * or adapters hold, nor on their order. */
+cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_adapter_weights* weights,
+                                   int64_t n_rows, const void* x, int64_t x_stride, const int32_t* row_adapter,
+                                   const float* row_scale, void* y, int64_t y_stride, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ---- Distillation from a teacher's top logits ------------------------------------------------
+ * Row r has top_k teacher entries (id, logit); an entry with a negative id or a logit of minus
+ * infinity is absent. With tau the temperature, p the softmax of the present entries' logits / tau
+ * and q the softmax of the student's whole row / tau:
+ *
+ *   row_loss = tau^2 sum_j p_j (log p_j - log q_{id_j}),   d row_loss / d logit_v = tau (q_v - sum_{j: id_j = v} p_j)
+ *
+ * A row without a present entry is not scored: its loss and gradient are zero. An id of vocab or
+ * more makes its row NaN. An id may come twice. losses[m] is the mean of the scored rows of model
+ * m, which owns the rows m (n_rows / n_models) onwards (NaN if it has none): the layout that
+ * cdrge_update reads for 2K perturbed models. Sums run in a fixed order. */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* type T of the logits and their gradient */
+  int32_t vocab;        /* 1 .. 2^24 */
+  int32_t top_k;        /* 1 .. 1024 */
+  int32_t n_models;     /* 1 .. 2^20; divides the number of rows */
+  float temperature;    /* > 0 */
+} cdrge_distill_config;
+
+/* logits: T [n_rows][vocab]; ids: int32 [n_rows][top_k]; teacher: float32 [n_rows][top_k];
+ * row_losses: float32 [n_rows]; losses: float32 [n_models], or NULL. n_rows may be 0, up to 2^30. */
+cdrge_status cdrge_distill_losses(const cdrge_distill_config* cfg, int64_t n_rows, const void* logits,
+                                  int64_t logits_stride, const int32_t* ids, const float* teacher,
+                                  float* row_losses, float* losses, void* stream);
+
+/* The same losses, and dlogits[r] = row_grad[r] * d row_loss_r / d logits_r (row_grad: float32
+ * [n_rows], or NULL: 1) in T. dlogits may be logits itself (same pointer and stride). A logit of
+ * minus infinity has q = 0. */
+cdrge_status cdrge_distill_grad(const cdrge_distill_config* cfg, int64_t n_rows, const void* logits,
+                                int64_t logits_stride, const int32_t* ids, const float* teacher,
+                                const float* row_grad, float* row_losses, float* losses, void* dlogits,
+                                int64_t dlogits_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,6 +41,59 @@ def make_config(n_layers, vocab, embed, hidden, batch, seq_len, n_probes, dtype,
                         probes_per_chunk, dt, eps, lr, base_seed)
 
 
+class cdrge_scan_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("state_dim", ctypes.c_int32),
+                ("conv_width", ctypes.c_int32)]
+
+
+class cdrge_scan_weights(ctypes.Structure):
+    _fields_ = [("conv_weight", ctypes.c_void_p), ("conv_bias", ctypes.c_void_p), ("decay", ctypes.c_void_p),
+                ("skip", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class cdrge_scan_io(ctypes.Structure):
+    _fields_ = [("xbc", ctypes.c_void_p), ("xbc_stride", ctypes.c_int64), ("dt", ctypes.c_void_p),
+                ("dt_stride", ctypes.c_int64), ("z", ctypes.c_void_p), ("z_stride", ctypes.c_int64),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64), ("n_tokens", ctypes.c_int64),
+                ("n_seqs", ctypes.c_int32), ("n_slots", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("conv_in", ctypes.c_void_p),
+                ("conv_out", ctypes.c_void_p), ("ssm_in", ctypes.c_void_p), ("ssm_out", ctypes.c_void_p)]
+
+
+class cdrge_adapter_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32), ("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32)]
+
+
+class cdrge_adapter_weights(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("up", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
+
+
+class cdrge_distill_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("n_models", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
+_OPERATOR_DTYPES = {"f32": CDRGE_F32, "bf16": CDRGE_BF16}
+
+
+def make_scan_config(n_heads, head_dim, n_groups, state_dim, conv_width, dtype) -> cdrge_scan_config:
+    return cdrge_scan_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), n_heads, head_dim, n_groups,
+                             state_dim, conv_width)
+
+
+def make_adapter_config(in_features, out_features, n_adapters, max_rank, dtype) -> cdrge_adapter_config:
+    return cdrge_adapter_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), in_features, out_features,
+                                n_adapters, max_rank)
+
+
+def make_distill_config(vocab, top_k, n_models, temperature, dtype) -> cdrge_distill_config:
+    return cdrge_distill_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), vocab, top_k, n_models,
+                                temperature)
+
+
 def config_from_preset(p) -> cdrge_config:
     return make_config(p.n_layers, p.vocab, p.embed, p.hidden, p.batch, p.seq_len, p.n_probes, p.dtype,
                        p.eps, p.lr, p.base_seed, p.probes_per_chunk)
@@ -75,6 +128,21 @@ EXPORTS = {
     "cdrge_step_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64,
                                           ctypes.c_void_p, ctypes.c_void_p]),
     "cdrge_noalloc_max_workspace_bytes": (ctypes.c_size_t, []),
+    "cdrge_scan_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+    "cdrge_scan_prompt": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_void_p]),
+    "cdrge_scan_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "cdrge_adapter_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+    "cdrge_adapter_project": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                             ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "cdrge_distill_losses": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p]),
+    "cdrge_distill_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
 }
 
 
@@ -263,3 +331,270 @@ class Context:
             self.close()
         except Exception:
             pass
+
+
+# ---- operators of a population of models ---------------------------------------------------------
+#
+# The C entry points take structures and pointers; the classes below hold an operator's weights and
+# check the tensors of a call (type, shape, device, rows whose elements are adjacent) before their
+# pointers cross the boundary. A call runs on torch's current stream of the tensors' device unless
+# one is given, allocates its workspace there through torch, and keeps nothing for the next call.
+
+def cdrge_scan_workspace_bytes(cfg: cdrge_scan_config, n_tokens: int, n_seqs: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().cdrge_scan_workspace_bytes(ctypes.byref(cfg), n_tokens, n_seqs, ctypes.byref(out)),
+           "cdrge_scan_workspace_bytes")
+    return int(out.value)
+
+
+def cdrge_scan_prompt(cfg, weights: cdrge_scan_weights, io: cdrge_scan_io, workspace, stream: int):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().cdrge_scan_prompt(ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(io), _ptr(workspace), nbytes,
+                                   stream), "cdrge_scan_prompt")
+
+
+def cdrge_scan_step(cfg, weights: cdrge_scan_weights, io: cdrge_scan_io, stream: int):
+    _check(lib().cdrge_scan_step(ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(io), stream), "cdrge_scan_step")
+
+
+def cdrge_adapter_workspace_bytes(cfg: cdrge_adapter_config, n_rows: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().cdrge_adapter_workspace_bytes(ctypes.byref(cfg), n_rows, ctypes.byref(out)),
+           "cdrge_adapter_workspace_bytes")
+    return int(out.value)
+
+
+def cdrge_adapter_project(cfg, weights: cdrge_adapter_weights, n_rows, x, row_adapter, row_scale, y, workspace,
+                          stream: int):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().cdrge_adapter_project(ctypes.byref(cfg), ctypes.byref(weights), n_rows, x.data_ptr(), _row_stride(x),
+                                       _ptr(row_adapter), _ptr(row_scale), y.data_ptr(), _row_stride(y),
+                                       _ptr(workspace), nbytes, stream), "cdrge_adapter_project")
+
+
+def cdrge_distill_losses(cfg, logits, ids, teacher, row_losses, losses, stream: int):
+    _check(lib().cdrge_distill_losses(ctypes.byref(cfg), logits.shape[0], logits.data_ptr(), _row_stride(logits),
+                                      ids.data_ptr(), teacher.data_ptr(), row_losses.data_ptr(), _ptr(losses), stream),
+           "cdrge_distill_losses")
+
+
+def cdrge_distill_grad(cfg, logits, ids, teacher, row_grad, row_losses, losses, dlogits, stream: int):
+    _check(lib().cdrge_distill_grad(ctypes.byref(cfg), logits.shape[0], logits.data_ptr(), _row_stride(logits),
+                                    ids.data_ptr(), teacher.data_ptr(), _ptr(row_grad), row_losses.data_ptr(),
+                                    _ptr(losses), dlogits.data_ptr(), _row_stride(dlogits), stream),
+           "cdrge_distill_grad")
+
+
+def _row_stride(t) -> int:
+    # a single row may have any stride, also one below its length; the library wants at least that
+    return max(t.stride(0), t.shape[1])
+
+
+def _tensor(name, t, dtype, shape, device, rows=False):
+    """Checks one argument. rows: a matrix whose rows may lie further apart than their length."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the operator's weights on {device}")
+    if rows:
+        if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0 or t.stride(0) < shape[1] and shape[0] > 1:
+            raise ValueError(f"{name} needs rows of adjacent elements that do not overlap, not strides {t.stride()}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class _Operator:
+    """What the operators share: the element type, the device, and running on its stream."""
+
+    def __init__(self, cfg, device):
+        import torch
+        self.cfg = cfg
+        if cfg.dtype not in (CDRGE_F32, CDRGE_BF16):
+            raise CdrgeError(1, type(self).__name__)
+        self.dtype = torch.float32 if cfg.dtype == CDRGE_F32 else torch.bfloat16
+        self.device = device
+        self._torch = torch
+        self._lib = lib()
+
+    def _run(self, call, nbytes, stream):
+        """call(workspace, stream handle) on the operator's device. The workspace belongs to the call's
+        stream, so that torch gives its memory to nobody before the call has run."""
+        torch = self._torch
+        cuda = torch.cuda
+        if stream is None and self.device.index == cuda.current_device():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+            call(ws, cuda.current_stream().cuda_stream)
+            return
+        with cuda.device(self.device):
+            on = cuda.current_stream() if stream is None else stream
+            if on.device != self.device:
+                raise ValueError(f"the stream is on {on.device}, the operator on {self.device}")
+            with cuda.stream(on):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+                call(ws, on.cuda_stream)
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+class ScanLayer(_Operator):
+    """Selective scan with its short causal convolution (cdrge_scan_prompt, cdrge_scan_step).
+
+    conv_weight [channels, conv_width] and conv_bias [channels] or None in the layer's type; decay, skip and dt_bias
+    [n_heads] in float32, the latter two or None. channels = n_heads * head_dim + 2 * n_groups * state_dim.
+    """
+
+    def __init__(self, cfg: cdrge_scan_config, conv_weight, conv_bias, decay, skip=None, dt_bias=None):
+        super().__init__(cfg, _cuda_device(conv_weight, "conv_weight"))
+        torch = self._torch
+        cdrge_scan_workspace_bytes(cfg, 0, 1)  # raises for a configuration that is not valid or supported
+        self.width = cfg.n_heads * cfg.head_dim
+        self.channels = self.width + 2 * cfg.n_groups * cfg.state_dim
+        _tensor("conv_weight", conv_weight, self.dtype, (self.channels, cfg.conv_width), self.device)
+        if conv_bias is not None:
+            _tensor("conv_bias", conv_bias, self.dtype, (self.channels,), self.device)
+        for name, t in (("decay", decay), ("skip", skip), ("dt_bias", dt_bias)):
+            if t is not None or name == "decay":
+                _tensor(name, t, torch.float32, (cfg.n_heads,), self.device)
+        self._held = (conv_weight, conv_bias, decay, skip, dt_bias)
+        self.weights = cdrge_scan_weights(*(None if t is None else t.data_ptr() for t in self._held))
+
+    def _io(self, xbc, dt, y, n_seqs, z, offsets, slots, positions, conv_in, ssm_in, conv_out, ssm_out):
+        cfg, torch, dev, n = self.cfg, self._torch, self.device, xbc.shape[0]
+        _tensor("xbc", xbc, self.dtype, (n, self.channels), dev, rows=True)
+        _tensor("dt", dt, self.dtype, (n, cfg.n_heads), dev, rows=True)
+        _tensor("y", y, self.dtype, (n, self.width), dev, rows=True)
+        if z is not None:
+            _tensor("z", z, self.dtype, (n, self.width), dev, rows=True)
+        if offsets is not None:
+            _tensor("offsets", offsets, torch.int32, (n_seqs + 1,), dev)
+        if slots is not None:
+            _tensor("slots", slots, torch.int32, (n_seqs,), dev)
+        if positions is not None:
+            _tensor("positions", positions, torch.int32, (n_seqs,), dev)
+        n_slots = 0
+        if (conv_in is None) != (ssm_in is None):
+            raise ValueError("the convolution's state and the scan's are given together or not at all")
+        if conv_in is not None:
+            n_slots = ssm_in.shape[0]
+            conv_out = conv_in if conv_out is None else conv_out
+            ssm_out = ssm_in if ssm_out is None else ssm_out
+            for name, t in (("the convolution's state", conv_in), ("conv_out", conv_out)):
+                _tensor(name, t, self.dtype, (n_slots, cfg.conv_width, self.channels), dev)
+            for name, t in (("the scan's state", ssm_in), ("ssm_out", ssm_out)):
+                _tensor(name, t, torch.float32, (n_slots, cfg.n_heads, cfg.head_dim, cfg.state_dim), dev)
+        elif conv_out is not None or ssm_out is not None:
+            raise ValueError("an output state needs the states that are read")
+        return cdrge_scan_io(xbc.data_ptr(), _row_stride(xbc), dt.data_ptr(), _row_stride(dt),
+                             None if z is None else z.data_ptr(), 0 if z is None else _row_stride(z),
+                             y.data_ptr(), _row_stride(y), n, n_seqs, n_slots,
+                             None if offsets is None else offsets.data_ptr(),
+                             None if slots is None else slots.data_ptr(),
+                             None if positions is None else positions.data_ptr(),
+                             None if conv_in is None else conv_in.data_ptr(),
+                             None if conv_in is None else conv_out.data_ptr(),
+                             None if conv_in is None else ssm_in.data_ptr(),
+                             None if conv_in is None else ssm_out.data_ptr())
+
+    def prompt(self, xbc, dt, y, n_seqs, z=None, offsets=None, slots=None, positions=None, conv_state=None,
+               ssm_state=None, conv_out=None, ssm_out=None, stream=None):
+        """Whole or continued prompts: rows offsets[i] .. offsets[i + 1] - 1 (or equal shares of the rows) belong to
+        sequence i. Writes y, and the states in place unless conv_out and ssm_out are given. Returns y."""
+        io = self._io(xbc, dt, y, n_seqs, z, offsets, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
+        nbytes = cdrge_scan_workspace_bytes(self.cfg, io.n_tokens, n_seqs)
+        self._run(lambda ws, s: cdrge_scan_prompt(self.cfg, self.weights, io, ws, s), nbytes, stream)
+        return y
+
+    def step(self, xbc, dt, y, positions, conv_state, ssm_state, z=None, slots=None, conv_out=None, ssm_out=None,
+             stream=None):
+        """One token of each sequence, row i at place positions[i] of the sequence in slot slots[i] (negative: padding).
+        Writes y, and the states in place unless conv_out and ssm_out are given. Returns y."""
+        io = self._io(xbc, dt, y, xbc.shape[0], z, None, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
+        if io.n_tokens:
+            self._run(lambda ws, s: cdrge_scan_step(self.cfg, self.weights, io, s), 0, stream)
+        return y
+
+
+class AdapterProjection(_Operator):
+    """A projection shared by all rows with a low-rank adapter by row (cdrge_adapter_project).
+
+    weight [out, in] (its rows may lie apart), bias [out] or None, down [n_adapters, max_rank, in], up [n_adapters, out,
+    max_rank] in the operator's type; ranks int32 [n_adapters] or None.
+    """
+
+    def __init__(self, cfg: cdrge_adapter_config, weight, bias=None, down=None, up=None, ranks=None):
+        super().__init__(cfg, _cuda_device(weight, "weight"))
+        cdrge_adapter_workspace_bytes(cfg, 0)
+        K, O, A, R = cfg.in_features, cfg.out_features, cfg.n_adapters, cfg.max_rank
+        _tensor("weight", weight, self.dtype, (O, K), self.device, rows=True)
+        if bias is not None:
+            _tensor("bias", bias, self.dtype, (O,), self.device)
+        if A > 0:
+            if down is None or up is None:
+                raise ValueError("adapters need their down and up weights")
+            _tensor("down", down, self.dtype, (A, R, K), self.device)
+            _tensor("up", up, self.dtype, (A, O, R), self.device)
+            if ranks is not None:
+                _tensor("ranks", ranks, self._torch.int32, (A,), self.device)
+        self._held = (weight, bias, down, up, ranks)
+        p = [None if t is None else t.data_ptr() for t in self._held]
+        self.weights = cdrge_adapter_weights(p[0], _row_stride(weight), *p[1:])
+
+    def project(self, x, row_adapter, y, row_scale=None, stream=None):
+        """y[r] = weight x[r] + bias + row_scale[r] up_a (down_a x[r]), a = row_adapter[r] (negative, or row_adapter None:
+        no adapter). Returns y."""
+        n, cfg, torch = x.shape[0], self.cfg, self._torch
+        _tensor("x", x, self.dtype, (n, cfg.in_features), self.device, rows=True)
+        _tensor("y", y, self.dtype, (n, cfg.out_features), self.device, rows=True)
+        if row_adapter is not None:
+            _tensor("row_adapter", row_adapter, torch.int32, (n,), self.device)
+        if row_scale is not None:
+            _tensor("row_scale", row_scale, torch.float32, (n,), self.device)
+        nbytes = cdrge_adapter_workspace_bytes(cfg, n)
+        self._run(lambda ws, s: cdrge_adapter_project(cfg, self.weights, n, x, row_adapter, row_scale, y, ws, s), nbytes,
+                  stream)
+        return y
+
+
+class DistillLoss(_Operator):
+    """Distillation from a teacher's top logits (cdrge_distill_losses, cdrge_distill_grad)."""
+
+    def __init__(self, cfg: cdrge_distill_config, device=None):
+        import torch
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise ValueError("the operator runs on a GPU")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        super().__init__(cfg, device)
+
+    def _inputs(self, logits, ids, teacher, row_losses, losses):
+        n, cfg, torch, dev = logits.shape[0], self.cfg, self._torch, self.device
+        _tensor("logits", logits, self.dtype, (n, cfg.vocab), dev, rows=True)
+        _tensor("ids", ids, torch.int32, (n, cfg.top_k), dev)
+        _tensor("teacher", teacher, torch.float32, (n, cfg.top_k), dev)
+        _tensor("row_losses", row_losses, torch.float32, (n,), dev)
+        if losses is not None:
+            _tensor("losses", losses, torch.float32, (cfg.n_models,), dev)
+
+    def losses(self, logits, ids, teacher, row_losses, losses=None, stream=None):
+        """Fills row_losses [rows] and, if given, losses [n_models], the means by model (NaN where no row is scored)."""
+        self._inputs(logits, ids, teacher, row_losses, losses)
+        self._run(lambda ws, s: cdrge_distill_losses(self.cfg, logits, ids, teacher, row_losses, losses, s), 0, stream)
+        return row_losses
+
+    def grad(self, logits, ids, teacher, row_grad, row_losses, losses, dlogits, stream=None):
+        """The losses, and dlogits[r] = row_grad[r] d row_loss_r / d logits[r] (row_grad None: 1; losses may be None).
+        dlogits may be logits itself. Returns dlogits."""
+        self._inputs(logits, ids, teacher, row_losses, losses)
+        _tensor("dlogits", dlogits, self.dtype, logits.shape, self.device, rows=True)
+        if row_grad is not None:
+            _tensor("row_grad", row_grad, self._torch.float32, (logits.shape[0],), self.device)
+        self._run(lambda ws, s: cdrge_distill_grad(self.cfg, logits, ids, teacher, row_grad, row_losses, losses, dlogits, s),
+                  0, stream)
+        return dlogits

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "cdrge.h"
+#include "host_common.h"
 #include "kernels_bf16.h"
 #include "kernels_common.h"
 #include "kernels_f32.h"
@@ -25,11 +26,8 @@ using namespace cdrge;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 constexpr int kMaxProbes = 1024;
 constexpr int64_t kMaxF32LdsBytes = 128 * 1024;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Nearest bf16 to x (ties to even), as a float. x is finite.
 float round_bf16_host(float x) {
@@ -50,17 +48,25 @@ float probe_radius(const cdrge_config& c) {
 // Text of the last device-side failure seen by this thread (for cdrge_last_error_detail).
 thread_local char g_last_error[256] = "";
 
+}  // namespace
+
+namespace cdrge {
+
 cdrge_status device_error(const char* what, hipError_t e) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e),
                 static_cast<int>(e));
   return CDRGE_ERR_DEVICE;
 }
 
-#define CDRGE_HIP(call)                                          \
-  do {                                                           \
-    const hipError_t _e = (call);                                \
-    if (_e != hipSuccess) return device_error(#call, _e);        \
-  } while (0)
+cdrge_status workspace_error(const char* who, size_t need, size_t have) {
+  std::snprintf(g_last_error, sizeof(g_last_error),
+                "%s: needs %zu workspace bytes at a base aligned to %zu, given %zu", who, need, kAlign, have);
+  return CDRGE_ERR_WORKSPACE;
+}
+
+}  // namespace cdrge
+
+namespace {
 
 struct TensorDesc {
   uint32_t id;
