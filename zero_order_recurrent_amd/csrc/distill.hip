@@ -24,20 +24,27 @@ cdrge_status check(const cdrge_distill_config* c, int64_t n_rows, const void* lo
   return CDRGE_OK;
 }
 
-template <class T, bool kGrad, int kTeam>
+template <class T, bool kGrad, int kTeam, int kPieces>
 void launch(const DistillArgs& a, hipStream_t s) {
-  constexpr int kRows = kTeam == 64 ? 4 : 1;
-  const size_t lds = size_t(8) * a.top_k * kRows;
-  hipLaunchKernelGGL((k_distill<T, kGrad, kTeam>), dim3(static_cast<uint32_t>((a.n_rows + kRows - 1) / kRows)),
-                     dim3(kTeam == 64 ? 256 : kTeam), lds, s, a);
+  constexpr int kThreads = distill_threads(kTeam), kRows = kThreads / kTeam;
+  const size_t lds = size_t(8) * ((a.top_k + 3) & ~3) * kRows;
+  hipLaunchKernelGGL((k_distill<T, kGrad, kTeam, kPieces>), dim3(static_cast<uint32_t>((a.n_rows + kRows - 1) / kRows)),
+                     dim3(kThreads), lds, s, a);
 }
 
+// Threads of a row and pieces a thread: the fewest threads that hold the row in at most 8 pieces each, so that short rows share a workgroup and long ones have enough loads in flight.
+// A team of 16 holds at most 256 teacher entries in its registers while the gradient is written.
 template <class T, bool kGrad>
 void launch_team(const DistillArgs& a, hipStream_t s) {
-  if (a.vocab <= 2048)
-    launch<T, kGrad, 64>(a, s);
-  else
-    launch<T, kGrad, 256>(a, s);
+  const int pieces = (a.vocab + DistillRow<T>::kPer - 1) / DistillRow<T>::kPer;
+  if (pieces <= 16 * 4 && a.top_k <= 256) return pieces <= 16 ? launch<T, kGrad, 16, 1>(a, s) : launch<T, kGrad, 16, 4>(a, s);
+  if (pieces <= 64 * 2) return launch<T, kGrad, 64, 2>(a, s);
+  if (pieces <= 64 * 8) return launch<T, kGrad, 64, 8>(a, s);
+  if (pieces <= 256 * 4) return launch<T, kGrad, 256, 4>(a, s);
+  if (pieces <= 256 * 8) return launch<T, kGrad, 256, 8>(a, s);
+  if (pieces <= 512 * 8) return launch<T, kGrad, 512, 8>(a, s);
+  if (pieces <= 1024 * 8) return launch<T, kGrad, 1024, 8>(a, s);
+  return launch<T, kGrad, 1024, 0>(a, s);
 }
 
 template <bool kGrad>
@@ -50,8 +57,7 @@ cdrge_status enqueue(const cdrge_distill_config* c, const DistillArgs& a, float*
     CDRGE_HIP(hipGetLastError());
   }
   if (losses) {
-    hipLaunchKernelGGL(k_distill_mean, dim3(c->n_models), dim3(256), 0, s, a.row_losses, a.ids, a.teacher, a.top_k,
-                       a.n_rows / c->n_models, losses);
+    hipLaunchKernelGGL(k_distill_mean, dim3(c->n_models), dim3(256), 0, s, a.row_losses, a.n_rows / c->n_models, losses);
     CDRGE_HIP(hipGetLastError());
   }
   return CDRGE_OK;

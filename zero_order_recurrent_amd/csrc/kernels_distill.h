@@ -23,25 +23,39 @@ struct DistillArgs {
   float tau;
 };
 
-// Sum or maximum over the kTeam threads that share a row. part: kTeam / 64 floats of LDS.
-template <int kTeam, bool kMax>
-__device__ __forceinline__ float team_reduce(float v, float* part) {
-  v = kMax ? wave_max(v) : wave_sum(v);
-  if (kTeam == 64) return v;
-  const int wave = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[wave] = v;
-  __syncthreads();
-  float r = part[0];
+// kN sums or maxima over the kTeam threads that share a row. part: kN * kTeam / 64 floats of LDS
+// that no other reduction of the row uses, so that one barrier does.
+template <int kTeam, bool kMax, int kN>
+__device__ __forceinline__ void team_reduce(float (&v)[kN], float* part) {
 #pragma unroll
-  for (int i = 1; i < kTeam / 64; ++i) r = kMax ? fmaxf(r, part[i]) : r + part[i];
-  return r;
+  for (int m = (kTeam < 64 ? kTeam : 64) / 2; m > 0; m >>= 1)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const float o = __shfl_xor(v[n], m);
+      v[n] = kMax ? fmaxf(v[n], o) : v[n] + o;
+    }
+  if (kTeam <= 64) return;
+  constexpr int kWaves = kTeam / 64;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) part[n * kWaves + (threadIdx.x >> 6)] = v[n];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    v[n] = part[n * kWaves + (threadIdx.x & (kWaves - 1))];
+#pragma unroll
+    for (int m = kWaves / 2; m > 0; m >>= 1) {
+      const float o = __shfl_xor(v[n], m);
+      v[n] = kMax ? fmaxf(v[n], o) : v[n] + o;
+    }
+  }
 }
 
-// Orders the team's memory accesses before it against those after it.
+// Orders the team's memory accesses before it against those after it (a team of at most one wave
+// runs in step).
 template <int kTeam>
 __device__ __forceinline__ void team_sync() {
-  if (kTeam == 64) {
+  if (kTeam <= 64) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     __builtin_amdgcn_wave_barrier();
   } else {
@@ -49,114 +63,209 @@ __device__ __forceinline__ void team_sync() {
   }
 }
 
-// One row by kTeam threads (64: four rows by a workgroup of 256).
-template <class T, bool kGrad, int kTeam>
-__global__ __launch_bounds__(kTeam == 64 ? 256 : kTeam) void k_distill(DistillArgs a) {
-  extern __shared__ float lds[];  // per row of the workgroup: top_k probabilities, top_k ids
-  __shared__ float part[16];
-  const int lane = kTeam == 64 ? (threadIdx.x & 63) : threadIdx.x;
-  const int team = kTeam == 64 ? (threadIdx.x >> 6) : 0;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kTeam == 64 ? 4 : 1) + team;
-  if (row >= a.n_rows) return;  // a whole wave, which waits for nobody below
-  float* prob = lds + 2 * team * a.top_k;
-  int* id = reinterpret_cast<int*>(prob + a.top_k);
+// A row as pieces of 16 bytes, wherever it starts (global memory takes such accesses at any element's
+// alignment). Sums group by piece, so a row's results do not depend on where it lies. Elements past
+// the row's end read as minus infinity and are neither loaded nor stored.
+template <class T>
+struct DistillRow {
+  static constexpr int kPer = 16 / sizeof(T);
+  int V, pieces;
+  __device__ __forceinline__ DistillRow(int vocab) : V(vocab), pieces((vocab + kPer - 1) / kPer) {}
+  __device__ __forceinline__ uint4 load(const T* x, int b) const {
+    uint4 r;
+    if ((b + 1) * kPer <= V) {
+      __builtin_memcpy(&r, x + b * kPer, 16);
+      return r;
+    }
+    T e[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = b * kPer + i < V ? x[b * kPer + i] : from_float<T>(-__builtin_inff());
+    __builtin_memcpy(&r, e, 16);
+    return r;
+  }
+  __device__ __forceinline__ void store(T* d, int b, uint4 r) const {
+    if ((b + 1) * kPer <= V) {
+      __builtin_memcpy(d + b * kPer, &r, 16);
+      return;
+    }
+    T e[kPer];
+    __builtin_memcpy(e, &r, 16);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (b * kPer + i < V) d[b * kPer + i] = e[i];
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void piece_max(uint4 r, float& m) {
+  T e[16 / sizeof(T)];
+  __builtin_memcpy(e, &r, 16);
+#pragma unroll
+  for (int i = 0; i < int(16 / sizeof(T)); ++i) m = fmaxf(m, to_float(e[i]));
+}
+template <class T>
+__device__ __forceinline__ float piece_sum(uint4 r, float shift, float scale) {
+  T e[16 / sizeof(T)];
+  __builtin_memcpy(e, &r, 16);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < int(16 / sizeof(T)); ++i) s += __builtin_amdgcn_exp2f(__builtin_fmaf(to_float(e[i]), scale, shift));
+  return s;
+}
+template <class T>
+__device__ __forceinline__ uint4 piece_grad(uint4 r, float shift, float scale, float up) {
+  T e[16 / sizeof(T)];
+  __builtin_memcpy(e, &r, 16);
+#pragma unroll
+  for (int i = 0; i < int(16 / sizeof(T)); ++i)
+    e[i] = from_float<T>(up * __builtin_amdgcn_exp2f(__builtin_fmaf(to_float(e[i]), scale, shift)));
+  __builtin_memcpy(&r, e, 16);
+  return r;
+}
+
+constexpr int distill_threads(int team) { return team < 256 ? 256 : team; }
+
+// Waves a SIMD should hold: rows wait for memory, then for each other's sums, so several have to be in flight.
+constexpr int distill_waves(int team, int pieces) { return team <= 64 ? 4 : (pieces == 8 && team < 1024 ? 6 : 8); }
+
+// One row by kTeam threads. kPieces > 0: the row stays in registers, kPieces pieces a thread, and is
+// read once. kPieces = 0 (rows too long for that): the row is read again, from the caches, for the sum
+// and for the gradient.
+template <class T, bool kGrad, int kTeam, int kPieces>
+__global__ __launch_bounds__(distill_threads(kTeam), distill_waves(kTeam, kPieces)) void k_distill(DistillArgs a) {
+  extern __shared__ float lds[];  // per row of the workgroup: kPad probabilities, as many ids
+  __shared__ float part[3 * 4 * 16];
+  constexpr int kRows = distill_threads(kTeam) / kTeam;
+  constexpr int kOwn = (kTeam == 16 ? 256 : 1024 + kTeam - 1) / kTeam;  // teacher entries of a thread
+  const int lane = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + team;
+  if (row >= a.n_rows) return;  // whole teams, of one wave at most, which wait for nobody below
+  const int V = a.vocab, k = a.top_k, k4 = (k + 3) & ~3;
+  float* prob = lds + 2 * team * k4;
+  int* id = reinterpret_cast<int*>(prob + k4);
   const T* x = static_cast<const T*>(a.logits) + row * a.logits_stride;
-  const int V = a.vocab, k = a.top_k;
+  const DistillRow<T> at(V);
   const float inv_tau = 1.f / a.tau, scale = 1.44269504088896340736f / a.tau;
   const float ninf = -__builtin_inff();
 
-  // teacher: softmax over the present entries
-  float tmax = ninf;
-  int bad = 0, present = 0;
-  for (int j = lane; j < k; j += kTeam) {
-    const int v = a.ids[row * k + j];
-    const float t = a.teacher[row * k + j];
+  uint4 held[kPieces > 0 ? kPieces : 1];
+  if (kPieces > 0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int b = lane + i * kTeam;
+      if (b < at.pieces) held[i] = at.load(x, b);
+    }
+  }
+
+  // the teacher's and the student's largest logits, whether an entry is present, whether one is bad
+  float most[4] = {ninf, ninf, 0.f, 0.f};
+  for (int j = lane; j < k4; j += kTeam) {
+    const int v = j < k ? a.ids[row * k + j] : -1;
+    const float t = j < k ? a.teacher[row * k + j] : ninf;
     const bool have = v >= 0 && !(t == ninf);
-    bad |= (have && v >= V) ? 1 : 0;
-    present |= have ? 1 : 0;
     id[j] = have ? v : -1;
     prob[j] = t;
-    if (have) tmax = fmaxf(tmax, t);
+    if (have) {
+      most[0] = fmaxf(most[0], t);
+      most[2] = 1.f;
+      if (v >= V) most[3] = 1.f;
+    }
   }
-  tmax = team_reduce<kTeam, true>(tmax, part);
-  bad = team_reduce<kTeam, true>(static_cast<float>(bad), part) > 0.f;
-  present = team_reduce<kTeam, true>(static_cast<float>(present), part) > 0.f;
+  if (kPieces > 0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (lane + i * kTeam < at.pieces) piece_max<T>(held[i], most[1]);
+  } else {
+    for (int b = lane; b < at.pieces; b += kTeam) piece_max<T>(at.load(x, b), most[1]);
+  }
+  team_reduce<kTeam, true, 4>(most, part);
+  const bool present = most[2] > 0.f, bad = most[3] > 0.f;
+  const float tmax = most[0];
+  // logits enter as x scale + shift: in units of log 2, the largest at (about) zero
+  const float shift = most[1] == ninf ? 0.f : -(most[1] * scale);
 
-  // student: largest logit, then the sum of exponentials
-  float xmax = ninf;
-  for (int v = lane; v < V; v += kTeam) xmax = fmaxf(xmax, to_float(x[v]));
-  xmax = team_reduce<kTeam, true>(xmax, part);
-  const float base = xmax == ninf ? 0.f : xmax;
-  float sum = 0.f;
-  for (int v = lane; v < V; v += kTeam) sum += __builtin_amdgcn_exp2f((to_float(x[v]) - base) * scale);
-  sum = team_reduce<kTeam, false>(sum, part);
-  const float log_sum = logf(sum);
+  float sums[2] = {0.f, 0.f};  // the student's exponentials, the teacher's
+  if (kPieces > 0) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (lane + i * kTeam < at.pieces) sums[0] += piece_sum<T>(held[i], shift, scale);
+      __builtin_amdgcn_sched_barrier(0);  // piece by piece: temporaries of one, not of all
+    }
+  } else {
+    for (int b = lane; b < at.pieces; b += kTeam) sums[0] += piece_sum<T>(at.load(x, b), shift, scale);
+  }
+  for (int j = lane; j < k; j += kTeam) sums[1] += id[j] >= 0 ? expf((prob[j] - tmax) * inv_tau) : 0.f;
+  team_reduce<kTeam, false, 2>(sums, part + 4 * 16);
+  const float log_sum = logf(sums[0]), log_mass = logf(sums[1]);
 
-  team_sync<kTeam>();
-  float mass = 0.f;
-  for (int j = lane; j < k; j += kTeam) mass += id[j] >= 0 ? expf((prob[j] - tmax) * inv_tau) : 0.f;
-  mass = team_reduce<kTeam, false>(mass, part);
-  const float log_mass = logf(mass);
-  float loss = 0.f;
-  for (int j = lane; j < k; j += kTeam) {
+  float loss[1] = {0.f}, mine[kOwn];  // mine: x scale + shift at this thread's teacher entries
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int j = lane + i * kTeam;
+    if (j >= k) continue;
     const float lp = (prob[j] - tmax) * inv_tau - log_mass;
     const float p = id[j] >= 0 ? expf(lp) : 0.f;
-    // a probability that underflows contributes its limit, zero
-    if (id[j] >= 0 && id[j] < V && !(p == 0.f)) loss += p * (lp + (base - to_float(x[id[j]])) * inv_tau + log_sum);
+    if (id[j] >= 0 && id[j] < V) {
+      mine[i] = __builtin_fmaf(to_float(x[id[j]]), scale, shift);
+      // a probability that underflows contributes its limit, zero
+      if (!(p == 0.f)) loss[0] += p * (lp - mine[i] * 0.693147180559945309417f + log_sum);
+    }
     prob[j] = p;
   }
-  loss = team_reduce<kTeam, false>(loss, part) * a.tau * a.tau;
-  if (bad) loss = __builtin_nanf("");
-  if (!present) loss = 0.f;
-  if (lane == 0) a.row_losses[row] = loss;
+  team_reduce<kTeam, false, 1>(loss, part + 8 * 16);
+  // rows that are not scored are marked for the mean by the sign of their zero
+  if (lane == 0) a.row_losses[row] = !present ? -0.f : (bad ? __builtin_nanf("") : loss[0] * a.tau * a.tau + 0.f);
 
   if (kGrad) {
-    const float g = (a.row_grad ? a.row_grad[row] : 1.f) * a.tau;
-    const float up = bad ? __builtin_nanf("") : g;
-    const float inv_sum = 1.f / sum;
     T* d = static_cast<T*>(a.dlogits) + row * a.dlogits_stride;
-    // the teacher's entries first (from logits that an update in place is about to overwrite),
-    // held by the threads that own them, written once the row's other entries are
-    float fix[(1024 + kTeam - 1) / kTeam];
+    if (!present) {
+      for (int b = lane; b < at.pieces; b += kTeam) at.store(d, b, make_uint4(0, 0, 0, 0));
+      return;  // for the whole team
+    }
+    const float up = bad ? __builtin_nanf("") : (a.row_grad ? a.row_grad[row] : 1.f) * a.tau;
+    const float up_q = up / sums[0];
+    // every read of the row at the teacher's ids is done (they lie before the last reduction, and in
+    // `mine`), so an update in place may begin; the teacher's entries are written over it afterwards
+    if (kPieces > 0) {
 #pragma unroll
-    for (int i = 0; i < (1024 + kTeam - 1) / kTeam; ++i) {
-      const int j = lane + i * kTeam;
-      fix[i] = 0.f;
-      if (j < k && id[j] >= 0 && id[j] < V) {
-        float p = 0.f;
-        for (int o = 0; o < k; ++o) p += id[o] == id[j] ? prob[o] : 0.f;
-        fix[i] = up * (__builtin_amdgcn_exp2f((to_float(x[id[j]]) - base) * scale) * inv_sum - p);
+      for (int i = 0; i < kPieces; ++i) {
+        const int b = lane + i * kTeam;
+        if (b < at.pieces) at.store(d, b, piece_grad<T>(held[i], shift, scale, up_q));
+        __builtin_amdgcn_sched_barrier(0);
       }
+    } else {
+      for (int b = lane; b < at.pieces; b += kTeam) at.store(d, b, piece_grad<T>(at.load(x, b), shift, scale, up_q));
     }
     team_sync<kTeam>();
-    for (int v = lane; v < V; v += kTeam)
-      d[v] = from_float<T>(present ? up * (__builtin_amdgcn_exp2f((to_float(x[v]) - base) * scale) * inv_sum) : 0.f);
-    team_sync<kTeam>();
-    if (present) {
 #pragma unroll
-      for (int i = 0; i < (1024 + kTeam - 1) / kTeam; ++i) {
-        const int j = lane + i * kTeam;
-        if (j < k && id[j] >= 0 && id[j] < V) d[id[j]] = from_float<T>(fix[i]);
+    for (int i = 0; i < kOwn; ++i) {
+      const int j = lane + i * kTeam;
+      if (j >= k || id[j] < 0 || id[j] >= V) continue;
+      const int v = id[j];
+      float p = 0.f;  // an id that comes twice has the sum, whoever writes it
+      for (int o = 0; o < k4; o += 4) {
+        const int4 io = *reinterpret_cast<const int4*>(id + o);
+        const float4 po = *reinterpret_cast<const float4*>(prob + o);
+        p += (io.x == v ? po.x : 0.f) + (io.y == v ? po.y : 0.f) + (io.z == v ? po.z : 0.f) + (io.w == v ? po.w : 0.f);
       }
+      d[v] = from_float<T>(up_q * __builtin_amdgcn_exp2f(mine[i]) - up * p);
     }
   }
 }
 
 // losses[m]: mean over the scored rows of model m, in a fixed order, in double. One workgroup a model.
-static __global__ __launch_bounds__(256) void k_distill_mean(const float* __restrict__ row_losses, const int32_t* __restrict__ ids,
-                                                      const float* __restrict__ teacher, int top_k, int64_t rows_per_model,
-                                                      float* __restrict__ losses) {
+static __global__ __launch_bounds__(256) void k_distill_mean(const float* __restrict__ row_losses, int64_t rows_per_model,
+                                                             float* __restrict__ losses) {
   __shared__ double part[256];
-  __shared__ double cnt[256];
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_model;
-  double s = 0.0, n = 0.0;
+  __shared__ int cnt[256];
+  const float* r = row_losses + static_cast<int64_t>(blockIdx.x) * rows_per_model;
+  double s = 0.0;
+  int n = 0;
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < rows_per_model; i += 256) {
-    const int64_t r = r0 + i;
-    s += static_cast<double>(row_losses[r]);
-    int have = 0;
-    for (int j = 0; j < top_k && !have; ++j)
-      have = ids[r * top_k + j] >= 0 && !(teacher[r * top_k + j] == -__builtin_inff());
-    n += have;
+    const float v = r[i];
+    s += static_cast<double>(v);
+    n += __float_as_uint(v) != 0x80000000u;
   }
   part[threadIdx.x] = s;
   cnt[threadIdx.x] = n;
@@ -168,7 +277,7 @@ static __global__ __launch_bounds__(256) void k_distill_mean(const float* __rest
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) losses[blockIdx.x] = static_cast<float>(part[0] / cnt[0]);
+  if (threadIdx.x == 0) losses[blockIdx.x] = static_cast<float>(part[0] / static_cast<double>(cnt[0]));
 }
 
 }  // namespace cdrge
