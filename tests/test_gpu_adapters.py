@@ -68,6 +68,16 @@ def test_project(case, order):
     assert (y[:, c.O:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype, rows, K, O, R, pad", [("bf16", 3333, 192, 3880, 8, 0), ("bf16", 3333, 70, 3880, 40, 3), ("f32", 3100, 64, 4070, 24, 0)])
+def test_many_rows(dtype, rows, K, O, R, pad):
+    """The largest tiles, with rows and outputs that end inside one, aligned and not."""
+    c = Case(dtype, rows, K, O, 5, R, order="runs", seed=rows, xpad=pad, ranks=[R, R - 1, 0, 3, R])
+    x, who, y, scale = c.inputs()
+    c.operator().project(x, who, y[:, :c.O], row_scale=scale)
+    c.check(y[:, :c.O])
+    assert (y[:, c.O:] == 7).all()
+
+
 @pytest.mark.parametrize("dtype, rows", [("bf16", 4), ("bf16", 200), ("f32", 70)])
 def test_ranks_and_no_scale(dtype, rows):
     c = Case(dtype, rows, 128, 96, 6, 24, bias=False, ranks=[0, 24, 1, 17, -4, 99], scale=False, xpad=0, ypad=0, wpad=8)

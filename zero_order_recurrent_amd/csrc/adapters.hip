@@ -1,6 +1,9 @@
 // Host side of cdrge_adapter_project (include/cdrge.h).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "cdrge.h"
 #include "host_common.h"
 #include "kernels_adapters.h"
@@ -21,18 +24,111 @@ cdrge_status check(const cdrge_adapter_config* c, int64_t n_rows) {
   return CDRGE_OK;
 }
 
-size_t workspace(const cdrge_adapter_config* c, int64_t n_rows) {
-  return align_up(sizeof(float) * static_cast<size_t>(n_rows) * c->max_rank);
+// How a call is cut up. It goes by the sizes alone, so that the workspace is known without pointers.
+struct Cut {
+  bool rows;             // k_adapter_rows (up to 64 rows)
+  bool big;              // 256 x 256 tiles, otherwise 128 x 128
+  int tiles_r, tiles_o, slices, slice_cols;
+  int v_slices, v_cols, v_slots;
+  int o_pad;
+  size_t off_partial, total;
+};
+
+constexpr int kWorkgroups = 512;  // two for each of 256 compute units
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Cuts n columns into at most `want` slices of a multiple of `unit` columns; returns a slice's columns.
+int slice_columns(int n, int want, int unit) { return ceil_div(ceil_div(n, unit), std::max(1, want)) * unit; }
+
+Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
+  Cut p{};
+  const int K = c->in_features, O = c->out_features;
+  const int step = c->dtype == CDRGE_F32 ? 32 : 64;  // columns of 128 bytes
+  p.o_pad = (O + 63) / 64 * 64;
+  p.rows = n_rows <= 64;
+  int want;
+  if (p.rows) {
+    p.tiles_r = 1;
+    p.tiles_o = p.o_pad / 64;
+    want = ceil_div(kWorkgroups, p.tiles_o);
+    // four waves share a slice: at least two steps of 64 bytes each for every wave
+    want = std::min(want, ceil_div(K, 4 * step));
+  } else {
+    p.big = int64_t(ceil_div(n_rows, 256)) * ceil_div(O, 256) >= 192;
+    const int side = p.big ? 256 : 128;
+    p.tiles_r = ceil_div(n_rows, side);
+    p.tiles_o = ceil_div(O, side);
+    // slices where the tiles alone leave compute units idle, of at least 8 steps
+    const int64_t tiles = int64_t(p.tiles_r) * p.tiles_o;
+    want = p.big || tiles >= 256 ? 1 : std::min(ceil_div(kWorkgroups, tiles), ceil_div(K, 8 * step));
+  }
+  p.slice_cols = slice_columns(K, want, p.rows ? 4 * step / 2 : step);
+  p.slices = ceil_div(K, p.slice_cols);
+  const int v_tiles = ceil_div(n_rows, 64);
+  p.v_slots = std::max(1, std::min({c->n_adapters, 16, ceil_div(kWorkgroups, 4 * int64_t(v_tiles))}));
+  p.v_cols = slice_columns(K, std::min(8, ceil_div(kWorkgroups, int64_t(v_tiles) * p.v_slots)), 4 * step);
+  p.v_slices = ceil_div(K, p.v_cols);
+  p.off_partial = c->n_adapters > 0 ? align_up(sizeof(float) * p.v_slices * static_cast<size_t>(n_rows) * c->max_rank) : 0;
+  p.total = p.off_partial;
+  if (p.rows || p.slices > 1) p.total = align_up(p.total + sizeof(float) * p.slices * static_cast<size_t>(n_rows) * p.o_pad);
+  return p;
+}
+
+constexpr int64_t kMostBlocks = (int64_t(1) << 31) - 1;
+
+template <class T, int kTiles>
+void launch_rows(const AdapterArgs& a, int blocks, hipStream_t s) {
+  hipLaunchKernelGGL((k_adapter_rows<T, kTiles>), dim3(blocks), dim3(256), 0, s, a);
+}
+
+template <class T, int kSide, int kWavesR, int kWavesO, bool kDirect>
+cdrge_status launch_tiles(const AdapterArgs& a, hipStream_t s) {
+  constexpr size_t kLds = 2 * 2 * kSide * 128;
+  const void* f = reinterpret_cast<const void*>(k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>);
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use this much LDS
+  int dev = 0;
+  CDRGE_HIP(hipGetDevice(&dev));
+  if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    CDRGE_HIP(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
+    ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
+  }
+  hipLaunchKernelGGL((k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>),
+                     dim3(static_cast<uint32_t>(int64_t(a.tiles_r) * a.tiles_o * a.slices)), dim3(64 * kWavesR * kWavesO), kLds, s, a);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
 }
 
 template <class T>
-cdrge_status enqueue(const AdapterArgs& a, hipStream_t s) {
-  const uint32_t tiles = static_cast<uint32_t>((a.n_rows + 15) / 16);
-  if (a.row_adapter && a.A > 0) {
-    hipLaunchKernelGGL(k_adapter_down<T>, dim3(tiles), dim3(64), 0, s, a);
+cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
+  const bool low = a.row_adapter && a.A > 0;
+  if (p.rows) {
+    const int blocks = a.tiles_o * a.slices + (low ? a.v_slices * a.v_slots : 0);
+    switch ((a.n_rows + 15) / 16) {
+      case 1: launch_rows<T, 1>(a, blocks, s); break;
+      case 2: launch_rows<T, 2>(a, blocks, s); break;
+      case 3: launch_rows<T, 3>(a, blocks, s); break;
+      default: launch_rows<T, 4>(a, blocks, s); break;
+    }
     CDRGE_HIP(hipGetLastError());
+  } else {
+    if (low) {
+      const int64_t blocks = int64_t(ceil_div(a.n_rows, 64)) * a.v_slices * a.v_slots;
+      hipLaunchKernelGGL(k_adapter_down<T>, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, s, a);
+      CDRGE_HIP(hipGetLastError());
+    }
+    constexpr int kPer = 16 / sizeof(T), kStep = 128 / sizeof(T);
+    const bool direct = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 &&
+                        a.x_stride % kPer == 0 && a.weight_stride % kPer == 0 && a.K % kStep == 0;
+    cdrge_status st;
+    if (p.big)
+      st = direct ? launch_tiles<T, 256, 2, 4, true>(a, s) : launch_tiles<T, 256, 2, 4, false>(a, s);
+    else
+      st = direct ? launch_tiles<T, 128, 2, 2, true>(a, s) : launch_tiles<T, 128, 2, 2, false>(a, s);
+    if (st != CDRGE_OK) return st;
+    if (a.slices == 1) return CDRGE_OK;
   }
-  hipLaunchKernelGGL(k_adapter_project<T>, dim3(tiles, (a.O + 63) / 64), dim3(64), 0, s, a);
+  hipLaunchKernelGGL(k_adapter_finish<T>, dim3(a.o_pad / 64, static_cast<uint32_t>((a.n_rows + 15) / 16)), dim3(64), 0, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -45,7 +141,7 @@ cdrge_status cdrge_adapter_workspace_bytes(const cdrge_adapter_config* cfg, int6
   if (!bytes_out) return CDRGE_ERR_INVALID_ARG;
   const cdrge_status st = check(cfg, n_rows);
   if (st != CDRGE_OK) return st;
-  *bytes_out = workspace(cfg, n_rows);
+  *bytes_out = n_rows > 0 ? make_cut(cfg, n_rows).total : 0;
   return CDRGE_OK;
 }
 
@@ -61,14 +157,19 @@ cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_
   if (row_adapter && cfg->n_adapters > 0 && (!weights->down || !weights->up)) return CDRGE_ERR_INVALID_ARG;
   if (n_rows == 0) return CDRGE_OK;
   if (!x || !y) return CDRGE_ERR_INVALID_ARG;
-  const size_t need = workspace(cfg, n_rows);
-  if (row_adapter && (!ws || workspace_bytes < need || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
-    return workspace_error("cdrge_adapter_project", need, ws ? workspace_bytes : 0);
+  const Cut p = make_cut(cfg, n_rows);
+  if (int64_t(p.tiles_r) * p.tiles_o * p.slices > kMostBlocks || int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks)
+    return CDRGE_ERR_UNSUPPORTED;
+  if (p.total > 0 && (!ws || workspace_bytes < p.total || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
+    return workspace_error("cdrge_adapter_project", p.total, ws ? workspace_bytes : 0);
+  float* const vp = static_cast<float*>(ws);
+  float* const partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_partial);
   const AdapterArgs a{x, x_stride, weights->weight, weights->weight_stride, weights->bias, weights->down, weights->up,
-                      weights->ranks, row_adapter, row_scale, y, y_stride, static_cast<float*>(ws), n_rows,
-                      K, O, cfg->n_adapters, cfg->max_rank};
+                      weights->ranks, row_adapter, row_scale, y, y_stride, vp, partial, n_rows,
+                      K, O, cfg->n_adapters, cfg->max_rank, p.v_slices, p.v_cols, p.v_slots, p.slices, p.slice_cols,
+                      p.o_pad, p.tiles_r, p.tiles_o};
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return cfg->dtype == CDRGE_F32 ? enqueue<float>(a, s) : enqueue<uint16_t>(a, s);
+  return cfg->dtype == CDRGE_F32 ? enqueue<float>(a, p, s) : enqueue<uint16_t>(a, p, s);
 }
 
 }  // extern "C"
