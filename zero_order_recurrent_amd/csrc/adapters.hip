@@ -30,7 +30,8 @@ struct Cut {
   bool big;              // 256 x 256 tiles, otherwise 128 x 128
   int tiles_r, tiles_o, slices, slice_cols;
   int v_slices, v_cols, v_slots;
-  int o_pad;
+  bool packed;           // v as operand rows
+  int vq_row, o_pad;
   size_t off_partial, total;
 };
 
@@ -51,7 +52,8 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
   if (p.rows) {
     p.tiles_r = 1;
     p.tiles_o = p.o_pad / 64;
-    want = ceil_div(kWorkgroups, p.tiles_o);
+    // the down product's workgroups (up to kMostVSlices * 16) take part in the same round
+    want = std::max(1, (kWorkgroups - 64) / p.tiles_o);
     // four waves share a slice: at least two steps of 64 bytes each for every wave
     want = std::min(want, ceil_div(K, 4 * step));
   } else {
@@ -66,10 +68,14 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
   p.slice_cols = slice_columns(K, want, p.rows ? 4 * step / 2 : step);
   p.slices = ceil_div(K, p.slice_cols);
   const int v_tiles = ceil_div(n_rows, 64);
-  p.v_slots = std::max(1, std::min({c->n_adapters, 16, ceil_div(kWorkgroups, 4 * int64_t(v_tiles))}));
-  p.v_cols = slice_columns(K, std::min(8, ceil_div(kWorkgroups, int64_t(v_tiles) * p.v_slots)), 4 * step);
+  // beside up to 64 rows: 16 workgroups for the adapters, four for K; otherwise as many as fill the chip
+  p.v_slots = std::max(1, std::min({c->n_adapters, 16, ceil_div(256, v_tiles)}));
+  p.v_cols = slice_columns(K, p.rows ? kMostVSlices : 1, 4 * step);
   p.v_slices = ceil_div(K, p.v_cols);
-  p.off_partial = c->n_adapters > 0 ? align_up(sizeof(float) * p.v_slices * static_cast<size_t>(n_rows) * c->max_rank) : 0;
+  p.packed = !p.rows && p.slices == 1;
+  p.vq_row = (c->max_rank + 31) / 32 * 32 * (c->dtype == CDRGE_F32 ? 1 : 2);
+  const size_t v_row = p.packed ? p.vq_row * (c->dtype == CDRGE_F32 ? 4 : 2) : sizeof(float) * p.v_slices * c->max_rank;
+  p.off_partial = c->n_adapters > 0 ? align_up(v_row * static_cast<size_t>(n_rows)) : 0;
   p.total = p.off_partial;
   if (p.rows || p.slices > 1) p.total = align_up(p.total + sizeof(float) * p.slices * static_cast<size_t>(n_rows) * p.o_pad);
   return p;
@@ -113,22 +119,30 @@ cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
     CDRGE_HIP(hipGetLastError());
   } else {
     if (low) {
-      const int64_t blocks = int64_t(ceil_div(a.n_rows, 64)) * a.v_slices * a.v_slots;
-      hipLaunchKernelGGL(k_adapter_down<T>, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, s, a);
+      const int64_t blocks = int64_t(ceil_div(a.n_rows, 64)) * a.v_slots;
+      hipLaunchKernelGGL(k_adapter_down<T>, dim3(static_cast<uint32_t>(blocks)), dim3(1024), 0, s, a);
       CDRGE_HIP(hipGetLastError());
     }
     constexpr int kPer = 16 / sizeof(T), kStep = 128 / sizeof(T);
     const bool direct = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 &&
-                        a.x_stride % kPer == 0 && a.weight_stride % kPer == 0 && a.K % kStep == 0;
+                        a.x_stride % kPer == 0 && a.weight_stride % kPer == 0 && a.K % kStep == 0 &&
+                        std::max(a.x_stride, a.weight_stride) <= int64_t(1 << 23) / int64_t(sizeof(T));
     cdrge_status st;
-    if (p.big)
-      st = direct ? launch_tiles<T, 256, 2, 4, true>(a, s) : launch_tiles<T, 256, 2, 4, false>(a, s);
-    else
-      st = direct ? launch_tiles<T, 128, 2, 2, true>(a, s) : launch_tiles<T, 128, 2, 2, false>(a, s);
+    if (p.big && direct) {
+      st = launch_tiles<T, 256, 2, 4, true>(a, s);
+    } else if (direct) {
+      st = launch_tiles<T, 128, 2, 2, true>(a, s);
+    } else {
+      // chunks that pass through registers leave no room for the products of the large tiles
+      AdapterArgs b = a;
+      b.tiles_r = ceil_div(a.n_rows, 128);
+      b.tiles_o = ceil_div(a.O, 128);
+      st = launch_tiles<T, 128, 2, 2, false>(b, s);
+    }
     if (st != CDRGE_OK) return st;
     if (a.slices == 1) return CDRGE_OK;
   }
-  hipLaunchKernelGGL(k_adapter_finish<T>, dim3(a.o_pad / 64, static_cast<uint32_t>((a.n_rows + 15) / 16)), dim3(64), 0, s, a);
+  hipLaunchKernelGGL(k_adapter_finish<T>, dim3(a.o_pad / 64, static_cast<uint32_t>((a.n_rows + 15) / 16)), dim3(256), 0, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -158,14 +172,15 @@ cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_
   if (n_rows == 0) return CDRGE_OK;
   if (!x || !y) return CDRGE_ERR_INVALID_ARG;
   const Cut p = make_cut(cfg, n_rows);
-  if (int64_t(p.tiles_r) * p.tiles_o * p.slices > kMostBlocks || int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks)
+  if (int64_t(ceil_div(n_rows, 128)) * ceil_div(O, 128) * p.slices > kMostBlocks || (p.rows && int64_t(p.tiles_o) * p.slices > kMostBlocks / 2) || int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks)
     return CDRGE_ERR_UNSUPPORTED;
   if (p.total > 0 && (!ws || workspace_bytes < p.total || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return workspace_error("cdrge_adapter_project", p.total, ws ? workspace_bytes : 0);
+  const bool low = row_adapter && cfg->n_adapters > 0;  // vq is set only where there are rows' adapters to read
   float* const vp = static_cast<float*>(ws);
   float* const partial = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_partial);
   const AdapterArgs a{x, x_stride, weights->weight, weights->weight_stride, weights->bias, weights->down, weights->up,
-                      weights->ranks, row_adapter, row_scale, y, y_stride, vp, partial, n_rows,
+                      weights->ranks, row_adapter, row_scale, y, y_stride, vp, p.packed && low ? ws : nullptr, p.vq_row, partial, n_rows,
                       K, O, cfg->n_adapters, cfg->max_rank, p.v_slices, p.v_cols, p.v_slots, p.slices, p.slice_cols,
                       p.o_pad, p.tiles_r, p.tiles_o};
   const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -5,12 +5,14 @@
 //   down      vp[ks][r][j] = sum over the ks-th slice of K of D_a[j][k] x_r[k], by tiles of 64 rows.
 //             Rows need no order: a tile runs once for each adapter that it meets and keeps, of each
 //             run, the rows that name the adapter.
-//   shared    W x, either in tiles that end with the epilogue, or in slices of K whose float32 sums
-//             (P[s][r][o]) the epilogue's own launch adds up: with few rows the tiles alone would not
+//   shared    W x, either in tiles, or in slices of K whose float32 sums
+//             (P[s][r][o]) a later launch adds up: with few rows the tiles alone would not
 //             fill the chip.
-//   epilogue  + bias + U_a v_r, v_r = s_r sum_ks vp, from the same matrix-core tiles, again once for
-//             each adapter among 16 rows and kept by selection: what one adapter holds (NaN
-//             included) cannot reach another's rows.
+//   up        + bias + U_a v_r, v_r = s_r sum_ks vp. A tile of the shared product takes it as further
+//             steps of its own reduction, one adapter after the other, with zeros for the rows that name
+//             another; after a product in slices it is a launch that adds the slices as well and keeps
+//             each adapter's rows by selection. What one adapter holds (NaN included) cannot reach
+//             another's rows: see there.
 //
 // Both element types run on the matrix cores with 16 bytes of a row in each lane: for bf16 that is
 // one 16x16x32 product over 32 columns, for float32 four 16x16x4 products over 16 columns, in which
@@ -22,6 +24,8 @@
 #include "operators_common.h"
 
 namespace cdrge {
+
+constexpr int kMostVSlices = 4;  // slices of K of the down product
 
 struct AdapterArgs {
   const void* x;
@@ -36,13 +40,15 @@ struct AdapterArgs {
   const float* row_scale;
   void* y;
   int64_t y_stride;
-  float* vp;        // [v_slices][n_rows][R]
+  float* vp;        // v in slices of K, [v_slices][n_rows][R], without the rows' scales
+  void* vq;         // or v as operand rows (see k_adapter_down), [n_rows][vq_row] of T
+  int vq_row;
   float* partial;   // [slices][n_rows][o_pad]
   int64_t n_rows;
   int K, O, A, R;
-  int v_slices, v_cols;    // slices of K of the down product, columns of each (a multiple of 128)
+  int v_slices, v_cols;    // slices of K of the down product, columns of each
   int v_slots;             // workgroups that share a row tile's adapters
-  int slices, slice_cols;  // slices of K of the shared product (1: the tiles end with the epilogue)
+  int slices, slice_cols;  // slices of K of the shared product (1: the tiles write y)
   int o_pad;               // O rounded up to 64
   int tiles_r, tiles_o;    // tiles of the shared product
 };
@@ -90,12 +96,17 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& a, int ad) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// down: one workgroup of four waves takes 64 rows (a lane knows the adapter of the row of its
-// number), one slice of K, which its waves share step by step, and every v_slots-th of the adapters
-// that the rows name.
+// down: one workgroup takes 64 rows (a lane knows the adapter of the row of its number), one slice of
+// K, which its waves share step by step, and every v_slots-th of the adapters that the rows name.
+// Beside up to 64 rows' shared product it runs in slices of K, four waves each, that leave float32
+// sums (vp). As a launch of its own it takes all of K with 16 waves, and for tiles that end the call it
+// leaves operand rows (vq): v_r times the row's scale, zero from the rank up to a multiple of 32 columns,
+// in bf16 as its high halves followed by its low ones, which keeps 16 bits of it.
 // ---------------------------------------------------------------------------------------------
-template <class T>
-__device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile, int slice, int slot, f32x4 (&lds)[4][4][64]) {
+__device__ __forceinline__ int vq_columns(int rank) { return (rank + 31) & ~31; }
+
+template <class T, int kWaves>
+__device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile, int slice, int slot, f32x4 (&lds)[kWaves][4][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int64_t r0 = tile * 64;
   const int ad = r0 + lane < a.n_rows ? a.row_adapter[r0 + lane] : -1;
@@ -104,52 +115,84 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
   for (int m = 0; m < 4; ++m) x[m] = static_cast<const T*>(a.x) + min(r0 + 16 * m + l16, a.n_rows - 1) * a.x_stride;
   const int k0 = slice * a.v_cols, k1 = min(a.K, k0 + a.v_cols);
   uint64_t todo = __ballot(ad >= 0 && ad < a.A);
+  const float scale = (a.vq && a.row_scale && r0 + lane < a.n_rows) ? a.row_scale[r0 + lane] : 1.f;
   for (int n = 0; todo; ++n) {
     const int cur = __shfl(ad, __builtin_ctzll(todo));
     const uint64_t mine = __ballot(ad == cur);
     todo &= ~mine;
     if (n % a.v_slots != slot) continue;
     const int rank = rank_of(a, cur);
-    for (int j0 = 0; j0 < rank; j0 += 16) {
+    const bool all = (mine & 0xffffu) && (mine & 0xffff0000u) && (mine >> 32 & 0xffffu) && (mine >> 48);
+    for (int j0 = 0; j0 < (a.vq ? vq_columns(rank) : rank); j0 += 16) {
       const T* d = static_cast<const T*>(a.down) + (static_cast<int64_t>(cur) * a.R + min(j0 + l16, rank - 1)) * a.K;
       f32x4 acc[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int k = k0 + wave * Frag<T>::kCols; k < k1; k += 4 * Frag<T>::kCols) {
-        const Frag<T> df = load_frag<T>(d, k + q * Frag<T>::kPer, k1);
+      constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer, kDeep = 4;  // steps whose loads are in flight together
+      int k = k0 + wave * kCols;
+      if (all) {
+        for (; k + (kWaves * (kDeep - 1) + 1) * kCols <= k1; k += kWaves * kDeep * kCols) {
+          Frag<T> df[kDeep], xf[kDeep][4];
+#pragma unroll
+          for (int s = 0; s < kDeep; ++s) {
+            const int at = k + kWaves * s * kCols + q * kPer;
+            __builtin_memcpy(&df[s].v, d + at, 16);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) __builtin_memcpy(&xf[s][m].v, x[m] + at, 16);
+          }
+#pragma unroll
+          for (int s = 0; s < kDeep; ++s)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) acc[m] = mma(df[s], xf[s][m], acc[m]);
+        }
+      }
+      for (; k < k1; k += kWaves * kCols) {
+        const Frag<T> df = load_frag<T>(d, k + q * kPer, k1);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          if ((mine >> (16 * m)) & 0xffffu) acc[m] = mma(df, load_frag<T>(x[m], k + q * Frag<T>::kPer, k1), acc[m]);
+          if ((mine >> (16 * m)) & 0xffffu) acc[m] = mma(df, load_frag<T>(x[m], k + q * kPer, k1), acc[m]);
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) lds[wave][m][lane] = acc[m];
       __syncthreads();
-      // wave m sums row tile m: rank indexes j0 + 4 q + e of row 16 m + l16
-      f32x4 sum = lds[0][wave][lane];
+      if (wave < 4) {
+        // wave m sums row tile m: rank indexes j0 + 4 q + e of row 16 m + l16
+        f32x4 sum = lds[0][wave][lane];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) sum += lds[w][wave][lane];
-      __syncthreads();
-      if ((mine >> (16 * wave + l16)) & 1) {
-        float* v = a.vp + (static_cast<int64_t>(slice) * a.n_rows + r0 + 16 * wave + l16) * a.R + j0 + 4 * q;
+        for (int w = 1; w < kWaves; ++w) sum += lds[w][wave][lane];
+        const int row = 16 * wave + l16, j = j0 + 4 * q;
+        if (a.vq) {
+          const float s = __shfl(scale, row);
+          T hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j0 + 4 * q + e < rank) v[e] = sum[e];
+          for (int e = 0; e < 4; ++e) {
+            const float f = j + e < rank ? sum[e] * s : 0.f;
+            hi[e] = from_float<T>(f);
+            // an infinite v has no low half (inf - inf would turn it into NaN)
+            lo[e] = from_float<T>(fabsf(f) <= 3.38953139e38f ? f - to_float(hi[e]) : 0.f);
+          }
+          if ((mine >> row) & 1) {
+            T* v = static_cast<T*>(a.vq) + (r0 + row) * a.vq_row + j;
+            __builtin_memcpy(v, hi, sizeof(hi));
+            if (sizeof(T) == 2) __builtin_memcpy(v + a.vq_row / 2, lo, sizeof(lo));
+          }
+        } else if ((mine >> row) & 1) {
+          float* v = a.vp + (static_cast<int64_t>(slice) * a.n_rows + r0 + row) * a.R + j;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e < rank) v[e] = sum[e];
+        }
       }
+      __syncthreads();
     }
   }
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void k_adapter_down(AdapterArgs a) {
-  __shared__ f32x4 lds[4][4][64];
-  const int slot = blockIdx.x % a.v_slots, slice = (blockIdx.x / a.v_slots) % a.v_slices;
-  adapter_down<T>(a, blockIdx.x / (a.v_slots * a.v_slices), slice, slot, lds);
+__global__ __launch_bounds__(1024) void k_adapter_down(AdapterArgs a) {
+  __shared__ f32x4 lds[16][4][64];
+  adapter_down<T, 16>(a, blockIdx.x / a.v_slots, 0, blockIdx.x % a.v_slots, lds);
 }
-
-// ---------------------------------------------------------------------------------------------
-// epilogue: of the sums of kAll row tiles, the kMT from kFirst on; sums[kFirst + m][t][e] is output
-// o0 + 16 q + 4 t + e of row r0 + 16 m + l16.
-// ---------------------------------------------------------------------------------------------
 
 // v_r from column j on: the sum over the slices of K, times the row's scale, zero from column n on.
 template <int kPer>
@@ -159,11 +202,13 @@ __device__ __forceinline__ void v_values(const AdapterArgs& a, int64_t r, int j,
   if (j >= n) return;
   const float* v = a.vp + r * a.R + j;
   if (j + kPer <= n) {
-    for (int ks = 0; ks < a.v_slices; ++ks, v += a.n_rows * a.R) {
-      float e[kPer];
-      __builtin_memcpy(e, v, sizeof(e));
+    // all slices' loads at once; a slice past the last reads the last again and is not added
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) f[i] += e[i];
+    for (int ks = 0; ks < kMostVSlices; ++ks) {
+      float e[kPer];
+      __builtin_memcpy(e, v + min(ks, a.v_slices - 1) * a.n_rows * a.R, sizeof(e));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[i] += ks < a.v_slices ? e[i] : 0.f;
     }
   } else {
     for (int ks = 0; ks < a.v_slices; ++ks, v += a.n_rows * a.R)
@@ -200,118 +245,121 @@ __device__ __forceinline__ void up_frags(const AdapterArgs& a, int cur, int rank
   }
 }
 
-template <class T, int kFirst, int kMT, int kAll>
-__device__ __forceinline__ void adapter_epilogue(const AdapterArgs& a, int64_t r0, int o0, f32x4 (&sums)[kAll][4]) {
-  f32x4 acc[kMT][4];
-#pragma unroll
-  for (int m = 0; m < kMT; ++m)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) acc[m][t] = sums[kFirst + m][t];
+// ---------------------------------------------------------------------------------------------
+// After a shared product in slices: 16 rows x 64 outputs by four waves, which share the slices and the
+// adapters among the rows and add up through LDS. The time is the latency of a few loads, so each wave
+// has those of up to four adapters in flight together. sum[t][e] is output o0 + 16 q + 4 t + e of row l16.
+// ---------------------------------------------------------------------------------------------
+template <class T>
+__global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   constexpr int kPer = Frag<T>::kPer, kCols = Frag<T>::kCols;
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-  int ad[kMT];
+  __shared__ f32x4 lds[4][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+  const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + l16;
+  const bool rok = r < a.n_rows;
+  const int o0 = blockIdx.x * 64;
+  const int ad = (a.row_adapter && rok) ? a.row_adapter[r] : -1;
+  f32x4 sum[4];
 #pragma unroll
-  for (int m = 0; m < kMT; ++m) {
-    const int64_t r = r0 + 16 * m + l16;
-    ad[m] = (a.row_adapter && r < a.n_rows) ? a.row_adapter[r] : -1;
+  for (int t = 0; t < 4; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (rok) {
+    const float* p = a.partial + r * a.o_pad + o0 + 16 * q;
+#pragma unroll 2
+    for (int s = wave; s < a.slices; s += 4)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) sum[t] += *reinterpret_cast<const f32x4*>(p + s * a.n_rows * a.o_pad + 4 * t);
   }
-  if (a.row_adapter && a.A > 0) {
-    const bool narrow = a.R <= kCols;  // one product a tile: all of v is fetched at once, and U once for equal neighbours
-    Frag<T> vh[kMT], vl[kMT], u[4];
-    int rank[kMT], u_of = -1;
-    float scale[kMT];
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      const bool has = ad[m] >= 0 && ad[m] < a.A;
-      rank[m] = has ? rank_of(a, ad[m]) : 0;
-      scale[m] = has && a.row_scale ? a.row_scale[r0 + 16 * m + l16] : 1.f;
-    }
+  const bool has = ad >= 0 && ad < a.A;
+  uint32_t todo = static_cast<uint32_t>(__ballot(has)) & 0xffffu;
+  if (todo) {
+    const int rank = has ? rank_of(a, ad) : 0;
+    const float scale = has && a.row_scale ? a.row_scale[r] : 1.f;
+    const bool narrow = a.R <= kCols;  // one product a tile
+    Frag<T> vh, vl;
     if (narrow) {
-#pragma unroll
-      for (int m = 0; m < kMT; ++m) {
-        float f[kPer];
-        v_values<kPer>(a, r0 + 16 * m + l16, q * kPer, rank[m], scale[m], f);
-        v_frag(f, vh[m], vl[m]);
-      }
+      float f[kPer];
+      v_values<kPer>(a, r, q * kPer, rank, scale, f);
+      v_frag(f, vh, vl);
     }
+    while (todo) {
+      // the next four of this wave's adapters (every fourth); a repeated one is loaded but not added
+      int cur[4], got = 0;
 #pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      uint32_t todo = static_cast<uint32_t>(__ballot(rank[m] > 0)) & 0xffffu;
-      while (todo) {
-        const int first = __builtin_ctz(todo);
-        const int cur = __builtin_amdgcn_readlane(ad[m], first), n = __builtin_amdgcn_readlane(rank[m], first);
-        const bool mine = ad[m] == cur;
-        todo &= ~static_cast<uint32_t>(__ballot(mine));
-        f32x4 low[4];
+      for (int i = 0; i < 4; ++i) {
+        cur[i] = i ? cur[0] : -1;
+        for (int step = 0; step < 4 && todo; ++step) {
+          const int c = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
+          todo &= ~static_cast<uint32_t>(__ballot(ad == c));
+          if (step == wave) {
+            cur[i] = c;
+            got = i + 1;
+          }
+        }
+      }
+      if (!got) break;
+      if (narrow) {
+        Frag<T> u[4][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) low[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (narrow) {
-          if (cur != u_of) up_frags<T>(a, cur, n, o0, q * kPer, u);
-          u_of = cur;
+        for (int i = 0; i < 4; ++i) up_frags<T>(a, cur[i], rank_of(a, cur[i]), o0, q * kPer, u[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            low[t] = mma(u[t], vh[m], low[t]);
-            if (sizeof(T) == 2) low[t] = mma(u[t], vl[m], low[t]);
+            f32x4 low = mma(u[i][t], vh, f32x4{0.f, 0.f, 0.f, 0.f});
+            if (sizeof(T) == 2) low = mma(u[i][t], vl, low);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[t][e] = (i < got && ad == cur[i]) ? sum[t][e] + low[e] : sum[t][e];
           }
-        } else {
-          for (int j = 0; j < n; j += kCols) {
+        }
+      } else {
+        for (int i = 0; i < got; ++i) {
+          const int c = i == 0 ? cur[0] : (i == 1 ? cur[1] : (i == 2 ? cur[2] : cur[3]));
+          const int rc = rank_of(a, c);
+          f32x4 low[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) low[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < rc; j += kCols) {
             float f[kPer];
-            Frag<T> hi, lo;
-            v_values<kPer>(a, r0 + 16 * m + l16, j + q * kPer, mine ? n : 0, scale[m], f);
+            Frag<T> hi, lo, u[4];
+            v_values<kPer>(a, r, j + q * kPer, ad == c ? rc : 0, scale, f);
             v_frag(f, hi, lo);
-            up_frags<T>(a, cur, n, o0, j + q * kPer, u);
+            up_frags<T>(a, c, rc, o0, j + q * kPer, u);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               low[t] = mma(u[t], hi, low[t]);
               if (sizeof(T) == 2) low[t] = mma(u[t], lo, low[t]);
             }
           }
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[t][e] = ad == c ? sum[t][e] + low[t][e] : sum[t][e];
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][t][e] = mine ? acc[m][t][e] + low[t][e] : acc[m][t][e];
       }
     }
   }
-  const int o = o0 + 16 * q;
-  float bias[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) bias[i] = a.bias && o + i < a.O ? to_float(static_cast<const T*>(a.bias)[o + i]) : 0.f;
+  for (int t = 0; t < 4; ++t) lds[wave][t][lane] = sum[t];
+  __syncthreads();
+  f32x4 out = lds[0][wave][lane];
 #pragma unroll
-  for (int m = 0; m < kMT; ++m) {
-    const int64_t r = r0 + 16 * m + l16;
-    if (r >= a.n_rows) continue;
-    T* y = static_cast<T*>(a.y) + r * a.y_stride + o;
-    T out[16];
+  for (int w = 1; w < 4; ++w) out += lds[w][wave][lane];
+  const int o = o0 + 16 * q + 4 * wave;
+  if (!rok) return;
+  T v[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[i] = from_float<T>(ad[m] >= a.A ? __builtin_nanf("") : acc[m][i >> 2][i & 3] + bias[i]);
-    if (o + 16 <= a.O) {
-      __builtin_memcpy(y, out, sizeof(out));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (o + i < a.O) y[i] = out[i];
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float b = a.bias && o + e < a.O ? to_float(static_cast<const T*>(a.bias)[o + e]) : 0.f;
+    v[e] = from_float<T>(ad >= a.A ? __builtin_nanf("") : out[e] + b);
   }
-}
-
-// The epilogue as a launch of its own, after a shared product in slices: 16 rows x 64 outputs a wave.
-template <class T>
-__global__ __launch_bounds__(64) void k_adapter_finish(AdapterArgs a) {
-  const int lane = threadIdx.x, l16 = lane & 15, q = lane >> 4;
-  const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + l16;
-  const int o0 = blockIdx.x * 64;
-  f32x4 acc[1][4];
+  T* y = static_cast<T*>(a.y) + r * a.y_stride + o;
+  if (o + 4 <= a.O) {
+    __builtin_memcpy(y, v, sizeof(v));
+  } else {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) acc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (r < a.n_rows)
-    for (int s = 0; s < a.slices; ++s) {
-      const float* p = a.partial + (static_cast<int64_t>(s) * a.n_rows + r) * a.o_pad + o0 + 16 * q;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) acc[0][t] += *reinterpret_cast<const f32x4*>(p + 4 * t);
-    }
-  adapter_epilogue<T, 0, 1>(a, static_cast<int64_t>(blockIdx.y) * 16, o0, acc);
+    for (int e = 0; e < 4; ++e)
+      if (o + e < a.O) y[e] = v[e];
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -327,7 +375,7 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
   const int main_blocks = a.tiles_o * a.slices;
   if (static_cast<int>(blockIdx.x) >= main_blocks) {
     const int i = blockIdx.x - main_blocks;
-    adapter_down<T>(a, 0, i / a.v_slots, i % a.v_slots, lds);
+    adapter_down<T, 4>(a, 0, i / a.v_slots, i % a.v_slots, lds);
     return;
   }
   const int o0 = (blockIdx.x / a.slices) * 64, slice = blockIdx.x % a.slices;
@@ -392,24 +440,30 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// More rows: tiles of kRowsT rows x kOutsT outputs. K goes through LDS in steps of 128 bytes of each
-// row, two buffers deep, so that one barrier a step does: the loads of a step are issued before the
-// products of the one before. Rows lie in LDS as eight 16-byte chunks each, chunk c of row i at
-// place c ^ f(i), f such that the eight rows that a matrix-core read touches at a time take all
-// eight places: no bank conflicts. kDirect (rows of x and W 16-byte aligned, K a multiple of a step)
-// loads straight into LDS; otherwise the chunks pass through registers and are cut at K.
+// More rows: tiles of kRowsT rows x kOutsT outputs, a wave takes kMT * 16 rows x kOT * 64 outputs.
+// K goes through LDS in steps of 128 bytes of each row, two buffers deep, in two halves:
+//
+//   read half 1 of step k | products of half 0      wait for the loads of step k + 1, barrier
+//   issue the loads of step k + 2 into the buffer just read | read half 0 of step k + 1 | products of half 1
+//
+// so that a load has a whole step to arrive, and LDS is read beside the matrix cores' work, never
+// before it. Rows lie in LDS as eight 16-byte chunks each, chunk c of row i at place c ^ f(i), f such
+// that the eight rows that a matrix-core read touches at a time take all eight places: no bank
+// conflicts. kDirect (rows of x and W 16-byte aligned, K a multiple of a step) loads straight into
+// LDS; otherwise the chunks pass through registers and are cut at K.
 // ---------------------------------------------------------------------------------------------
+
 // s_waitcnt operand: no vector memory load in flight (vmcnt 0), the other counters not waited for
 constexpr int kWaitLoads = 0x0f70;
 
-// 16 bytes a lane from global memory into LDS, lane by lane behind `to` (the same for the whole wave). The
-// load has no register result. It is written as an instruction because the compiler, which cannot tell
-// the two buffers apart, would wait for every load of this kind before any read of LDS; the wait that
-// is needed stands before the step's barrier.
-__device__ __forceinline__ void load_to_lds(const char* from, uint4* to) {
+// 16 bytes a lane from base + offset into LDS, lane by lane behind `to` (base and to are the same for
+// the whole wave). The load has no register result. It is written as an instruction because the
+// compiler, which cannot tell the two buffers apart, would wait for every load of this kind before any
+// read of LDS; the wait that is needed stands before the step's barrier.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, uint4* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)to)));
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(at) : "memory");
 }
 
 __device__ __forceinline__ int place_x(int row) { return row & 7; }
@@ -420,10 +474,11 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   constexpr int kThreads = 64 * kWavesR * kWavesO;
   constexpr int kStep = 128 / sizeof(T);  // columns of a step
   constexpr int kPer = Frag<T>::kPer;
-  constexpr int kMT = kRowsT / kWavesR / 16, kOT = kOutsT / kWavesO / 64;  // 16-row tiles, 64-output tiles of a wave
-  constexpr int kLoads = (kRowsT + kOutsT) * 8 / kThreads;                // chunks a thread loads a step
-  static_assert((kRowsT * 8) % kThreads == 0 && (kOutsT * 8) % kThreads == 0, "a load step takes one operand");
-  extern __shared__ uint4 stage[];  // [2][(kRowsT + kOutsT) * 8]
+  constexpr int kMT = kRowsT / kWavesR / 16, kOT = kOutsT / kWavesO / 64;
+  constexpr int kLoadsX = kRowsT * 8 / kThreads, kLoadsW = kOutsT * 8 / kThreads;  // chunks a thread loads a step
+  constexpr int kBuf = (kRowsT + kOutsT) * 8;
+  static_assert((kRowsT * 8) % kThreads == 0 && (kOutsT * 8) % kThreads == 0, "a load takes rows of one operand");
+  extern __shared__ uint4 stage[];  // [2][kBuf]: x rows, then W rows
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
   const int wr = wave / kWavesO, wo = wave % kWavesO;
 
@@ -441,39 +496,73 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   const int o0 = in_band / band_rows * kOutsT;
   const int k_first = slice * a.slice_cols, k_end = min(a.K, k_first + a.slice_cols);
 
-  // chunk i of a thread: row (tid + i kThreads) / 8 of the stage (x rows, then W rows), place tid % 8
-  const char* src[kLoads];
-  int chunk[kLoads];
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int at = tid + i * kThreads, row = at >> 3;
-    if (i < kRowsT * 8 / kThreads) {
-      chunk[i] = (at & 7) ^ place_x(row);
-      src[i] = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + min(r0 + row, a.n_rows - 1) * a.x_stride);
-    } else {
-      chunk[i] = (at & 7) ^ place_w(row - kRowsT);
-      src[i] = reinterpret_cast<const char*>(static_cast<const T*>(a.weight) + static_cast<int64_t>(min(o0 + row - kRowsT, a.O - 1)) * a.weight_stride);
-    }
-    src[i] += chunk[i] * 16;
-  }
-  uint4 hold[kDirect ? 1 : kLoads];
+  // load i of a thread: row (tid + i kThreads) / 8 of its operand, place tid % 8. Offsets in bytes from
+  // the tile's first row fit 32 bits: the host sends strides past 2^23 bytes down the other way.
+  const char* xb = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + r0 * a.x_stride);
+  const char* wb = reinterpret_cast<const char*>(static_cast<const T*>(a.weight) + static_cast<int64_t>(o0) * a.weight_stride);
+  static_assert(kThreads % 256 == 0, "all loads of a thread have the same chunk");
+  const int chunk_x = (tid & 7) ^ place_x(tid >> 3), chunk_w = (tid & 7) ^ place_w(tid >> 3);
+  const int last_x = static_cast<int>(min(static_cast<int64_t>(kRowsT), a.n_rows - r0)) - 1, last_w = min(kOutsT, a.O - o0) - 1;
+  auto row_x = [&](int t, int i) { return min((t + i * kThreads) >> 3, last_x); };
+  auto row_w = [&](int t, int i) { return min((t + i * kThreads) >> 3, last_w); };
+  // The thread's number, as a value that the compiler has to take for a new one each time: otherwise it
+  // keeps every address that follows from it across the loop, and spills them for the products' registers.
+  auto fresh_tid = [&]() {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return t;
+  };
+  const uint32_t stride_x = static_cast<uint32_t>(a.x_stride * sizeof(T)), stride_w = static_cast<uint32_t>(a.weight_stride * sizeof(T));
+  uint4 hold[kDirect ? 1 : kLoadsX + kLoadsW];
   auto fetch = [&](int k, int buf) {
+    const int ft = fresh_tid();
+    if (kDirect) {
+      // a wave's 64 chunks of a load are adjacent in LDS
+      uint4* to = stage + buf * kBuf + (tid & ~63);
+      const char* x = xb + static_cast<int64_t>(k) * sizeof(T);
+      const char* w = wb + static_cast<int64_t>(k) * sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      if (kDirect) {
-        // a wave's 64 chunks are adjacent in LDS, lane by lane
-        uint4* to = stage + buf * (kRowsT + kOutsT) * 8 + (tid & ~63) + i * kThreads;
-        load_to_lds(src[i] + static_cast<int64_t>(k) * sizeof(T), to);
-      } else {
-        const Frag<T> f = load_frag<T>(reinterpret_cast<const T*>(src[i] - chunk[i] * 16), k + chunk[i] * kPer, k_end);
+      for (int i = 0; i < kLoadsX; ++i) load_to_lds(x, row_x(ft, i) * stride_x + 16 * chunk_x, to + i * kThreads);
+#pragma unroll
+      for (int i = 0; i < kLoadsW; ++i) load_to_lds(w, row_w(ft, i) * stride_w + 16 * chunk_w, to + kRowsT * 8 + i * kThreads);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoadsX; ++i) {
+        const Frag<T> f = load_frag<T>(reinterpret_cast<const T*>(xb) + row_x(ft, i) * a.x_stride, k + chunk_x * kPer, k_end);
         __builtin_memcpy(&hold[i], &f.v, 16);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoadsW; ++i) {
+        const Frag<T> f = load_frag<T>(reinterpret_cast<const T*>(wb) + row_w(ft, i) * a.weight_stride, k + chunk_w * kPer, k_end);
+        __builtin_memcpy(&hold[kLoadsX + i], &f.v, 16);
       }
     }
   };
+  // ends a fetch: its data is this wave's own until it has arrived in LDS
   auto settle = [&](int buf) {
-    if (!kDirect) {
+    if (kDirect) {
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    } else {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) stage[buf * (kRowsT + kOutsT) * 8 + tid + i * kThreads] = hold[i];
+      for (int i = 0; i < kLoadsX; ++i) stage[buf * kBuf + tid + i * kThreads] = hold[i];
+#pragma unroll
+      for (int i = 0; i < kLoadsW; ++i) stage[buf * kBuf + kRowsT * 8 + tid + i * kThreads] = hold[kLoadsX + i];
+    }
+  };
+  auto read = [&](int buf, int half, Frag<T> (&xf)[kMT], Frag<T> (&wf)[kOT][4]) {
+    const uint4* sx = stage + buf * kBuf;
+    const uint4* sw = sx + kRowsT * 8;
+#pragma unroll
+    for (int n = 0; n < kOT; ++n)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = (wo * kOT + n) * 64 + 16 * (l16 >> 2) + 4 * t + (l16 & 3);
+        __builtin_memcpy(&wf[n][t].v, &sw[row * 8 + ((4 * half + q) ^ place_w(row))], 16);
+      }
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const int row = (wr * kMT + m) * 16 + l16;
+      __builtin_memcpy(&xf[m].v, &sx[row * 8 + ((4 * half + q) ^ place_x(row))], 16);
     }
   };
 
@@ -484,50 +573,116 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
     for (int m = 0; m < kMT; ++m)
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[n][m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  fetch(k_first, 0);
-  settle(0);
-  if (kDirect) __builtin_amdgcn_s_waitcnt(kWaitLoads);
-  __syncthreads();
-  int buf = 0;
-  for (int k = k_first; k < k_end; k += kStep, buf ^= 1) {
-    const bool more = k + kStep < k_end;
-    if (more) fetch(k + kStep, buf ^ 1);
-    const uint4* sx = stage + buf * (kRowsT + kOutsT) * 8;
-    const uint4* sw = sx + kRowsT * 8;
+  auto products = [&](Frag<T> (&xf)[kMT], Frag<T> (&wf)[kOT][4]) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      Frag<T> wf[kOT][4];
+    for (int m = 0; m < kMT; ++m)
 #pragma unroll
       for (int n = 0; n < kOT; ++n)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int row = (wo * kOT + n) * 64 + 16 * (l16 >> 2) + 4 * t + (l16 & 3);
-          __builtin_memcpy(&wf[n][t].v, &sw[row * 8 + ((4 * half + q) ^ place_w(row))], 16);
-        }
+        for (int t = 0; t < 4; ++t) acc[n][m][t] = mma(wf[n][t], xf[m], acc[n][m][t]);
+  };
+
+  // The up product: for each adapter among the tile's rows, steps of 32 rank columns at the end of the
+  // reduction, x rows holding v (bf16: its high halves, then its low ones) or zero, W rows holding U
+  // (bf16: twice). Zeros keep an adapter out of other rows unless it holds an infinity or NaN: such
+  // entries are staged as zero, and the adapter's rows are noted and computed one by one at the end.
+  __shared__ uint32_t spoiled[kRowsT / 32];
+  constexpr int kIds = (kRowsT + 63) / 64;
+  constexpr int kSplit = sizeof(T) == 2 ? 4 : 8;  // chunks of a row before the columns repeat
+  auto row_id = [&](int t, int i) {               // the adapter of tile row 64 i + t, t the lane
+    const int64_t r = r0 + 64 * i + t;
+    return (64 * i + t < kRowsT && r < a.n_rows) ? a.row_adapter[r] : -1;
+  };
+  uint64_t todo[kIds];  // tile rows whose adapter is still to come; the same in every wave
+  int cur = -1, cur_rank = 0, cur_col = 0;
 #pragma unroll
-      for (int m = 0; m < kMT; ++m) {
-        const int row = (wr * kMT + m) * 16 + l16;
-        Frag<T> xf;
-        __builtin_memcpy(&xf.v, &sx[row * 8 + ((4 * half + q) ^ place_x(row))], 16);
+  for (int i = 0; i < kIds; ++i) todo[i] = 0;
+  if (tid < kRowsT / 32) spoiled[tid] = 0u;
+  if (a.vq) {
 #pragma unroll
-        for (int n = 0; n < kOT; ++n)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[n][m][t] = mma(wf[n][t], xf, acc[n][m][t]);
-      }
+    for (int i = 0; i < kIds; ++i) {
+      const int id = row_id(lane, i);
+      todo[i] = __ballot(id >= 0 && id < a.A);
     }
-    if (more) settle(buf ^ 1);
-    // loads into LDS are this wave's own until they have arrived: wait before the others may read them
-    if (kDirect) __builtin_amdgcn_s_waitcnt(kWaitLoads);
+  }
+  auto next_up = [&]() {  // moves on by 32 columns or to the next adapter; false if none is left
+    cur_col += 32;
+    while (cur_col >= cur_rank) {
+      int first = -1;
+#pragma unroll
+      for (int i = kIds - 1; i >= 0; --i)
+        if (todo[i]) first = 64 * i + __builtin_ctzll(todo[i]);
+      if (first < 0) return false;
+      const int ft = fresh_tid() & 63;
+      cur = __builtin_amdgcn_readfirstlane(a.row_adapter[r0 + first]);
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) todo[i] &= ~__ballot(row_id(ft, i) == cur);
+      cur_rank = __builtin_amdgcn_readfirstlane(rank_of(a, cur));
+      cur_col = 0;
+    }
+    return true;
+  };
+  auto stage_up = [&](int buf) {
+    const int ft = fresh_tid();
+#pragma unroll
+    for (int i = 0; i < kLoadsX; ++i) {
+      const int64_t r = r0 + ((ft + i * kThreads) >> 3);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < a.n_rows && a.row_adapter[r] == cur)
+        v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.vq) + r * a.vq_row + (chunk_x < kSplit ? 0 : a.vq_row / 2) + cur_col +
+                                            (chunk_x & (kSplit - 1)) * kPer);
+      stage[buf * kBuf + tid + i * kThreads] = v;
+    }
+    bool wild = false;
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i) {
+      const Frag<T> u = load_frag<T>(static_cast<const T*>(a.up) + (static_cast<int64_t>(cur) * a.O + o0 + row_w(ft, i)) * a.R,
+                                     cur_col + (chunk_w & (kSplit - 1)) * kPer, cur_rank);
+      T e[kPer];
+      __builtin_memcpy(e, &u.v, 16);
+#pragma unroll
+      for (int n = 0; n < kPer; ++n)
+        if (!(fabsf(to_float(e[n])) <= 3.4028235e38f)) {
+          wild = true;
+          e[n] = T(0);
+        }
+      __builtin_memcpy(&stage[buf * kBuf + kRowsT * 8 + tid + i * kThreads], e, 16);
+    }
+    if (wild)
+      for (int row = 0; row < kRowsT; ++row)
+        if (r0 + row < a.n_rows && a.row_adapter[r0 + row] == cur) atomicOr(&spoiled[row >> 5], 1u << (row & 31));
+  };
+
+  Frag<T> x0[kMT], x1[kMT], w0[kOT][4], w1[kOT][4];
+  fetch(k_first, 0);
+  settle(0);
+  __syncthreads();
+  if (k_first + kStep < k_end) fetch(k_first + kStep, 1);
+  read(0, 0, x0, w0);
+  for (int k = k_first, buf = 0;; k += kStep, buf ^= 1) {
+    read(buf, 1, x1, w1);
+    products(x0, w0);
+    bool more = true;
+    if (k + kStep < k_end)
+      settle(buf ^ 1);
+    else if ((more = next_up()))
+      stage_up(buf ^ 1);
+    __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
+    if (more) {
+      if (k + 2 * kStep < k_end) fetch(k + 2 * kStep, buf);
+      read(buf ^ 1, 0, x0, w0);
+    }
+    products(x1, w1);
+    if (!more) break;
   }
 
   const int64_t rw = r0 + wr * kMT * 16;
+  if (a.slices > 1) {
 #pragma unroll
-  for (int n = 0; n < kOT; ++n) {
-    const int o = o0 + (wo * kOT + n) * 64;
-    if (o >= a.O) continue;
-    if (a.slices > 1) {
+    for (int n = 0; n < kOT; ++n) {
+      const int o = o0 + (wo * kOT + n) * 64;
+      if (o >= a.O) continue;
 #pragma unroll
       for (int m = 0; m < kMT; ++m) {
         const int64_t r = rw + 16 * m + l16;
@@ -536,9 +691,53 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
 #pragma unroll
         for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(p + 4 * t) = acc[n][m][t];
       }
-    } else {
-      adapter_epilogue<T, 0, 4>(a, rw, o, acc[n]);
-      if constexpr (kMT > 4) adapter_epilogue<T, 4, 4>(a, rw + 64, o, acc[n]);
+    }
+    return;
+  }
+
+  uint32_t noted = 0;
+#pragma unroll
+  for (int i = 0; i < kRowsT / 32; ++i) noted |= spoiled[i];
+#pragma unroll
+  for (int n = 0; n < kOT; ++n) {
+    const int o = o0 + (wo * kOT + n) * 64 + 16 * q;
+    float bias[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bias[i] = a.bias && o + i < a.O ? to_float(static_cast<const T*>(a.bias)[o + i]) : 0.f;
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const int row = (wr * kMT + m) * 16 + l16;
+      const int64_t r = r0 + row;
+      if (r >= a.n_rows || (noted && (spoiled[row >> 5] >> (row & 31) & 1u))) continue;
+      const bool out_of_range = a.row_adapter && a.row_adapter[r] >= a.A;
+      T out[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[i] = from_float<T>(out_of_range ? __builtin_nanf("") : acc[n][m][i >> 2][i & 3] + bias[i]);
+      T* y = static_cast<T*>(a.y) + r * a.y_stride + o;
+      if (o + 16 <= a.O) {
+        __builtin_memcpy(y, out, sizeof(out));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (o + i < a.O) y[i] = out[i];
+      }
+    }
+  }
+  if (noted) {
+    for (int row = 0; row < kRowsT; ++row) {
+      if (!(spoiled[row >> 5] >> (row & 31) & 1u)) continue;
+      const int64_t r = r0 + row;
+      const int ad = a.row_adapter[r], rank = rank_of(a, ad);
+      const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+      for (int o = o0 + tid; o < min(o0 + kOutsT, a.O); o += kThreads) {
+        const T* w = static_cast<const T*>(a.weight) + static_cast<int64_t>(o) * a.weight_stride;
+        const T* u = static_cast<const T*>(a.up) + (static_cast<int64_t>(ad) * a.O + o) * a.R;
+        float s = a.bias ? to_float(static_cast<const T*>(a.bias)[o]) : 0.f;
+        for (int k = 0; k < a.K; ++k) s += to_float(x[k]) * to_float(w[k]);
+        const T* v = static_cast<const T*>(a.vq) + r * a.vq_row;
+        for (int j = 0; j < rank; ++j) s += (to_float(v[j]) + (sizeof(T) == 2 ? to_float(v[a.vq_row / 2 + j]) : 0.f)) * to_float(u[j]);
+        static_cast<T*>(a.y)[r * a.y_stride + o] = from_float<T>(s);
+      }
     }
   }
 }
