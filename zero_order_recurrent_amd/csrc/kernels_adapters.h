@@ -21,6 +21,8 @@
 // of one row; tile t of four takes the outputs 16 (i / 4) + 4 t + i % 4 for its rows i, which makes a
 // lane's outputs of all four tiles 16 adjacent ones.
 #pragma once
+#include <type_traits>
+
 #include "operators_common.h"
 
 namespace cdrge {
@@ -477,6 +479,8 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   constexpr int kMT = kRowsT / kWavesR / 16, kOT = kOutsT / kWavesO / 64;
   constexpr int kLoadsX = kRowsT * 8 / kThreads, kLoadsW = kOutsT * 8 / kThreads;  // chunks a thread loads a step
   constexpr int kBuf = (kRowsT + kOutsT) * 8;
+  constexpr int kPerTile = (kLoadsX + kLoadsW) / kMT;  // loads of a step beside one row tile's products
+  static_assert(kPerTile * kMT == kLoadsX + kLoadsW, "all loads of a step are issued");
   static_assert((kRowsT * 8) % kThreads == 0 && (kOutsT * 8) % kThreads == 0, "a load takes rows of one operand");
   extern __shared__ uint4 stage[];  // [2][kBuf]: x rows, then W rows
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
@@ -514,17 +518,21 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   };
   const uint32_t stride_x = static_cast<uint32_t>(a.x_stride * sizeof(T)), stride_w = static_cast<uint32_t>(a.weight_stride * sizeof(T));
   uint4 hold[kDirect ? 1 : kLoadsX + kLoadsW];
+  // Load n of a step (n counts x's, then W's), straight into LDS: a wave's 64 chunks are adjacent there.
+  // Rows past the operand's last are read from the last.
+  auto load = [&](int n, int k, int buf, int ft) {
+    const bool of_x = n < kLoadsX;
+    const int i = of_x ? n : n - kLoadsX;
+    const uint32_t stride = of_x ? stride_x : stride_w, last = (of_x ? last_x : last_w) * stride;
+    const uint32_t row = (ft >> 3) * stride + (i * kThreads / 8) * stride;
+    load_to_lds((of_x ? xb : wb) + static_cast<int64_t>(k) * sizeof(T), min(row, last) + 16 * (of_x ? chunk_x : chunk_w),
+                stage + buf * kBuf + (of_x ? 0 : kRowsT * 8) + (tid & ~63) + i * kThreads);
+  };
   auto fetch = [&](int k, int buf) {
     const int ft = fresh_tid();
     if (kDirect) {
-      // a wave's 64 chunks of a load are adjacent in LDS
-      uint4* to = stage + buf * kBuf + (tid & ~63);
-      const char* x = xb + static_cast<int64_t>(k) * sizeof(T);
-      const char* w = wb + static_cast<int64_t>(k) * sizeof(T);
 #pragma unroll
-      for (int i = 0; i < kLoadsX; ++i) load_to_lds(x, row_x(ft, i) * stride_x + 16 * chunk_x, to + i * kThreads);
-#pragma unroll
-      for (int i = 0; i < kLoadsW; ++i) load_to_lds(w, row_w(ft, i) * stride_w + 16 * chunk_w, to + kRowsT * 8 + i * kThreads);
+      for (int n = 0; n < kLoadsX + kLoadsW; ++n) load(n, k, buf, ft);
     } else {
 #pragma unroll
       for (int i = 0; i < kLoadsX; ++i) {
@@ -549,9 +557,9 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
       for (int i = 0; i < kLoadsW; ++i) stage[buf * kBuf + kRowsT * 8 + tid + i * kThreads] = hold[kLoadsX + i];
     }
   };
-  auto read = [&](int buf, int half, Frag<T> (&xf)[kMT], Frag<T> (&wf)[kOT][4]) {
-    const uint4* sx = stage + buf * kBuf;
-    const uint4* sw = sx + kRowsT * 8;
+  // The operands of one half of a step: W's for all output tiles, x's by row tile.
+  auto read_w = [&](int buf, int half, Frag<T> (&wf)[kOT][4]) {
+    const uint4* sw = stage + buf * kBuf + kRowsT * 8;
 #pragma unroll
     for (int n = 0; n < kOT; ++n)
 #pragma unroll
@@ -559,11 +567,10 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
         const int row = (wo * kOT + n) * 64 + 16 * (l16 >> 2) + 4 * t + (l16 & 3);
         __builtin_memcpy(&wf[n][t].v, &sw[row * 8 + ((4 * half + q) ^ place_w(row))], 16);
       }
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) {
-      const int row = (wr * kMT + m) * 16 + l16;
-      __builtin_memcpy(&xf[m].v, &sx[row * 8 + ((4 * half + q) ^ place_x(row))], 16);
-    }
+  };
+  auto read_x = [&](int buf, int half, int m, Frag<T> (&xf)[kMT]) {
+    const int row = (wr * kMT + m) * 16 + l16;
+    __builtin_memcpy(&xf[m].v, &(stage + buf * kBuf)[row * 8 + ((4 * half + q) ^ place_x(row))], 16);
   };
 
   f32x4 acc[kOT][kMT][4];
@@ -573,13 +580,11 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
     for (int m = 0; m < kMT; ++m)
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[n][m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto products = [&](Frag<T> (&xf)[kMT], Frag<T> (&wf)[kOT][4]) {
+  auto products = [&](int m, Frag<T> (&xf)[kMT], Frag<T> (&wf)[kOT][4]) {
 #pragma unroll
-    for (int m = 0; m < kMT; ++m)
+    for (int n = 0; n < kOT; ++n)
 #pragma unroll
-      for (int n = 0; n < kOT; ++n)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[n][m][t] = mma(wf[n][t], xf[m], acc[n][m][t]);
+      for (int t = 0; t < 4; ++t) acc[n][m][t] = mma(wf[n][t], xf[m], acc[n][m][t]);
   };
 
   // The up product: for each adapter among the tile's rows, steps of 32 rank columns at the end of the
@@ -658,23 +663,45 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   settle(0);
   __syncthreads();
   if (k_first + kStep < k_end) fetch(k_first + kStep, 1);
-  read(0, 0, x0, w0);
-  for (int k = k_first, buf = 0;; k += kStep, buf ^= 1) {
-    read(buf, 1, x1, w1);
-    products(x0, w0);
+  read_w(0, 0, w0);
+#pragma unroll
+  for (int m = 0; m < kMT; ++m) read_x(0, 0, m, x0);
+  // One step; kLoad: the step after next is loaded on the way, between two row tiles' products, so that a
+  // full load queue does not keep the matrix cores waiting. Returns false after the last step.
+  auto step = [&](auto load_too, int k, int buf) {
+    constexpr bool kLoad = decltype(load_too)::value;
+    read_w(buf, 1, w1);
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      read_x(buf, 1, m, x1);
+      products(m, x0, w0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     bool more = true;
-    if (k + kStep < k_end)
+    if (kLoad || k + kStep < k_end)
       settle(buf ^ 1);
     else if ((more = next_up()))
       stage_up(buf ^ 1);
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
-    if (more) {
-      if (k + 2 * kStep < k_end) fetch(k + 2 * kStep, buf);
-      read(buf ^ 1, 0, x0, w0);
+    const int ft = fresh_tid();
+    if (kLoad && !kDirect) fetch(k + 2 * kStep, buf);
+    read_w(buf ^ 1, 0, w0);  // after the last step: what lies there, not used
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      if (kLoad && kDirect) {
+#pragma unroll
+        for (int n = m * kPerTile; n < (m + 1) * kPerTile; ++n) load(n, k + 2 * kStep, buf, ft);
+      }
+      read_x(buf ^ 1, 0, m, x0);
+      products(m, x1, w1);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    products(x1, w1);
-    if (!more) break;
+    return more;
+  };
+  int k = k_first, buf = 0;
+  for (; k + 2 * kStep < k_end; k += kStep, buf ^= 1) step(std::true_type{}, k, buf);
+  for (; step(std::false_type{}, k, buf); k += kStep, buf ^= 1) {
   }
 
   const int64_t rw = r0 + wr * kMT * 16;
