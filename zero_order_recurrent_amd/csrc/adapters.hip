@@ -27,7 +27,7 @@ cdrge_status check(const cdrge_adapter_config* c, int64_t n_rows) {
 // How a call is cut up. It goes by the sizes alone, so that the workspace is known without pointers.
 struct Cut {
   bool rows;             // k_adapter_rows (up to 64 rows)
-  bool big;              // 256 x 256 tiles, otherwise 128 x 128
+  int side;              // of the tiles of the shared product (k_adapter_tiles)
   int tiles_r, tiles_o, slices, slice_cols;
   int v_slices, v_cols, v_slots;
   bool packed;           // v as operand rows
@@ -57,20 +57,20 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
     // four waves share a slice: at least two steps of 64 bytes each for every wave
     want = std::min(want, ceil_div(K, 4 * step));
   } else {
-    p.big = int64_t(ceil_div(n_rows, 256)) * ceil_div(O, 256) >= 192;
-    const int side = p.big ? 256 : 128;
-    p.tiles_r = ceil_div(n_rows, side);
-    p.tiles_o = ceil_div(O, side);
-    // slices where the tiles alone leave compute units idle, of at least 8 steps
-    const int64_t tiles = int64_t(p.tiles_r) * p.tiles_o;
-    want = p.big || tiles >= 256 ? 1 : std::min(ceil_div(kWorkgroups, tiles), ceil_div(K, 8 * step));
+    // 256 x 256 tiles where they fill the chip; 128 x 128, in slices of at least 8 steps where the tiles alone
+    // leave compute units idle; 64 x 64 where K is too short for slices
+    auto tiles = [&](int side) { return int64_t(ceil_div(n_rows, side)) * ceil_div(O, side); };
+    p.side = tiles(256) >= 192 ? 256 : (tiles(128) >= 192 || K >= 16 * step ? 128 : 64);
+    p.tiles_r = ceil_div(n_rows, p.side);
+    p.tiles_o = ceil_div(O, p.side);
+    want = p.side != 128 || tiles(128) >= 256 ? 1 : std::min(ceil_div(kWorkgroups, tiles(128)), ceil_div(K, 8 * step));
   }
   p.slice_cols = slice_columns(K, want, p.rows ? 4 * step / 2 : step);
   p.slices = ceil_div(K, p.slice_cols);
   const int v_tiles = ceil_div(n_rows, 64);
   // beside up to 64 rows: 16 workgroups for the adapters, four for K; otherwise as many as fill the chip
   p.v_slots = std::max(1, std::min({c->n_adapters, 16, ceil_div(256, v_tiles)}));
-  p.v_cols = slice_columns(K, p.rows ? kMostVSlices : 1, 4 * step);
+  p.v_cols = slice_columns(K, p.rows || p.slices > 1 ? kMostVSlices : 1, 4 * step);
   p.v_slices = ceil_div(K, p.v_cols);
   p.packed = !p.rows && p.slices == 1;
   p.vq_row = (c->max_rank + 31) / 32 * 32 * (c->dtype == CDRGE_F32 ? 1 : 2);
@@ -89,7 +89,7 @@ void launch_rows(const AdapterArgs& a, int blocks, hipStream_t s) {
 }
 
 template <class T, int kSide, int kWavesR, int kWavesO, bool kDirect>
-cdrge_status launch_tiles(const AdapterArgs& a, hipStream_t s) {
+cdrge_status launch_tiles(const AdapterArgs& a, int64_t blocks, hipStream_t s) {
   constexpr size_t kLds = 2 * 2 * kSide * 128;
   const void* f = reinterpret_cast<const void*>(k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>);
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use this much LDS
@@ -99,10 +99,26 @@ cdrge_status launch_tiles(const AdapterArgs& a, hipStream_t s) {
     CDRGE_HIP(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
     ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL((k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>),
-                     dim3(static_cast<uint32_t>(int64_t(a.tiles_r) * a.tiles_o * a.slices)), dim3(64 * kWavesR * kWavesO), kLds, s, a);
+  hipLaunchKernelGGL((k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>), dim3(static_cast<uint32_t>(blocks)),
+                     dim3(64 * kWavesR * kWavesO), kLds, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
+}
+
+template <class T, bool kDirect>
+cdrge_status launch_side(AdapterArgs a, int side, bool low, hipStream_t s) {
+  // chunks that pass through registers leave no room for the products of the largest tiles
+  if (!kDirect && side == 256) {
+    side = 128;
+    a.tiles_r = ceil_div(a.n_rows, side);
+    a.tiles_o = ceil_div(a.O, side);
+  }
+  const int64_t down = low && a.slices > 1 ? int64_t(ceil_div(a.n_rows, 64)) * a.v_slices * a.v_slots : 0;
+  const int64_t blocks = int64_t(a.tiles_r) * a.tiles_o * a.slices + down;
+  if (side == 64) return launch_tiles<T, 64, 4, 1, kDirect>(a, blocks, s);
+  if (side == 128) return launch_tiles<T, 128, 2, 2, kDirect>(a, blocks, s);
+  if constexpr (kDirect) return launch_tiles<T, 256, 2, 4, true>(a, blocks, s);
+  return CDRGE_ERR_UNSUPPORTED;
 }
 
 template <class T>
@@ -118,7 +134,7 @@ cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
     }
     CDRGE_HIP(hipGetLastError());
   } else {
-    if (low) {
+    if (low && a.slices == 1) {
       const int64_t blocks = int64_t(ceil_div(a.n_rows, 64)) * a.v_slots;
       hipLaunchKernelGGL(k_adapter_down<T>, dim3(static_cast<uint32_t>(blocks)), dim3(1024), 0, s, a);
       CDRGE_HIP(hipGetLastError());
@@ -127,20 +143,8 @@ cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
     const bool direct = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0 &&
                         a.x_stride % kPer == 0 && a.weight_stride % kPer == 0 && a.K % kStep == 0 &&
                         std::max(a.x_stride, a.weight_stride) <= int64_t(1 << 23) / int64_t(sizeof(T));
-    cdrge_status st;
-    if (p.big && direct) {
-      st = launch_tiles<T, 256, 2, 4, true>(a, s);
-    } else if (direct) {
-      st = launch_tiles<T, 128, 2, 2, true>(a, s);
-    } else {
-      // chunks that pass through registers leave no room for the products of the large tiles
-      AdapterArgs b = a;
-      b.tiles_r = ceil_div(a.n_rows, 128);
-      b.tiles_o = ceil_div(a.O, 128);
-      st = launch_tiles<T, 128, 2, 2, false>(b, s);
-    }
-    if (st != CDRGE_OK) return st;
-    if (a.slices == 1) return CDRGE_OK;
+    const cdrge_status st = direct ? launch_side<T, true>(a, p.side, low, s) : launch_side<T, false>(a, p.side, low, s);
+    if (st != CDRGE_OK || a.slices == 1) return st;
   }
   hipLaunchKernelGGL(k_adapter_finish<T>, dim3(a.o_pad / 64, static_cast<uint32_t>((a.n_rows + 15) / 16)), dim3(256), 0, s, a);
   CDRGE_HIP(hipGetLastError());
@@ -172,7 +176,7 @@ cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_
   if (n_rows == 0) return CDRGE_OK;
   if (!x || !y) return CDRGE_ERR_INVALID_ARG;
   const Cut p = make_cut(cfg, n_rows);
-  if (int64_t(ceil_div(n_rows, 128)) * ceil_div(O, 128) * p.slices > kMostBlocks || (p.rows && int64_t(p.tiles_o) * p.slices > kMostBlocks / 2) || int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks)
+  if (int64_t(ceil_div(n_rows, 64)) * ceil_div(O, 64) * p.slices > kMostBlocks / 2 ||  int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks / 2)
     return CDRGE_ERR_UNSUPPORTED;
   if (p.total > 0 && (!ws || workspace_bytes < p.total || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return workspace_error("cdrge_adapter_project", p.total, ws ? workspace_bytes : 0);

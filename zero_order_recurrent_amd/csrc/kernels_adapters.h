@@ -77,21 +77,48 @@ __device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b,
   return c;
 }
 
-// Columns k .. k + kPer - 1 of a row that ends at column n: one 16-byte load where they lie inside (global
-// memory takes it at any element's alignment), element by element at the end, zero past it.
+// The 16 bytes from element `at` of a matrix on (global memory takes them at any element's alignment).
 template <class T>
-__device__ __forceinline__ Frag<T> load_frag(const T* row, int k, int n) {
+__device__ __forceinline__ Frag<T> load_frag(const T* at) {
   Frag<T> f;
-  if (k + Frag<T>::kPer <= n) {
-    __builtin_memcpy(&f.v, row + k, 16);
-    return f;
-  }
-  T e[Frag<T>::kPer];
+  __builtin_memcpy(&f.v, at, 16);
+  return f;
+}
+
+// The same where a row may end inside: elements from n on are zero. The load is one for all lanes, with no
+// branch between a wave's loads; it may pass into the next row, but never past the matrix's last element
+// (`total` elements): there it starts earlier and is moved into place.
+template <class T>
+__device__ __forceinline__ Frag<T> load_cut(const T* base, int64_t at, int64_t total, int n) {
+  constexpr int kPer = Frag<T>::kPer;
+  T e[kPer];
+  if (total >= kPer) {
+    const int64_t from = min(at, total - kPer);
+    __builtin_memcpy(e, base + from, 16);
+    const int late = static_cast<int>(min(at - from, static_cast<int64_t>(kPer)));
+    if (__any(late != 0)) {
 #pragma unroll
-  for (int i = 0; i < Frag<T>::kPer; ++i) e[i] = k + i < n ? row[k + i] : T(0);
+      for (int step = 1; step <= kPer; step *= 2)
+        if (late & step) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) e[i] = i + step < kPer ? e[i + step] : T(0);
+        }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = at + i < total ? base[at + i] : T(0);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) e[i] = i < n ? e[i] : T(0);
+  Frag<T> f;
   __builtin_memcpy(&f.v, e, 16);
   return f;
 }
+
+// Elements from the first of a matrix to its last.
+__device__ __forceinline__ int64_t span_x(const AdapterArgs& a) { return (a.n_rows - 1) * a.x_stride + a.K; }
+__device__ __forceinline__ int64_t span_w(const AdapterArgs& a) { return static_cast<int64_t>(a.O - 1) * a.weight_stride + a.K; }
+__device__ __forceinline__ int64_t span_up(const AdapterArgs& a) { return static_cast<int64_t>(a.A) * a.O * a.R; }
 
 __device__ __forceinline__ int rank_of(const AdapterArgs& a, int ad) {
   return a.ranks ? min(max(a.ranks[ad], 0), a.R) : a.R;
@@ -112,9 +139,10 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int64_t r0 = tile * 64;
   const int ad = r0 + lane < a.n_rows ? a.row_adapter[r0 + lane] : -1;
-  const T* x[4];
+  const T* const xs = static_cast<const T*>(a.x);
+  int64_t x[4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) x[m] = static_cast<const T*>(a.x) + min(r0 + 16 * m + l16, a.n_rows - 1) * a.x_stride;
+  for (int m = 0; m < 4; ++m) x[m] = min(r0 + 16 * m + l16, a.n_rows - 1) * a.x_stride;
   const int k0 = slice * a.v_cols, k1 = min(a.K, k0 + a.v_cols);
   uint64_t todo = __ballot(ad >= 0 && ad < a.A);
   const float scale = (a.vq && a.row_scale && r0 + lane < a.n_rows) ? a.row_scale[r0 + lane] : 1.f;
@@ -123,24 +151,26 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
     const uint64_t mine = __ballot(ad == cur);
     todo &= ~mine;
     if (n % a.v_slots != slot) continue;
-    const int rank = rank_of(a, cur);
+    // rows of D past the rank give values that are not kept, so with up to 16 of them nothing waits for the rank
+    const int rank = rank_of(a, cur), most = a.R <= 16 ? a.R : rank;
     const bool all = (mine & 0xffffu) && (mine & 0xffff0000u) && (mine >> 32 & 0xffffu) && (mine >> 48);
-    for (int j0 = 0; j0 < (a.vq ? vq_columns(rank) : rank); j0 += 16) {
-      const T* d = static_cast<const T*>(a.down) + (static_cast<int64_t>(cur) * a.R + min(j0 + l16, rank - 1)) * a.K;
+    for (int j0 = 0; j0 < (a.vq ? vq_columns(most) : most); j0 += 16) {
+      const T* const ds = static_cast<const T*>(a.down);
+      const int64_t d = (static_cast<int64_t>(cur) * a.R + min(j0 + l16, most - 1)) * a.K;
       f32x4 acc[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
       constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer, kDeep = 4;  // steps whose loads are in flight together
-      int k = k0 + wave * kCols;
+      int k = j0 < most ? k0 + wave * kCols : k1;  // past the rank: zeros
       if (all) {
         for (; k + (kWaves * (kDeep - 1) + 1) * kCols <= k1; k += kWaves * kDeep * kCols) {
           Frag<T> df[kDeep], xf[kDeep][4];
 #pragma unroll
           for (int s = 0; s < kDeep; ++s) {
             const int at = k + kWaves * s * kCols + q * kPer;
-            __builtin_memcpy(&df[s].v, d + at, 16);
+            df[s] = load_frag<T>(ds + d + at);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) __builtin_memcpy(&xf[s][m].v, x[m] + at, 16);
+            for (int m = 0; m < 4; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
           }
 #pragma unroll
           for (int s = 0; s < kDeep; ++s)
@@ -149,10 +179,11 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
         }
       }
       for (; k < k1; k += kWaves * kCols) {
-        const Frag<T> df = load_frag<T>(d, k + q * kPer, k1);
+        const int at = k + q * kPer;
+        const Frag<T> df = load_cut<T>(ds, d + at, static_cast<int64_t>(a.A) * a.R * a.K, k1 - at);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          if ((mine >> (16 * m)) & 0xffffu) acc[m] = mma(df, load_frag<T>(x[m], k + q * kPer, k1), acc[m]);
+          if ((mine >> (16 * m)) & 0xffffu) acc[m] = mma(df, load_cut<T>(xs, x[m] + at, span_x(a), k1 - at), acc[m]);
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) lds[wave][m][lane] = acc[m];
@@ -196,14 +227,15 @@ __global__ __launch_bounds__(1024) void k_adapter_down(AdapterArgs a) {
   adapter_down<T, 16>(a, blockIdx.x / a.v_slots, 0, blockIdx.x % a.v_slots, lds);
 }
 
-// v_r from column j on: the sum over the slices of K, times the row's scale, zero from column n on.
+// v_r from column j on: the sum over the slices of K, without the row's scale; columns from R on are zero.
+// A row without an adapter gives what lies there, not to be used.
 template <int kPer>
-__device__ __forceinline__ void v_values(const AdapterArgs& a, int64_t r, int j, int n, float scale, float (&f)[kPer]) {
+__device__ __forceinline__ void v_sums(const AdapterArgs& a, int64_t r, int j, float (&f)[kPer]) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) f[i] = 0.f;
-  if (j >= n) return;
+  if (j >= a.R || r >= a.n_rows) return;
   const float* v = a.vp + r * a.R + j;
-  if (j + kPer <= n) {
+  if (j + kPer <= a.R) {
     // all slices' loads at once; a slice past the last reads the last again and is not added
 #pragma unroll
     for (int ks = 0; ks < kMostVSlices; ++ks) {
@@ -216,10 +248,15 @@ __device__ __forceinline__ void v_values(const AdapterArgs& a, int64_t r, int j,
     for (int ks = 0; ks < a.v_slices; ++ks, v += a.n_rows * a.R)
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (j + i < n) f[i] += v[i];
+        if (j + i < a.R) f[i] += v[i];
   }
+}
+
+// Those columns from j on, times the scale, with zero from column n on.
+template <int kPer>
+__device__ __forceinline__ void v_scaled(float (&f)[kPer], int j, int n, float scale) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) f[i] *= scale;
+  for (int i = 0; i < kPer; ++i) f[i] = j + i < n ? f[i] * scale : 0.f;
 }
 
 // v_r as an operand. bf16 takes it in two halves, which keeps 16 bits of it.
@@ -236,15 +273,22 @@ __device__ __forceinline__ void v_frag(const float (&f)[8], Frag<uint16_t>& hi, 
   }
 }
 
-// Columns from j on of the four output tiles of adapter cur's up matrix.
+// Columns from j on of the four output tiles of adapter cur's up matrix; up_cut sets those from n on to zero.
 template <class T>
-__device__ __forceinline__ void up_frags(const AdapterArgs& a, int cur, int rank, int o0, int j, Frag<T> (&u)[4]) {
+__device__ __forceinline__ void up_frags(const AdapterArgs& a, int cur, int o0, int j, Frag<T> (&u)[4]) {
   const int l16 = threadIdx.x & 15;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int o = min(o0 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), a.O - 1);
-    u[t] = load_frag<T>(static_cast<const T*>(a.up) + (static_cast<int64_t>(cur) * a.O + o) * a.R, j, rank);
+    u[t] = load_cut<T>(static_cast<const T*>(a.up), (static_cast<int64_t>(cur) * a.O + o) * a.R + j, span_up(a), a.R - j);
   }
+}
+template <class T>
+__device__ __forceinline__ void up_cut(int j, int n, Frag<T> (&u)[4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int i = 0; i < Frag<T>::kPer; ++i) u[t].v[i] = j + i < n ? u[t].v[i] : 0;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -261,6 +305,9 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   const bool rok = r < a.n_rows;
   const int o0 = blockIdx.x * 64;
   const int ad = (a.row_adapter && rok) ? a.row_adapter[r] : -1;
+  const bool narrow = a.R <= kCols;  // one product a tile
+  float vs[kPer];
+  if (narrow && a.row_adapter && a.A > 0) v_sums<kPer>(a, r, q * kPer, vs);
   f32x4 sum[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -274,21 +321,15 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   const bool has = ad >= 0 && ad < a.A;
   uint32_t todo = static_cast<uint32_t>(__ballot(has)) & 0xffffu;
   if (todo) {
+    // two rounds of loads: the adapters of the rows, with the sums; then everything that an adapter names
     const int rank = has ? rank_of(a, ad) : 0;
     const float scale = has && a.row_scale ? a.row_scale[r] : 1.f;
-    const bool narrow = a.R <= kCols;  // one product a tile
-    Frag<T> vh, vl;
-    if (narrow) {
-      float f[kPer];
-      v_values<kPer>(a, r, q * kPer, rank, scale, f);
-      v_frag(f, vh, vl);
-    }
     while (todo) {
-      // the next four of this wave's adapters (every fourth); a repeated one is loaded but not added
+      // the next four of this wave's adapters (every fourth); one that is missing repeats the first
       int cur[4], got = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        cur[i] = i ? cur[0] : -1;
+        cur[i] = i ? cur[0] : 0;
         for (int step = 0; step < 4 && todo; ++step) {
           const int c = __builtin_amdgcn_readlane(ad, __builtin_ctz(todo));
           todo &= ~static_cast<uint32_t>(__ballot(ad == c));
@@ -302,9 +343,16 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
       if (narrow) {
         Frag<T> u[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) up_frags<T>(a, cur[i], rank_of(a, cur[i]), o0, q * kPer, u[i]);
+        for (int i = 0; i < 4; ++i) up_frags<T>(a, cur[i], o0, q * kPer, u[i]);
+        Frag<T> vh, vl;
+        float f[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] = vs[i];
+        v_scaled<kPer>(f, q * kPer, rank, scale);
+        v_frag(f, vh, vl);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (a.ranks) up_cut<T>(q * kPer, rank_of(a, cur[i]), u[i]);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             f32x4 low = mma(u[i][t], vh, f32x4{0.f, 0.f, 0.f, 0.f});
@@ -323,9 +371,11 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
           for (int j = 0; j < rc; j += kCols) {
             float f[kPer];
             Frag<T> hi, lo, u[4];
-            v_values<kPer>(a, r, j + q * kPer, ad == c ? rc : 0, scale, f);
+            up_frags<T>(a, c, o0, j + q * kPer, u);
+            v_sums<kPer>(a, r, j + q * kPer, f);
+            v_scaled<kPer>(f, j + q * kPer, ad == c ? rc : 0, scale);
             v_frag(f, hi, lo);
-            up_frags<T>(a, c, rc, o0, j + q * kPer, u);
+            up_cut<T>(j + q * kPer, rc, u);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               low[t] = mma(u[t], hi, low[t]);
@@ -382,13 +432,13 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
   }
   const int o0 = (blockIdx.x / a.slices) * 64, slice = blockIdx.x % a.slices;
   const int k0 = slice * a.slice_cols, k1 = min(a.K, k0 + a.slice_cols);
-  const T* w[4];
-  const T* x[kTiles];
+  const T* const ws = static_cast<const T*>(a.weight);
+  const T* const xs = static_cast<const T*>(a.x);
+  int64_t w[4], x[kTiles];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    w[t] = static_cast<const T*>(a.weight) + min(o0 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), a.O - 1) * a.weight_stride;
+  for (int t = 0; t < 4; ++t) w[t] = min(o0 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), a.O - 1) * a.weight_stride;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m) x[m] = static_cast<const T*>(a.x) + min(int64_t(16 * m + l16), a.n_rows - 1) * a.x_stride;
+  for (int m = 0; m < kTiles; ++m) x[m] = min(int64_t(16 * m + l16), a.n_rows - 1) * a.x_stride;
   f32x4 acc[kTiles][4];
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
@@ -403,9 +453,9 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
     for (int s = 0; s < kDeep; ++s) {
       const int at = k + 4 * s * kCols + q * kPer;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) __builtin_memcpy(&wf[s][t].v, w[t] + at, 16);
+      for (int t = 0; t < 4; ++t) wf[s][t] = load_frag<T>(ws + w[t] + at);
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) __builtin_memcpy(&xf[s][m].v, x[m] + at, 16);
+      for (int m = 0; m < kTiles; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
     }
 #pragma unroll
     for (int s = 0; s < kDeep; ++s)
@@ -418,13 +468,14 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
     const int at = k + q * kPer;
     Frag<T> wf[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) wf[t] = load_frag<T>(w[t], at, k1);
+    for (int t = 0; t < 4; ++t) wf[t] = load_cut<T>(ws, w[t] + at, span_w(a), k1 - at);
+    Frag<T> xf[kTiles];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const Frag<T> xf = load_frag<T>(x[m], at, k1);
+    for (int m = 0; m < kTiles; ++m) xf[m] = load_cut<T>(xs, x[m] + at, span_x(a), k1 - at);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[m][t] = mma(wf[t], xf, acc[m][t]);
-    }
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[m][t] = mma(wf[t], xf[m], acc[m][t]);
   }
 #pragma unroll
   for (int m = 0; m < kTiles; ++m) {
@@ -488,7 +539,17 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
 
   // Tiles by XCD: workgroups go round the eight XCDs, each of which has its own L2. XCD i gets the
   // i-th eighth of the tiles, walked in columns of up to four row tiles.
-  const int n_tiles = a.tiles_r * a.tiles_o, slice = blockIdx.x / n_tiles;
+  const int n_tiles = a.tiles_r * a.tiles_o;
+  if constexpr (kThreads == 256) {
+    // after a product in slices the up product has a launch of its own, and the down product runs beside it
+    const int64_t past = static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(n_tiles) * a.slices;
+    if (past >= 0) {
+      const int slot = past % a.v_slots, part = past / a.v_slots % a.v_slices;
+      adapter_down<T, 4>(a, past / (a.v_slots * a.v_slices), part, slot, *reinterpret_cast<f32x4(*)[4][4][64]>(stage));
+      return;
+    }
+  }
+  const int slice = blockIdx.x / n_tiles;
   int id = blockIdx.x % n_tiles;
   {
     const int per = n_tiles >> 3, rest = n_tiles & 7, xcd = id & 7;
@@ -534,16 +595,18 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
 #pragma unroll
       for (int n = 0; n < kLoadsX + kLoadsW; ++n) load(n, k, buf, ft);
     } else {
+      const bool whole = k + kStep <= k_end;
+      auto one = [&](uint4& to, const void* base, int64_t row, int col, int64_t span) {
+        const T* m = static_cast<const T*>(base);
+        const Frag<T> f = whole ? load_frag<T>(m + row + col) : load_cut<T>(m, row + col, span, k_end - col);
+        __builtin_memcpy(&to, &f.v, 16);
+      };
 #pragma unroll
-      for (int i = 0; i < kLoadsX; ++i) {
-        const Frag<T> f = load_frag<T>(reinterpret_cast<const T*>(xb) + row_x(ft, i) * a.x_stride, k + chunk_x * kPer, k_end);
-        __builtin_memcpy(&hold[i], &f.v, 16);
-      }
+      for (int i = 0; i < kLoadsX; ++i)
+        one(hold[i], a.x, (r0 + row_x(ft, i)) * a.x_stride, k + chunk_x * kPer, span_x(a));
 #pragma unroll
-      for (int i = 0; i < kLoadsW; ++i) {
-        const Frag<T> f = load_frag<T>(reinterpret_cast<const T*>(wb) + row_w(ft, i) * a.weight_stride, k + chunk_w * kPer, k_end);
-        __builtin_memcpy(&hold[kLoadsX + i], &f.v, 16);
-      }
+      for (int i = 0; i < kLoadsW; ++i)
+        one(hold[kLoadsX + i], a.weight, (o0 + row_w(ft, i)) * a.weight_stride, k + chunk_w * kPer, span_w(a));
     }
   };
   // ends a fetch: its data is this wave's own until it has arrived in LDS
@@ -641,8 +704,9 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
     bool wild = false;
 #pragma unroll
     for (int i = 0; i < kLoadsW; ++i) {
-      const Frag<T> u = load_frag<T>(static_cast<const T*>(a.up) + (static_cast<int64_t>(cur) * a.O + o0 + row_w(ft, i)) * a.R,
-                                     cur_col + (chunk_w & (kSplit - 1)) * kPer, cur_rank);
+      const int col = cur_col + (chunk_w & (kSplit - 1)) * kPer;
+      const Frag<T> u = load_cut<T>(static_cast<const T*>(a.up), (static_cast<int64_t>(cur) * a.O + o0 + row_w(ft, i)) * a.R + col,
+                                    span_up(a), cur_rank - col);
       T e[kPer];
       __builtin_memcpy(e, &u.v, 16);
 #pragma unroll
