@@ -166,112 +166,788 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Prompts, token by token: a workgroup walks one sequence for 64 channels of one head; thread
-// (p, quarter) holds a quarter of the state row of channel p.
+// Prompts. With a_q = step_q decay (in units of log 2), s_i the sum of a over a block's tokens up to i
+// and S the state before the block, a block of up to 64 tokens is matrix products:
+//
+//   y_i = sum_{j <= i} (C_i B_j^T) 2^(s_i - s_j) step_j x_j  +  2^(s_i) S C_i  + skip x_i
+//   S'  = 2^(s_last) S + sum_j 2^(s_last - s_j) step_j x_j B_j^T
+//
+// k_scan_blocks forms, once for all heads of a group, what they share: the convolved B and C, C B^T
+// and, by head, the steps and sums s. k_scan_heads walks the blocks of a piece of a sequence for 64
+// channels of one head, with S in its registers. Where sequences times heads leave compute units
+// idle, sequences are cut into pieces: a first run of k_scan_heads forms each piece's own state from
+// zero (without y), and in the second run a piece starts from its predecessors' states, each faded
+// by the pieces behind it. This reads x twice but leaves no state in memory but one a piece.
+//
+// Products run on the matrix cores in half precision (11 bits), operands scaled by a power of two of
+// the block so that their largest magnitude is below 2^14: for bf16 tensors one product for y (its
+// operands' rounding, 2^-12, is far below y's own, 2^-9), and for the state, which is float32, operands
+// in two halves each (22 bits) and three products. float32 tensors take every operand in two halves.
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void scan_bounds(const ScanArgs& a, int i, int64_t& first, int64_t& len) {
-  if (!a.offsets) {
-    len = a.n_tokens / a.n_seqs;
-    first = i * len;
-    return;
-  }
-  first = min(max(static_cast<int64_t>(a.offsets[i]), int64_t(0)), a.n_tokens);
-  len = max(min(static_cast<int64_t>(a.offsets[i + 1]), a.n_tokens) - first, int64_t(0));
+constexpr int kScanBlock = 64;
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+
+__device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// A power of two that brings magnitudes of at most `most` below 2^14; its inverse is a float as well.
+__device__ __forceinline__ float scan_scale(float most) {
+  const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
+  return __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+}
+__device__ __forceinline__ float scan_unscale(float scale) {
+  return __uint_as_float((254u << 23) - __float_as_uint(scale));
+}
+// v in two halves. v is pinned as one float first: left to itself the compiler may convert a product to hi
+// exactly in one place and from its rounded value in another, and near a tie the two differ.
+__device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) {
+  asm("" : "+v"(v));
+  hi = static_cast<_Float16>(v);
+  lo = static_cast<_Float16>(v - static_cast<float>(hi));
 }
 
-template <class T>
-__device__ __forceinline__ float scan_conv(const ScanArgs& a, int c, int64_t first, int64_t t, int pos, const T* ring) {
-  const T* w = static_cast<const T*>(a.conv_weight) + static_cast<int64_t>(c) * a.W;
-  float u = a.conv_bias ? to_float(static_cast<const T*>(a.conv_bias)[c]) : 0.f;
-  for (int j = 0; j < a.W; ++j) {
-    const int64_t back = t - (a.W - 1 - j);
-    if (back >= 0)
-      u += to_float(w[j]) * to_float(static_cast<const T*>(a.xbc)[(first + back) * a.xbc_stride + c]);
-    else if (ring && pos + back >= 0)
-      u += to_float(w[j]) * to_float(ring[((pos + back) % a.W) * a.C + c]);
+// What k_scan_blocks leaves for a block and group: matrix-core operands, 16 bytes a lane.
+//   cb     [strip 4][step 2][lane][8] float: C_i B_j^T, i = 16 strip + lane % 16, j = 32 step + 8 (lane / 16) + e
+//   c      [strip 4][kN / 32][lane][8] half: C_i, columns 32 step + 8 (lane / 16) + e; then the low halves (float32)
+//   b      [tile kN / 16][step 2][lane][8] half: B_j at column 16 tile + lane % 16; then the low halves
+//   scale  float4: the scales of c and of b, the largest |cb|, the largest |B|
+template <int kN, bool kSplit>
+struct ScanBlock {
+  static constexpr int kCb = 4 * 2 * 64 * 8 * 4;
+  static constexpr int kC = 4 * (kN / 32) * 64 * 16;
+  static constexpr int kB = (kN / 16) * 2 * 64 * 16;
+  static constexpr int kOffC = kCb, kOffB = kOffC + kC * (kSplit ? 2 : 1), kOffScale = kOffB + 2 * kB;
+  static constexpr int kBytes = kOffScale + 256;
+};
+
+struct ScanWork {  // the workspace
+  char* blocks;      // [block][group]
+  float4* steps;     // [block][head][64]: step, s, the rest of s below float32, 2^(s_last - s) step
+  float4* totals;    // [block][head]: s_last, largest step, largest and sum of 2^(s_last - s) step
+  int32_t* slots;    // [sequence]: scan_slot
+  int32_t* counts;   // blocks and pieces in all
+  int2* start;       // [sequence]: its first block, its first piece
+  int2* bounds;      // [sequence]: its first row, its rows
+  int2* block_of;    // [block]: sequence, number in it
+  int2* piece_of;    // [piece]: sequence, number in it
+  float* states;     // [piece][head][tile]: a piece's own state (the last piece's place: the sequence's start)
+  float* fades;      // [piece][head]: the sum of a over a piece
+  int piece_blocks;  // blocks of a piece
+  int max_blocks, max_pieces;
+};
+
+__host__ __device__ __forceinline__ int scan_blocks_of(int64_t len) { return len > kScanBlock ? static_cast<int>((len + kScanBlock - 1) / kScanBlock) : 1; }
+
+// One sequence of a call: rows, blocks and pieces, and where the latter two start.
+struct ScanSeq {
+  int64_t first;
+  int len, blocks, pieces, block0, piece0;
+};
+
+// Without offsets all sequences are equally long and everything follows by division; with offsets
+// k_scan_map has worked it out.
+__device__ __forceinline__ ScanSeq scan_seq(const ScanArgs& a, const ScanWork& w, int i) {
+  ScanSeq q;
+  int2 start;
+  if (a.offsets) {
+    const int2 b = w.bounds[i];
+    start = w.start[i];
+    q.first = b.x;
+    q.len = b.y;
+  } else {
+    q.len = static_cast<int>(a.n_tokens / a.n_seqs);
+    q.first = static_cast<int64_t>(i) * q.len;
   }
-  return silu(u);
+  q.blocks = scan_blocks_of(q.len);
+  q.pieces = (q.blocks + w.piece_blocks - 1) / w.piece_blocks;
+  q.block0 = a.offsets ? start.x : i * q.blocks;
+  q.piece0 = a.offsets ? start.y : i * q.pieces;
+  return q;
 }
 
-template <class T, int kQuarter>
-__global__ __launch_bounds__(256) void k_scan_walk(ScanArgs a) {
-  __shared__ float sx[64], sb[kScanMaxState], sc[kScanMaxState];
-  const int tid = threadIdx.x;
-  const int tile = blockIdx.x % a.ptiles, h = (blockIdx.x / a.ptiles) % a.H, i = blockIdx.x / (a.ptiles * a.H);
-  const int slot = a.ssm_in ? scan_slot(a, i) : -1;
-  int64_t first, len;
-  scan_bounds(a, i, first, len);
-  const int p0 = tile * 64, np = min(64, a.P - p0), p = tid >> 2, n0 = (tid & 3) * kQuarter, N = a.N;
-  T* y = static_cast<T*>(a.y) + static_cast<int64_t>(h) * a.P + p0;
-  if (slot == -2) {
-    for (int64_t t = 0; t < len; ++t)
-      if (tid < np) y[(first + t) * a.y_stride + tid] = from_float<T>(__builtin_nanf(""));
-    return;
-  }
-  const int pos = (slot >= 0 && a.positions) ? max(a.positions[i], 0) : 0;
-  const T* ring = slot >= 0 ? static_cast<const T*>(a.conv_in) + static_cast<int64_t>(slot) * a.W * a.C : nullptr;
-  const int64_t sbase = ((static_cast<int64_t>(max(slot, 0)) * a.H + h) * a.P + p0 + p) * N;
-  float st[kQuarter];
+// Which sequence block (or piece) `id` belongs to, and which it is of it; x = -1 past the last.
+__device__ __forceinline__ int2 scan_find(const ScanArgs& a, const ScanWork& w, int id, bool piece) {
+  if (a.offsets) return id < w.counts[piece] ? (piece ? w.piece_of : w.block_of)[id] : make_int2(-1, 0);
+  const int blocks = scan_blocks_of(a.n_tokens / a.n_seqs);
+  const int each = piece ? (blocks + w.piece_blocks - 1) / w.piece_blocks : blocks;
+  const int i = id / each;
+  return i < a.n_seqs ? make_int2(i, id - i * each) : make_int2(-1, 0);
+}
+
+// Ragged sequences: bounds (offsets clamped into [0, n_tokens] and into a rising row), where blocks and
+// pieces start, and whose each of them is. One workgroup; 1,024 sequences at a time.
+static __global__ __launch_bounds__(1024) void k_scan_map(ScanArgs a, ScanWork w) {
+  __shared__ int scan[3][16];
+  __shared__ int seq_blocks[1024], seq_pieces[1024], seq_block0[1024], seq_piece0[1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto clamped = [&](int i) { return min(max(a.offsets[i], 0), static_cast<int>(a.n_tokens)); };
+  int most = clamped(0), blocks = 0, pieces = 0;  // largest offset, blocks and pieces so far
+  for (int i0 = 0; i0 < a.n_seqs; i0 += 1024) {
+    const int i = i0 + tid;
+    const bool ok = i < a.n_seqs;
+    // running maximum of offsets[i + 1]
+    int end = ok ? clamped(i + 1) : 0;
 #pragma unroll
-  for (int n = 0; n < kQuarter; ++n) st[n] = (pos > 0 && p < np && n0 + n < N) ? a.ssm_in[sbase + n0 + n] : 0.f;
-  const int g = h / (a.H / a.G);
-  for (int64_t t = 0; t < len; ++t) {
-    __syncthreads();
-    for (int idx = tid; idx < np + 2 * N; idx += 256) {
-      const int c = idx < np ? h * a.P + p0 + idx
-                             : (idx < np + N ? a.H * a.P + g * N + idx - np : a.H * a.P + a.G * N + g * N + idx - np - N);
-      const float u = scan_conv<T>(a, c, first, t, pos, ring);
-      if (idx < np)
-        sx[idx] = u;
-      else if (idx < np + N)
-        sb[idx - np] = u;
-      else
-        sc[idx - np - N] = u;
+    for (int m = 1; m < 64; m <<= 1) {
+      const int o = __shfl_up(end, m);
+      if (lane >= m) end = max(end, o);
     }
-    const float dt = softplus(to_float(static_cast<const T*>(a.dt)[(first + t) * a.dt_stride + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f));
-    const float fade = expf(dt * a.decay[h]);
+    if (lane == 63) scan[0][wave] = end;
     __syncthreads();
-    const float x = p < np ? sx[p] : 0.f;
-    float sum = 0.f;
+    int before = most;  // the largest offset before this wave's
+    for (int v = 0; v < wave; ++v) before = max(before, scan[0][v]);
+    int first = __shfl_up(end, 1);
+    first = lane == 0 ? before : max(before, first);
+    end = max(before, end);
+    for (int v = 0; v < 16; ++v) most = max(most, scan[0][v]);
+    const int len = ok ? end - first : 0, nb = ok ? scan_blocks_of(len) : 0;
+    const int np = (nb + w.piece_blocks - 1) / w.piece_blocks;
+    int sb = nb, sp = np;  // running sums
 #pragma unroll
-    for (int n = 0; n < kQuarter; ++n)
-      if (n0 + n < N) {
-        st[n] = st[n] * fade + dt * x * sb[n0 + n];
-        sum += st[n] * sc[n0 + n];
+    for (int m = 1; m < 64; m <<= 1) {
+      const int ob = __shfl_up(sb, m), op = __shfl_up(sp, m);
+      if (lane >= m) {
+        sb += ob;
+        sp += op;
       }
-    sum += __shfl_xor(sum, 1);
-    sum += __shfl_xor(sum, 2);
-    if ((tid & 3) == 0 && p < np) {
-      float v = sum + (a.skip ? a.skip[h] * x : 0.f);
-      if (a.z) v *= silu(to_float(static_cast<const T*>(a.z)[(first + t) * a.z_stride + static_cast<int64_t>(h) * a.P + p0 + p]));
-      y[(first + t) * a.y_stride + p] = from_float<T>(v);
+    }
+    if (lane == 63) {
+      scan[1][wave] = sb;
+      scan[2][wave] = sp;
+    }
+    __syncthreads();
+    int b0 = blocks + sb - nb, p0 = pieces + sp - np;
+    for (int v = 0; v < 16; ++v) {
+      if (v < wave) {
+        b0 += scan[1][v];
+        p0 += scan[2][v];
+      }
+      blocks += scan[1][v];
+      pieces += scan[2][v];
+    }
+    if (ok) {
+      w.bounds[i] = make_int2(first, len);
+      w.start[i] = make_int2(b0, p0);
+    }
+    seq_blocks[tid] = nb;
+    seq_pieces[tid] = np;
+    seq_block0[tid] = b0;
+    seq_piece0[tid] = p0;
+    __syncthreads();
+    for (int t = wave; t < min(1024, a.n_seqs - i0); t += 16) {
+      for (int n = lane; n < seq_blocks[t]; n += 64) w.block_of[seq_block0[t] + n] = make_int2(i0 + t, n);
+      for (int n = lane; n < seq_pieces[t]; n += 64) w.piece_of[seq_piece0[t] + n] = make_int2(i0 + t, n);
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    w.counts[0] = blocks;
+    w.counts[1] = pieces;
+  }
+}
+
+// Eight columns n0 .. n0 + 7 of a row of u as an operand, and its low half.
+__device__ __forceinline__ void scan_operand(const float* row, float scale, f16x8& hi, f16x8& lo) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = *reinterpret_cast<const float2*>(row + e);
+    _Float16 h[2], l[2];
+    split_half(v.x * scale, h[0], l[0]);
+    split_half(v.y * scale, h[1], l[1]);
+    hi[e] = h[0];
+    hi[e + 1] = h[1];
+    lo[e] = l[0];
+    lo[e + 1] = l[1];
+  }
+}
+
+// What a block's heads share, one workgroup a block and group. kN: state_dim rounded up to 32, 64, 128 or 256.
+template <class T, int kN, bool kSplit>
+__global__ __launch_bounds__(256) void k_scan_blocks(ScanArgs a, ScanWork w) {
+  using Block = ScanBlock<kN, kSplit>;
+  constexpr int kCols = 2 * kN, kRow = kCols + 2;  // a row's pad: eight rows on lies 16 banks on
+  extern __shared__ float u[];                     // [64][kRow]: the convolved B, then C
+  __shared__ float red[3][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int block = blockIdx.x / a.G, g = blockIdx.x % a.G;
+  const int2 at = scan_find(a, w, block, false);
+  if (at.x < 0) return;
+  const ScanSeq sq = scan_seq(a, w, at.x);
+  const int64_t row0 = sq.first + static_cast<int64_t>(at.y) * kScanBlock;
+  const int L = min(kScanBlock, sq.len - at.y * kScanBlock);  // zero for a sequence without rows
+  int slot = -1, pos = 0;
+  if (a.ssm_in) {
+    slot = scan_slot(a, at.x);
+    if (slot >= 0 && a.positions) pos = max(a.positions[at.x], 0);
+    if (at.y == 0 && g == 0 && tid == 0) w.slots[at.x] = slot;
+  }
+
+  // convolution: a thread takes one column of B or C and an equal share of the block's tokens
+  float most_b = 0.f, most_c = 0.f;
+  {
+    constexpr int kParts = kCols < 256 ? 256 / kCols : 1, kTokens = kScanBlock / kParts;
+    const int part = kCols < 256 ? tid / kCols : 0, t0 = part * kTokens;
+    const T* const ring = (slot >= 0 && at.y == 0) ? static_cast<const T*>(a.conv_in) + static_cast<int64_t>(slot) * a.W * a.C : nullptr;
+    for (int col = kCols < 256 ? tid % kCols : tid; col < kCols; col += 256) {
+      const int n = col < kN ? col : col - kN;
+      if (n >= a.N || L <= 0) {
+        for (int t = t0; t < t0 + kTokens; ++t) u[t * kRow + col] = 0.f;
+        continue;
+      }
+      const int c = a.H * a.P + (col < kN ? 0 : a.G * a.N) + g * a.N + n;
+      const T* const x = static_cast<const T*>(a.xbc) + row0 * a.xbc_stride + c;
+      float cw[kScanMaxConv];  // the newest token's weight last
+#pragma unroll
+      for (int j = 0; j < kScanMaxConv; ++j)
+        cw[j] = j >= kScanMaxConv - a.W ? to_float(static_cast<const T*>(a.conv_weight)[static_cast<int64_t>(c) * a.W + j - (kScanMaxConv - a.W)]) : 0.f;
+      const float cb = a.conv_bias ? to_float(static_cast<const T*>(a.conv_bias)[c]) : 0.f;
+      float past[3];  // tokens t - 3, t - 2, t - 1
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int t = t0 - 3 + j;
+        past[j] = 0.f;
+        if (3 - j < a.W) {
+          if (t >= 0 || at.y > 0)
+            past[j] = t < L ? to_float(x[static_cast<int64_t>(t) * a.xbc_stride]) : 0.f;
+          else if (ring && pos + t >= 0)
+            past[j] = to_float(ring[static_cast<int64_t>((pos + t) % a.W) * a.C + c]);
+        }
+      }
+      for (int t = t0; t < t0 + kTokens; t += 8) {
+        float now[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) now[e] = to_float(x[static_cast<int64_t>(min(t + e, L - 1)) * a.xbc_stride]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // a tap past the width is left out, not multiplied by zero: its token may be anything
+          float v = cb + cw[3] * now[e] + cw[2] * past[2];
+          if (a.W > 2) v += cw[1] * past[1];
+          if (a.W > 3) v += cw[0] * past[0];
+          past[0] = past[1];
+          past[1] = past[2];
+          past[2] = now[e];
+          v = t + e < L ? silu(v) : 0.f;
+          u[(t + e) * kRow + col] = v;
+          if (col < kN)
+            most_b = fmaxf(most_b, fabsf(v));
+          else
+            most_c = fmaxf(most_c, fabsf(v));
+        }
+      }
     }
   }
-  if (slot >= 0 && p < np) {
+  most_b = wave_max(most_b);
+  most_c = wave_max(most_c);
+  if (lane == 0) {
+    red[0][wave] = most_b;
+    red[1][wave] = most_c;
+  }
+  __syncthreads();
+  most_b = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  most_c = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+  const float fb = scan_scale(most_b), fc = scan_scale(most_c);
+  char* const out = w.blocks + (static_cast<int64_t>(block) * a.G + g) * Block::kBytes;
+
+  // C B^T: wave i takes the strip of tokens 16 i ..; the columns of x that come with it are this strip's C
+  float most_cb = 0.f;
+  if (16 * wave < L) {
+    f16x8 ch[kN / 32], cl[kN / 32];
 #pragma unroll
-    for (int n = 0; n < kQuarter; ++n)
-      if (n0 + n < N) a.ssm_out[sbase + n0 + n] = st[n];
+    for (int k = 0; k < kN / 32; ++k) {
+      scan_operand(u + (16 * wave + l16) * kRow + kN + 32 * k + 8 * q, fc, ch[k], cl[k]);
+      if (at.y > 0 || pos > 0) {
+        f16x8* const to = reinterpret_cast<f16x8*>(out + Block::kOffC) + (wave * (kN / 32) + k) * 64 + lane;
+        to[0] = ch[k];
+        if (kSplit) to[4 * (kN / 32) * 64] = cl[k];
+      }
+    }
+    for (int step = 0; step <= wave >> 1; ++step) {
+      f32x4 acc[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int j = 32 * step + 8 * (l16 >> 2) + 4 * t + (l16 & 3);
+#pragma unroll
+        for (int k = 0; k < kN / 32; ++k) {
+          f16x8 bh, bl;
+          scan_operand(u + j * kRow + 32 * k + 8 * q, fb, bh, bl);
+          acc[t] = mma16(bh, ch[k], acc[t]);
+          acc[t] = mma16(bh, cl[k], acc[t]);
+          acc[t] = mma16(bl, ch[k], acc[t]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[t][e] = acc[t][e] * scan_unscale(fb) * scan_unscale(fc);
+          if (32 * step + 8 * q + 4 * t + e <= 16 * wave + l16) most_cb = fmaxf(most_cb, fabsf(acc[t][e]));
+        }
+      }
+      f32x4* const to = reinterpret_cast<f32x4*>(out) + ((wave * 2 + step) * 64 + lane) * 2;
+      to[0] = acc[0];
+      to[1] = acc[1];
+    }
+  }
+  most_cb = wave_max(most_cb);
+  if (lane == 0) red[2][wave] = most_cb;
+
+  // B by column, for the state
+  if (slot >= 0 || at.y < sq.blocks - 1) {
+    for (int f = wave; f < (kN / 16) * 2; f += 4) {
+      const int tile = f >> 1, step = f & 1;
+      if (32 * step >= L) continue;
+      f16x8 bh, bl;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = u[(32 * step + 8 * q + e) * kRow + 16 * tile + l16] * fb;
+        _Float16 vh, vl;
+        split_half(v, vh, vl);
+        bh[e] = vh;
+        bl[e] = vl;
+      }
+      f16x8* const to = reinterpret_cast<f16x8*>(out + Block::kOffB) + f * 64 + lane;
+      to[0] = bh;
+      to[(kN / 16) * 2 * 64] = bl;
+    }
+  }
+
+  // steps and decays of the group's heads, a wave a head
+  for (int n = wave; n < a.H / a.G; n += 4) {
+    const int h = g * (a.H / a.G) + n;
+    float step = 0.f;
+    if (lane < L)
+      step = softplus(to_float(static_cast<const T*>(a.dt)[(row0 + lane) * a.dt_stride + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f));
+    double sum = static_cast<double>(step) * static_cast<double>(a.decay[h]) * 1.4426950408889634;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(sum, m);
+      if (lane >= m) sum += o;
+    }
+    const double last = __shfl(sum, 63);
+    const float s = static_cast<float>(sum), rest = static_cast<float>(sum - static_cast<double>(s));
+    const float left = lane < L ? step * __builtin_amdgcn_exp2f(static_cast<float>(last - sum)) : 0.f;
+    const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
+    w.steps[at_head * 64 + lane] = make_float4(step, s, rest, left);
+    const float most_step = wave_max(step), most_left = wave_max(left), all_left = wave_sum(left);
+    if (lane == 0) w.totals[at_head] = make_float4(static_cast<float>(last), most_step, most_left, all_left);
+  }
+  __syncthreads();
+  if (tid == 0)
+    *reinterpret_cast<float4*>(out + Block::kOffScale) =
+        make_float4(fc, fb, fmaxf(fmaxf(red[2][0], red[2][1]), fmaxf(red[2][2], red[2][3])), most_b);
+}
+
+// LDS rows of 16-byte chunks, chunk c of row p at place c ^ f(p): the eight rows that a matrix-core read
+// touches at a time (four neighbours, and those 16 on) take different places, and so do stores down the rows.
+__device__ __forceinline__ int scan_place(int p) { return ((p ^ (p >> 2)) & 3) | ((p >> 2) & 4); }
+
+// The blocks of a piece for 64 channels of a head (see above). first_run: only the piece's own state, for
+// pieces that have a successor. Lane (l16, q) of wave i holds the state at columns 16 tile + 4 q + e and
+// channel 16 m + l16, the tiles shared among the waves, and y at token 16 i + l16 and channels 16 q + 4 m + e.
+template <class T, int kN, bool kSplit>
+__global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, int first_run) {
+  using Block = ScanBlock<kN, kSplit>;
+  constexpr int kTiles = kN / 16 >= 4 ? kN / 64 : 1;  // column tiles of a wave
+  constexpr int kCh = kN / 16 >= 4 ? 4 : 2;           // channel tiles of a wave
+  constexpr int kHalves = kSplit ? 2 : 1;
+  __shared__ _Float16 xt[kHalves][64 * 64], xw[2][64 * 64], hs[kHalves][64 * kN];  // by channel: x, faded x, state
+  __shared__ float tokens[2][4][64], red[4];  // by token, for this block and the next: s, its rest, step, faded step
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
+
+  // workgroups go round the eight XCDs: the heads of a piece, which share its blocks' operands, stay on one
+  int id = blockIdx.x;
+  {
+    const int n = gridDim.x, per = n >> 3, rest = n & 7, xcd = id & 7;
+    id = xcd * per + min(xcd, rest) + (id >> 3);
+  }
+  const int tile = id % a.ptiles, h = id / a.ptiles % a.H, piece = id / (a.ptiles * a.H);
+  const int2 at = scan_find(a, w, piece, true);
+  if (at.x < 0) return;
+  const ScanSeq sq = scan_seq(a, w, at.x);
+  const bool last_piece = at.y == sq.pieces - 1;
+  if (first_run && last_piece) return;
+  const int slot = a.ssm_in ? w.slots[at.x] : -1;
+  const int p0 = tile * 64, np = min(64, a.P - p0), g = h / (a.H / a.G);
+  T* const y = static_cast<T*>(a.y) + static_cast<int64_t>(h) * a.P + p0;
+  const int nb0 = at.y * w.piece_blocks, nb1 = min(sq.blocks, nb0 + w.piece_blocks);
+  if (slot == -2) {
+    if (!first_run)
+      for (int64_t t = static_cast<int64_t>(nb0) * 64 + (tid >> 6); t < min(static_cast<int64_t>(nb1) * 64, static_cast<int64_t>(sq.len)); t += 4)
+        if (lane < np) y[(sq.first + t) * a.y_stride + lane] = from_float<T>(__builtin_nanf(""));
+    return;
+  }
+  const int pos = (slot >= 0 && a.positions) ? max(a.positions[at.x], 0) : 0;
+
+  // the state before the piece
+  f32x4 st[kTiles][kCh];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int m = 0; m < kCh; ++m) st[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // a stored state of a piece, as the lanes hold it
+  auto stored = [&](int which, int t, int m) {
+    const int64_t tiles = static_cast<int64_t>(kTiles) * kCh;
+    return reinterpret_cast<f32x4*>(w.states) +
+           (((static_cast<int64_t>(which) * a.H + h) * a.ptiles + tile) * 4 + wave) * tiles * 64 + (t * kCh + m) * 64 + lane;
+  };
+  const int64_t sbase = ((static_cast<int64_t>(max(slot, 0)) * a.H + h) * a.P + p0) * a.N;
+  bool has = false;
+  if (at.y > 0) {
+    if (!first_run) {
+      has = true;
+      for (int k = 0; k < at.y; ++k) {
+        const float fade = k ? __builtin_amdgcn_exp2f(w.fades[static_cast<int64_t>(sq.piece0 + k) * a.H + h]) : 0.f;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int m = 0; m < kCh; ++m) {
+            const f32x4 v = *stored(sq.piece0 + k, t, m);
+            st[t][m] = k ? st[t][m] * fade + v : v;
+          }
+      }
+    }
+  } else if (pos > 0) {
+    has = true;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int m = 0; m < kCh; ++m) {
+        const int n = 16 * (tile0 + t) + 4 * q, p = 16 * (ch0 + m) + l16;
+        if (!first_run && sq.pieces > 1) {
+          // a later piece may have updated the slot in place already
+          st[t][m] = *stored(sq.piece0 + sq.pieces - 1, t, m);
+        } else if (p < np) {
+          const float* const s = a.ssm_in + sbase + static_cast<int64_t>(p) * a.N + n;
+          if (a.N % 4 == 0) {
+            if (n < a.N) st[t][m] = *reinterpret_cast<const f32x4*>(s);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < a.N) st[t][m][e] = s[e];
+          }
+        }
+        if (first_run) *stored(sq.piece0 + sq.pieces - 1, t, m) = st[t][m];
+      }
+  }
+  float most_state = 0.f;  // bounds the state's magnitudes
+  if (has) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int m = 0; m < kCh; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most_state = fmaxf(most_state, fabsf(st[t][m][e]));
+    most_state = wave_max(most_state);
+    if (lane == 0) red[wave] = most_state;
+    __syncthreads();
+    most_state = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    __syncthreads();
+  }
+
+  // convolution of x: thread (tid / 16, tid % 16) takes four tokens of four channels
+  const int pc = (tid & 15) * 4, tg = (tid >> 4) * 4, c0 = h * a.P + p0 + pc;
+  float cw[4][kScanMaxConv], cb[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const bool ok = pc + c < np;
+    cb[c] = ok && a.conv_bias ? to_float(static_cast<const T*>(a.conv_bias)[c0 + c]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kScanMaxConv; ++j)
+      cw[c][j] = ok && j >= kScanMaxConv - a.W
+                     ? to_float(static_cast<const T*>(a.conv_weight)[static_cast<int64_t>(c0 + c) * a.W + j - (kScanMaxConv - a.W)])
+                     : 0.f;
+  }
+  T raw[7][4];  // tokens tg - 3 .. tg + 3 of the block
+  auto load_raw = [&](int nth) {
+    const int L = min(kScanBlock, sq.len - nth * kScanBlock);
+    const T* const x = static_cast<const T*>(a.xbc) + (sq.first + static_cast<int64_t>(nth) * kScanBlock) * a.xbc_stride + c0;
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      const int t = tg - 3 + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) raw[r][c] = T(0);
+      if (r < 4 - a.W || t >= L) continue;
+      const T* from = x + static_cast<int64_t>(t) * a.xbc_stride;
+      if (t < 0 && nth == 0) {
+        if (slot < 0 || pos + t < 0) continue;
+        from = static_cast<const T*>(a.conv_in) + (static_cast<int64_t>(slot) * a.W + (pos + t) % a.W) * a.C + c0;
+      }
+      if (pc + 4 <= np) {
+        __builtin_memcpy(raw[r], from, sizeof(raw[r]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (pc + c < np) raw[r][c] = from[c];
+      }
+    }
+  };
+
+  const float skip = a.skip ? a.skip[h] : 0.f;
+  double faded = 0.0;
+  load_raw(nb0);
+  for (int nth = nb0; nth < nb1; ++nth) {
+    const int block = sq.block0 + nth, L = min(kScanBlock, sq.len - nth * kScanBlock);
+    if (L <= 0) break;  // a sequence without rows
+    const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
+    const char* const in = w.blocks + (static_cast<int64_t>(block) * a.G + g) * Block::kBytes;
+    const bool keep = slot >= 0 || nth < sq.blocks - 1;  // whether anybody wants the state behind the block
+    float* const ts = tokens[nth & 1][0];
+    float* const tl = tokens[nth & 1][1];
+    float* const td = tokens[nth & 1][2];
+    float* const tw = tokens[nth & 1][3];
+    if (wave == 0) {
+      const float4 v = w.steps[at_head * 64 + lane];
+      td[lane] = v.x;
+      ts[lane] = v.y;
+      tl[lane] = v.z;
+      tw[lane] = v.w;
+    }
+    const float4 total = w.totals[at_head], scale = *reinterpret_cast<const float4*>(in + Block::kOffScale);
+    float u[4][4], most = 0.f;  // [token][channel]
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // a tap past the width is left out, not multiplied by zero: its token may be anything
+        float v = cb[c] + cw[c][3] * to_float(raw[t + 3][c]) + cw[c][2] * to_float(raw[t + 2][c]);
+        if (a.W > 2) v += cw[c][1] * to_float(raw[t + 1][c]);
+        if (a.W > 3) v += cw[c][0] * to_float(raw[t][c]);
+        u[t][c] = (tg + t < L && pc + c < np) ? silu(v) : 0.f;
+        most = fmaxf(most, fabsf(u[t][c]));
+      }
+    most = wave_max(most);
+    if (lane == 0) red[wave] = most;
+    __syncthreads();  // every wave is past the block before: its operands may be overwritten
+    most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float fx = scan_scale(most), fw = scan_scale(most * total.z), fh = scan_scale(most_state);
+    {
+      const float4 left = *reinterpret_cast<const float4*>(tw + tg);
+      const float l4[4] = {left.x * fw, left.y * fw, left.z * fw, left.w * fw};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int p = pc + c, to = p * 64 + (((tg >> 3) ^ scan_place(p)) << 3) + (tg & 7);
+        f16x4 hi, lo, wh, wl;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          _Float16 vh, vl;
+          split_half(u[t][c] * fx, vh, vl);
+          hi[t] = vh;
+          lo[t] = vl;
+          split_half(u[t][c] * l4[t], vh, vl);
+          wh[t] = vh;
+          wl[t] = vl;
+        }
+        if (!first_run) {
+          *reinterpret_cast<f16x4*>(&xt[0][to]) = hi;
+          if (kSplit) *reinterpret_cast<f16x4*>(&xt[kHalves - 1][to]) = lo;
+        }
+        if (keep) {
+          *reinterpret_cast<f16x4*>(&xw[0][to]) = wh;
+          *reinterpret_cast<f16x4*>(&xw[1][to]) = wl;
+        }
+      }
+    }
+    if (has && !first_run) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < kCh; ++m) {
+          const int p = 16 * (ch0 + m) + l16, chunk = 2 * (tile0 + t) + (q >> 1);
+          const int to = p * kN + ((chunk ^ (scan_place(p) & (kN / 8 - 1))) << 3) + 4 * (q & 1);
+          f16x4 hi, lo;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            _Float16 vh, vl;
+            split_half(st[t][m][e] * fh, vh, vl);
+            hi[e] = vh;
+            lo[e] = vl;
+          }
+          *reinterpret_cast<f16x4*>(&hs[0][to]) = hi;
+          if (kSplit) *reinterpret_cast<f16x4*>(&hs[kHalves - 1][to]) = lo;
+        }
+    }
+    __syncthreads();
+    if (nth + 1 < nb1) load_raw(nth + 1);
+
+    if (!first_run && 16 * wave < L) {
+      const int i = 16 * wave + l16;  // the lane's token
+      const float si = ts[i], li = tl[i];
+      f32x4 far[4], near[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) far[m] = near[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (has) {
+        const f16x8* const cf = reinterpret_cast<const f16x8*>(in + Block::kOffC) + wave * (kN / 32) * 64 + lane;
+#pragma unroll
+        for (int k = 0; k < kN / 32; ++k) {
+          const f16x8 ch = cf[k * 64];
+          f16x8 cl;
+          if (kSplit) cl = cf[(4 * (kN / 32) + k) * 64];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3);
+            const int from = p * kN + (((4 * k + q) ^ (scan_place(p) & (kN / 8 - 1))) << 3);
+            const f16x8 hh = *reinterpret_cast<const f16x8*>(&hs[0][from]);
+            far[m] = mma16(hh, ch, far[m]);
+            if (kSplit) {
+              far[m] = mma16(hh, cl, far[m]);
+              far[m] = mma16(*reinterpret_cast<const f16x8*>(&hs[kHalves - 1][from]), ch, far[m]);
+            }
+          }
+        }
+      }
+      const float most_mix = fmaxf(scale.z * total.y * __builtin_amdgcn_exp2f(fmaxf(total.x, 0.f)), fabsf(skip));
+      const float fm = scan_scale(most_mix);
+      for (int step = 0; step <= wave >> 1; ++step) {
+        const f32x4* const cbf = reinterpret_cast<const f32x4*>(in) + ((wave * 2 + step) * 64 + lane) * 2;
+        const f32x4 c01[2] = {cbf[0], cbf[1]};
+        f16x8 mh, ml;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int j0 = 32 * step + 8 * q + 4 * half;
+          const f32x4 sj = *reinterpret_cast<const f32x4*>(ts + j0), lj = *reinterpret_cast<const f32x4*>(tl + j0),
+                      dj = *reinterpret_cast<const f32x4*>(td + j0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + e;
+            float v = c01[half][e] * (dj[e] * fm) * __builtin_amdgcn_exp2f((si - sj[e]) + (li - lj[e]));
+            v = j < i ? v : (j == i ? v + skip * fm : 0.f);
+            _Float16 vh, vl;
+            split_half(v, vh, vl);
+            mh[4 * half + e] = vh;
+            if (kSplit) ml[4 * half + e] = vl;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3);
+          const int from = p * 64 + (((4 * step + q) ^ scan_place(p)) << 3);
+          const f16x8 xh = *reinterpret_cast<const f16x8*>(&xt[0][from]);
+          near[m] = mma16(xh, mh, near[m]);
+          if (kSplit) {
+            near[m] = mma16(xh, ml, near[m]);
+            near[m] = mma16(*reinterpret_cast<const f16x8*>(&xt[kHalves - 1][from]), mh, near[m]);
+          }
+        }
+      }
+      if (i < L) {
+        const float es = __builtin_amdgcn_exp2f(si) * scan_unscale(scale.x), uh = scan_unscale(fh);
+        const float um = scan_unscale(fm), ux = scan_unscale(fx);
+        const int64_t row = sq.first + static_cast<int64_t>(nth) * kScanBlock + i;
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          v[k] = near[k >> 2][k & 3] * um * ux;
+          if (has) v[k] += far[k >> 2][k & 3] * es * uh;
+        }
+        const int p = 16 * q;
+        if (a.z) {
+          const T* const z = static_cast<const T*>(a.z) + row * a.z_stride + static_cast<int64_t>(h) * a.P + p0 + p;
+          if (p + 16 <= np) {
+            T zv[16];
+            __builtin_memcpy(zv, z, sizeof(zv));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] *= silu(to_float(zv[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (p + k < np) v[k] *= silu(to_float(z[k]));
+          }
+        }
+        T o[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = from_float<T>(v[k]);
+        T* const to = y + row * a.y_stride + p;
+        if (p + 16 <= np) {
+          __builtin_memcpy(to, o, sizeof(o));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (p + k < np) to[k] = o[k];
+        }
+      }
+    }
+
+    if (keep) {
+      const float fade = __builtin_amdgcn_exp2f(total.x), uw = scan_unscale(fw), ub = scan_unscale(scale.y);
+      const f16x8* const bf = reinterpret_cast<const f16x8*>(in + Block::kOffB) + lane;
+      f32x4 add[kTiles][kCh];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < kCh; ++m) add[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int step = 0; 32 * step < L; ++step) {
+        f16x8 wh[kCh], wl[kCh];
+#pragma unroll
+        for (int m = 0; m < kCh; ++m) {
+          const int p = 16 * (ch0 + m) + l16, from = p * 64 + (((4 * step + q) ^ scan_place(p)) << 3);
+          wh[m] = *reinterpret_cast<const f16x8*>(&xw[0][from]);
+          wl[m] = *reinterpret_cast<const f16x8*>(&xw[1][from]);
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const f16x8 bh = bf[((tile0 + t) * 2 + step) * 64], bl = bf[((kN / 16 + tile0 + t) * 2 + step) * 64];
+#pragma unroll
+          for (int m = 0; m < kCh; ++m) {
+            add[t][m] = mma16(bh, wh[m], add[t][m]);
+            add[t][m] = mma16(bh, wl[m], add[t][m]);
+            add[t][m] = mma16(bl, wh[m], add[t][m]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int m = 0; m < kCh; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st[t][m][e] = st[t][m][e] * fade + add[t][m][e] * uw * ub;
+      most_state = most_state * fade + scale.w * most * total.w;
+      faded += static_cast<double>(total.x);
+      has = true;
+    }
+  }
+
+  if (first_run) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int m = 0; m < kCh; ++m) *stored(piece, t, m) = st[t][m];
+    if (tid == 0) w.fades[static_cast<int64_t>(piece) * a.H + h] = static_cast<float>(faded);
+  } else if (last_piece && slot >= 0) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int m = 0; m < kCh; ++m) {
+        const int n = 16 * (tile0 + t) + 4 * q, p = 16 * (ch0 + m) + l16;
+        if (p >= np) continue;
+        float* const s = a.ssm_out + sbase + static_cast<int64_t>(p) * a.N + n;
+        if (a.N % 4 == 0) {
+          if (n < a.N) *reinterpret_cast<f32x4*>(s) = st[t][m];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) s[e] = st[t][m][e];
+        }
+      }
   }
 }
 
 // The rings after a prompt call, a launch of its own: in place, every reader of the old rings is
 // done. grid: (channel blocks of 256, sequences).
 template <class T>
-__global__ __launch_bounds__(256) void k_scan_ring(ScanArgs a, int cblocks) {
+__global__ __launch_bounds__(256) void k_scan_ring(ScanArgs a, ScanWork w, int cblocks) {
   const int i = blockIdx.x / cblocks, c = (blockIdx.x % cblocks) * 256 + threadIdx.x;
-  const int slot = scan_slot(a, i);
+  const int slot = w.slots[i];
   if (slot < 0 || c >= a.C) return;
-  int64_t first, len;
-  scan_bounds(a, i, first, len);
+  const ScanSeq sq = scan_seq(a, w, i);
   const int pos = a.positions ? max(a.positions[i], 0) : 0;
   const T* ring = static_cast<const T*>(a.conv_in) + static_cast<int64_t>(slot) * a.W * a.C + c;
   T* out = static_cast<T*>(a.conv_out) + static_cast<int64_t>(slot) * a.W * a.C + c;
   for (int e = 0; e < a.W; ++e) {
     // the newest of this call's tokens whose place is e modulo W
-    const int64_t last = pos + len - 1;
+    const int64_t last = static_cast<int64_t>(pos) + sq.len - 1;
     const int64_t q = last - (((last - e) % a.W) + a.W) % a.W;
     if (q >= pos)
-      out[static_cast<int64_t>(e) * a.C] = static_cast<const T*>(a.xbc)[(first + q - pos) * a.xbc_stride + c];
+      out[static_cast<int64_t>(e) * a.C] = static_cast<const T*>(a.xbc)[(sq.first + q - pos) * a.xbc_stride + c];
     else if (a.conv_in != a.conv_out)
       out[static_cast<int64_t>(e) * a.C] = ring[static_cast<int64_t>(e) * a.C];
   }

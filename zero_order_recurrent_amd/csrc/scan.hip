@@ -1,6 +1,9 @@
 // Host side of cdrge_scan_prompt and cdrge_scan_step (include/cdrge.h).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "cdrge.h"
 #include "host_common.h"
 #include "kernels_scan.h"
@@ -104,27 +107,137 @@ cdrge_status enqueue_step(const ScanArgs& a, hipStream_t s) {
   return launch_step<T, 64, 8>(a, s);
 }
 
-template <class T, int kQuarter>
-cdrge_status launch_walk(ScanArgs a, hipStream_t s) {
-  a.ptiles = (a.P + 63) / 64;
-  const int64_t n = int64_t(a.n_seqs) * a.H * a.ptiles;
-  if (n > kMostBlocks) return CDRGE_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((k_scan_walk<T, kQuarter>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, a);
+// How a prompt call is cut up and where its workspace's parts lie; by sizes alone.
+struct Plan {
+  int kn;  // state_dim as the kernels have it
+  int ptiles, max_blocks, max_pieces, piece_blocks;
+  size_t blocks, steps, totals, slots, counts, start, bounds, block_of, piece_of, states, fades, total;
+};
+
+constexpr int kPieceWorkgroups = 512;  // two for each of 256 compute units
+
+size_t block_bytes(int kn, bool split) {
+  switch (kn) {
+    case 32: return split ? ScanBlock<32, true>::kBytes : ScanBlock<32, false>::kBytes;
+    case 64: return split ? ScanBlock<64, true>::kBytes : ScanBlock<64, false>::kBytes;
+    case 128: return split ? ScanBlock<128, true>::kBytes : ScanBlock<128, false>::kBytes;
+    default: return split ? ScanBlock<256, true>::kBytes : ScanBlock<256, false>::kBytes;
+  }
+}
+
+// Whether a sequence may have more than one piece.
+bool cut(const Plan& p, int64_t n_tokens, int32_t n_seqs, bool equal) {
+  return scan_blocks_of(equal ? n_tokens / n_seqs : n_tokens) > p.piece_blocks;
+}
+
+// equal: every sequence has n_tokens / n_seqs rows.
+Plan make_plan(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs, bool equal) {
+  Plan p{};
+  p.kn = c->state_dim <= 32 ? 32 : (c->state_dim <= 64 ? 64 : (c->state_dim <= 128 ? 128 : 256));
+  p.ptiles = (c->head_dim + 63) / 64;
+  const int64_t blocks = equal ? int64_t(n_seqs) * scan_blocks_of(n_tokens / n_seqs) : n_tokens / kScanBlock + n_seqs;
+  p.max_blocks = static_cast<int>(blocks);
+  const int64_t share = blocks * c->n_heads * p.ptiles / kPieceWorkgroups;
+  p.piece_blocks = static_cast<int>(std::max<int64_t>(4, share));
+  const int64_t pieces = equal ? int64_t(n_seqs) * ((scan_blocks_of(n_tokens / n_seqs) + p.piece_blocks - 1) / p.piece_blocks)
+                               : blocks / p.piece_blocks + n_seqs;
+  p.max_pieces = static_cast<int>(pieces);
+  size_t at = 0;
+  auto region = [&](size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes);
+    return here;
+  };
+  p.blocks = region(block_bytes(p.kn, c->dtype == CDRGE_F32) * blocks * c->n_groups);
+  p.steps = region(sizeof(float4) * 64 * blocks * c->n_heads);
+  p.totals = region(sizeof(float4) * blocks * c->n_heads);
+  p.slots = region(sizeof(int32_t) * n_seqs);
+  if (!equal) {
+    p.counts = region(2 * sizeof(int32_t));
+    p.start = region(sizeof(int2) * n_seqs);
+    p.bounds = region(sizeof(int2) * n_seqs);
+    p.block_of = region(sizeof(int2) * blocks);
+    p.piece_of = region(sizeof(int2) * pieces);
+  }
+  if (cut(p, n_tokens, n_seqs, equal)) {
+    p.states = region(sizeof(float) * 64 * p.kn * p.ptiles * c->n_heads * pieces);
+    p.fades = region(sizeof(float) * c->n_heads * pieces);
+  }
+  p.total = at;
+  return p;
+}
+
+ScanWork make_work(const Plan& p, void* ws) {
+  char* const at = static_cast<char*>(ws);
+  ScanWork w;
+  w.blocks = at + p.blocks;
+  w.steps = reinterpret_cast<float4*>(at + p.steps);
+  w.totals = reinterpret_cast<float4*>(at + p.totals);
+  w.slots = reinterpret_cast<int32_t*>(at + p.slots);
+  w.counts = reinterpret_cast<int32_t*>(at + p.counts);
+  w.start = reinterpret_cast<int2*>(at + p.start);
+  w.bounds = reinterpret_cast<int2*>(at + p.bounds);
+  w.block_of = reinterpret_cast<int2*>(at + p.block_of);
+  w.piece_of = reinterpret_cast<int2*>(at + p.piece_of);
+  w.states = reinterpret_cast<float*>(at + p.states);
+  w.fades = reinterpret_cast<float*>(at + p.fades);
+  w.piece_blocks = p.piece_blocks;
+  w.max_blocks = p.max_blocks;
+  w.max_pieces = p.max_pieces;
+  return w;
+}
+
+template <class T, int kN>
+cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pieces, hipStream_t s) {
+  constexpr bool kSplit = sizeof(T) == 4;
+  a.ptiles = p.ptiles;
+  if (a.offsets) {
+    hipLaunchKernelGGL(k_scan_map, dim3(1), dim3(1024), 0, s, a, w);
+    CDRGE_HIP(hipGetLastError());
+  }
+  constexpr size_t kLds = sizeof(float) * kScanBlock * (2 * kN + 2);
+  if (kLds > 64 * 1024) {
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use this much LDS
+    int dev = 0;
+    CDRGE_HIP(hipGetDevice(&dev));
+    if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+      CDRGE_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k_scan_blocks<T, kN, kSplit>),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
+      ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
+    }
+  }
+  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), dim3(static_cast<uint32_t>(int64_t(p.max_blocks) * a.G)), dim3(256), kLds, s, a, w);
+  CDRGE_HIP(hipGetLastError());
+  const dim3 grid(static_cast<uint32_t>(int64_t(p.max_pieces) * a.H * p.ptiles));
+  if (pieces) {
+    hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit>), grid, dim3(256), 0, s, a, w, 1);
+    CDRGE_HIP(hipGetLastError());
+  }
+  hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit>), grid, dim3(256), 0, s, a, w, 0);
   CDRGE_HIP(hipGetLastError());
   if (a.conv_in) {
     const int cblocks = (a.C + 255) / 256;
-    hipLaunchKernelGGL(k_scan_ring<T>, dim3(static_cast<uint32_t>(a.n_seqs) * cblocks), dim3(256), 0, s, a, cblocks);
+    hipLaunchKernelGGL(k_scan_ring<T>, dim3(static_cast<uint32_t>(int64_t(a.n_seqs) * cblocks)), dim3(256), 0, s, a, w, cblocks);
     CDRGE_HIP(hipGetLastError());
   }
   return CDRGE_OK;
 }
 
 template <class T>
-cdrge_status enqueue_prompt(const ScanArgs& a, hipStream_t s) {
-  if (a.N <= 16) return launch_walk<T, 4>(a, s);
-  if (a.N <= 64) return launch_walk<T, 16>(a, s);
-  if (a.N <= 128) return launch_walk<T, 32>(a, s);
-  return launch_walk<T, 64>(a, s);
+cdrge_status enqueue_prompt(const ScanArgs& a, const Plan& p, const ScanWork& w, bool pieces, hipStream_t s) {
+  switch (p.kn) {
+    case 32: return launch_prompt<T, 32>(a, p, w, pieces, s);
+    case 64: return launch_prompt<T, 64>(a, p, w, pieces, s);
+    case 128: return launch_prompt<T, 128>(a, p, w, pieces, s);
+    default: return launch_prompt<T, 256>(a, p, w, pieces, s);
+  }
+}
+
+// Whether the call's sizes fit the kernels' 32-bit counts.
+bool fits(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs) {
+  const int64_t blocks = n_tokens / kScanBlock + n_seqs, ptiles = (c->head_dim + 63) / 64;
+  return n_tokens <= (int64_t(1) << 30) && n_seqs <= (1 << 20) && blocks * c->n_heads * ptiles <= kMostBlocks &&
+         int64_t(n_seqs) * ((channels(c) + 255) / 256) <= kMostBlocks;
 }
 
 }  // namespace
@@ -136,7 +249,10 @@ cdrge_status cdrge_scan_workspace_bytes(const cdrge_scan_config* cfg, int64_t n_
   if (!bytes_out || n_tokens < 0 || n_seqs < 1) return CDRGE_ERR_INVALID_ARG;
   const cdrge_status st = check_config(cfg);
   if (st != CDRGE_OK) return st;
-  *bytes_out = 256;
+  if (!fits(cfg, n_tokens, n_seqs)) return CDRGE_ERR_UNSUPPORTED;
+  // ragged sequences may take more blocks than equal ones, equal ones more pieces
+  *bytes_out = make_plan(cfg, n_tokens, n_seqs, false).total;
+  if (n_tokens % n_seqs == 0) *bytes_out = std::max(*bytes_out, make_plan(cfg, n_tokens, n_seqs, true).total);
   return CDRGE_OK;
 }
 
@@ -145,14 +261,19 @@ cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_we
   cdrge_status st = check_config(cfg);
   if (st == CDRGE_OK) st = check_io(cfg, weights, io);
   if (st != CDRGE_OK) return st;
+  if (!fits(cfg, io->n_tokens, io->n_seqs)) return CDRGE_ERR_UNSUPPORTED;
+  const bool equal = !io->offsets;
+  const Plan p = make_plan(cfg, io->n_tokens, io->n_seqs, equal);
   size_t need = 0;
   st = cdrge_scan_workspace_bytes(cfg, io->n_tokens, io->n_seqs, &need);
   if (st != CDRGE_OK) return st;
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0)
     return workspace_error("cdrge_scan_prompt", need, workspace ? workspace_bytes : 0);
   const ScanArgs a = make_args(cfg, weights, io);
+  const ScanWork w = make_work(p, workspace);
+  const bool pieces = cut(p, io->n_tokens, io->n_seqs, equal);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, s) : enqueue_prompt<uint16_t>(a, s);
+  return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, p, w, pieces, s) : enqueue_prompt<uint16_t>(a, p, w, pieces, s);
 }
 
 cdrge_status cdrge_scan_step(const cdrge_scan_config* cfg, const cdrge_scan_weights* weights,
