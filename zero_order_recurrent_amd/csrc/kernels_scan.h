@@ -362,20 +362,57 @@ __device__ __forceinline__ void scan_operand(const float* row, float scale, f16x
   }
 }
 
-// What a block's heads share, one workgroup a block and group. kN: state_dim rounded up to 32, 64, 128 or 256.
+// Steps and decays of a block's heads: a wave takes kScanHeads heads, lane = token, with the loads of all
+// of them in flight together.
+constexpr int kScanHeads = 2;
+template <class T>
+__device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w, int block, int64_t row0, int L, int h0, int h1) {
+  const int lane = threadIdx.x & 63;
+  float raw[kScanHeads];
+#pragma unroll
+  for (int n = 0; n < kScanHeads; ++n)
+    raw[n] = (lane < L && h0 + n < h1) ? to_float(static_cast<const T*>(a.dt)[(row0 + lane) * a.dt_stride + h0 + n]) : 0.f;
+#pragma unroll
+  for (int n = 0; n < kScanHeads; ++n) {
+    const int h = h0 + n;
+    if (h >= h1) break;
+    const float step = lane < L ? softplus(raw[n] + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
+    double sum = static_cast<double>(step) * static_cast<double>(a.decay[h]) * 1.4426950408889634;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(sum, m);
+      if (lane >= m) sum += o;
+    }
+    const double last = __shfl(sum, 63);
+    const float s = static_cast<float>(sum), rest = static_cast<float>(sum - static_cast<double>(s));
+    const float left = lane < L ? step * __builtin_amdgcn_exp2f(static_cast<float>(last - sum)) : 0.f;
+    const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
+    w.steps[at_head * 64 + lane] = make_float4(step, s, rest, left);
+    const float most_step = wave_max(step), most_left = wave_max(left), all_left = wave_sum(left);
+    if (lane == 0) w.totals[at_head] = make_float4(static_cast<float>(last), most_step, most_left, all_left);
+  }
+}
+
+// What a block's heads share: one workgroup of eight waves a block and group for B and C, and further ones
+// for the steps of kScanHeads * 8 heads each. kN: state_dim rounded up to 32, 64, 128 or 256.
 template <class T, int kN, bool kSplit>
-__global__ __launch_bounds__(256) void k_scan_blocks(ScanArgs a, ScanWork w) {
+__global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int parts) {
   using Block = ScanBlock<kN, kSplit>;
   constexpr int kCols = 2 * kN, kRow = kCols + 2;  // a row's pad: eight rows on lies 16 banks on
   extern __shared__ float u[];                     // [64][kRow]: the convolved B, then C
-  __shared__ float red[3][4];
+  __shared__ float red[3][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
-  const int block = blockIdx.x / a.G, g = blockIdx.x % a.G;
+  const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, block = blockIdx.x / (parts * a.G);
   const int2 at = scan_find(a, w, block, false);
   if (at.x < 0) return;
   const ScanSeq sq = scan_seq(a, w, at.x);
   const int64_t row0 = sq.first + static_cast<int64_t>(at.y) * kScanBlock;
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);  // zero for a sequence without rows
+  if (part > 0) {
+    const int each = a.H / a.G, n = ((part - 1) * 8 + wave) * kScanHeads;
+    if (n < each) scan_steps<T>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
+    return;
+  }
   int slot = -1, pos = 0;
   if (a.ssm_in) {
     slot = scan_slot(a, at.x);
@@ -386,15 +423,13 @@ __global__ __launch_bounds__(256) void k_scan_blocks(ScanArgs a, ScanWork w) {
   // convolution: a thread takes one column of B or C and an equal share of the block's tokens
   float most_b = 0.f, most_c = 0.f;
   {
-    constexpr int kParts = kCols < 256 ? 256 / kCols : 1, kTokens = kScanBlock / kParts;
-    const int part = kCols < 256 ? tid / kCols : 0, t0 = part * kTokens;
+    constexpr int kParts = 512 / kCols, kTokens = kScanBlock / kParts;
+    const int col = tid % kCols, t0 = tid / kCols * kTokens;
     const T* const ring = (slot >= 0 && at.y == 0) ? static_cast<const T*>(a.conv_in) + static_cast<int64_t>(slot) * a.W * a.C : nullptr;
-    for (int col = kCols < 256 ? tid % kCols : tid; col < kCols; col += 256) {
-      const int n = col < kN ? col : col - kN;
-      if (n >= a.N || L <= 0) {
-        for (int t = t0; t < t0 + kTokens; ++t) u[t * kRow + col] = 0.f;
-        continue;
-      }
+    const int n = col < kN ? col : col - kN;
+    if (n >= a.N || L <= 0) {
+      for (int t = t0; t < t0 + kTokens; ++t) u[t * kRow + col] = 0.f;
+    } else {
       const int c = a.H * a.P + (col < kN ? 0 : a.G * a.N) + g * a.N + n;
       const T* const x = static_cast<const T*>(a.xbc) + row0 * a.xbc_stride + c;
       float cw[kScanMaxConv];  // the newest token's weight last
@@ -444,55 +479,57 @@ __global__ __launch_bounds__(256) void k_scan_blocks(ScanArgs a, ScanWork w) {
     red[1][wave] = most_c;
   }
   __syncthreads();
-  most_b = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  most_c = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    most_b = fmaxf(most_b, red[0][v]);
+    most_c = fmaxf(most_c, red[1][v]);
+  }
   const float fb = scan_scale(most_b), fc = scan_scale(most_c);
   char* const out = w.blocks + (static_cast<int64_t>(block) * a.G + g) * Block::kBytes;
 
-  // C B^T: wave i takes the strip of tokens 16 i ..; the columns of x that come with it are this strip's C
+  // C B^T: of the strips of tokens i (16 each) and steps of tokens j (32 each), the six that have j <= i
   float most_cb = 0.f;
-  if (16 * wave < L) {
+  const int strip = wave < 2 ? wave : (wave < 4 ? 2 : 3), step = wave < 2 ? 0 : wave & 1;
+  if (wave < 6 && 16 * strip < L) {
     f16x8 ch[kN / 32], cl[kN / 32];
 #pragma unroll
     for (int k = 0; k < kN / 32; ++k) {
-      scan_operand(u + (16 * wave + l16) * kRow + kN + 32 * k + 8 * q, fc, ch[k], cl[k]);
-      if (at.y > 0 || pos > 0) {
-        f16x8* const to = reinterpret_cast<f16x8*>(out + Block::kOffC) + (wave * (kN / 32) + k) * 64 + lane;
+      scan_operand(u + (16 * strip + l16) * kRow + kN + 32 * k + 8 * q, fc, ch[k], cl[k]);
+      if (step == 0 && (at.y > 0 || pos > 0)) {
+        f16x8* const to = reinterpret_cast<f16x8*>(out + Block::kOffC) + (strip * (kN / 32) + k) * 64 + lane;
         to[0] = ch[k];
         if (kSplit) to[4 * (kN / 32) * 64] = cl[k];
       }
     }
-    for (int step = 0; step <= wave >> 1; ++step) {
-      f32x4 acc[2];
+    f32x4 acc[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int j = 32 * step + 8 * (l16 >> 2) + 4 * t + (l16 & 3);
+    for (int t = 0; t < 2; ++t) {
+      acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int j = 32 * step + 8 * (l16 >> 2) + 4 * t + (l16 & 3);
 #pragma unroll
-        for (int k = 0; k < kN / 32; ++k) {
-          f16x8 bh, bl;
-          scan_operand(u + j * kRow + 32 * k + 8 * q, fb, bh, bl);
-          acc[t] = mma16(bh, ch[k], acc[t]);
-          acc[t] = mma16(bh, cl[k], acc[t]);
-          acc[t] = mma16(bl, ch[k], acc[t]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[t][e] = acc[t][e] * scan_unscale(fb) * scan_unscale(fc);
-          if (32 * step + 8 * q + 4 * t + e <= 16 * wave + l16) most_cb = fmaxf(most_cb, fabsf(acc[t][e]));
-        }
+      for (int k = 0; k < kN / 32; ++k) {
+        f16x8 bh, bl;
+        scan_operand(u + j * kRow + 32 * k + 8 * q, fb, bh, bl);
+        acc[t] = mma16(bh, ch[k], acc[t]);
+        acc[t] = mma16(bh, cl[k], acc[t]);
+        acc[t] = mma16(bl, ch[k], acc[t]);
       }
-      f32x4* const to = reinterpret_cast<f32x4*>(out) + ((wave * 2 + step) * 64 + lane) * 2;
-      to[0] = acc[0];
-      to[1] = acc[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[t][e] = acc[t][e] * scan_unscale(fb) * scan_unscale(fc);
+        if (32 * step + 8 * q + 4 * t + e <= 16 * strip + l16) most_cb = fmaxf(most_cb, fabsf(acc[t][e]));
+      }
     }
+    f32x4* const to = reinterpret_cast<f32x4*>(out) + ((strip * 2 + step) * 64 + lane) * 2;
+    to[0] = acc[0];
+    to[1] = acc[1];
   }
   most_cb = wave_max(most_cb);
   if (lane == 0) red[2][wave] = most_cb;
 
   // B by column, for the state
   if (slot >= 0 || at.y < sq.blocks - 1) {
-    for (int f = wave; f < (kN / 16) * 2; f += 4) {
+    for (int f = wave; f < (kN / 16) * 2; f += 8) {
       const int tile = f >> 1, step = f & 1;
       if (32 * step >= L) continue;
       f16x8 bh, bl;
@@ -510,47 +547,77 @@ __global__ __launch_bounds__(256) void k_scan_blocks(ScanArgs a, ScanWork w) {
     }
   }
 
-  // steps and decays of the group's heads, a wave a head
-  for (int n = wave; n < a.H / a.G; n += 4) {
-    const int h = g * (a.H / a.G) + n;
-    float step = 0.f;
-    if (lane < L)
-      step = softplus(to_float(static_cast<const T*>(a.dt)[(row0 + lane) * a.dt_stride + h]) + (a.dt_bias ? a.dt_bias[h] : 0.f));
-    double sum = static_cast<double>(step) * static_cast<double>(a.decay[h]) * 1.4426950408889634;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double o = __shfl_up(sum, m);
-      if (lane >= m) sum += o;
-    }
-    const double last = __shfl(sum, 63);
-    const float s = static_cast<float>(sum), rest = static_cast<float>(sum - static_cast<double>(s));
-    const float left = lane < L ? step * __builtin_amdgcn_exp2f(static_cast<float>(last - sum)) : 0.f;
-    const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
-    w.steps[at_head * 64 + lane] = make_float4(step, s, rest, left);
-    const float most_step = wave_max(step), most_left = wave_max(left), all_left = wave_sum(left);
-    if (lane == 0) w.totals[at_head] = make_float4(static_cast<float>(last), most_step, most_left, all_left);
-  }
   __syncthreads();
   if (tid == 0)
     *reinterpret_cast<float4*>(out + Block::kOffScale) =
-        make_float4(fc, fb, fmaxf(fmaxf(red[2][0], red[2][1]), fmaxf(red[2][2], red[2][3])), most_b);
+        make_float4(fc, fb, fmaxf(fmaxf(fmaxf(red[2][0], red[2][1]), fmaxf(red[2][2], red[2][3])), fmaxf(red[2][4], red[2][5])), most_b);
 }
+
+// Four adjacent elements as they lie in memory.
+template <class T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void load(const float* from, int n) {  // n: how many there are
+    if (n >= 4) {
+      __builtin_memcpy(&v, from, 16);
+    } else {
+      if (n > 0) v.x = from[0];
+      if (n > 1) v.y = from[1];
+      if (n > 2) v.z = from[2];
+    }
+  }
+  __device__ __forceinline__ void load_back(const float* from, int n) {  // two to four, the last in the last place
+    v.w = from[n - 1];
+    v.z = from[n - 2];
+    if (n > 2) v.y = from[n - 3];
+    if (n > 3) v.x = from[0];
+  }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
+};
+template <>
+struct Four<uint16_t> {
+  uint2 v = make_uint2(0u, 0u);
+  __device__ __forceinline__ void load(const uint16_t* from, int n) {
+    if (n >= 4) {
+      __builtin_memcpy(&v, from, 8);
+    } else {
+      if (n > 0) v.x = from[0];
+      if (n > 1) v.x |= static_cast<uint32_t>(from[1]) << 16;
+      if (n > 2) v.y = from[2];
+    }
+  }
+  __device__ __forceinline__ void load_back(const uint16_t* from, int n) {
+    v.y = from[n - 2] | static_cast<uint32_t>(from[n - 1]) << 16;
+    if (n > 2) v.x = static_cast<uint32_t>(from[n - 3]) << 16;
+    if (n > 3) v.x |= from[0];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
 
 // LDS rows of 16-byte chunks, chunk c of row p at place c ^ f(p): the eight rows that a matrix-core read
 // touches at a time (four neighbours, and those 16 on) take different places, and so do stores down the rows.
 __device__ __forceinline__ int scan_place(int p) { return ((p ^ (p >> 2)) & 3) | ((p >> 2) & 4); }
 
-// The blocks of a piece for 64 channels of a head (see above). first_run: only the piece's own state, for
+// The blocks of a piece for 64 channels of a head (see above). kFirstRun: only the piece's own state, for
 // pieces that have a successor. Lane (l16, q) of wave i holds the state at columns 16 tile + 4 q + e and
 // channel 16 m + l16, the tiles shared among the waves, and y at token 16 i + l16 and channels 16 q + 4 m + e.
-template <class T, int kN, bool kSplit>
-__global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, int first_run) {
+// Loads are issued a phase or more before their use: a block's time is otherwise theirs, one after the other.
+template <class T, int kN, bool kSplit, bool kFirstRun>
+__global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
+  constexpr bool first_run = kFirstRun;
   using Block = ScanBlock<kN, kSplit>;
   constexpr int kTiles = kN / 16 >= 4 ? kN / 64 : 1;  // column tiles of a wave
   constexpr int kCh = kN / 16 >= 4 ? 4 : 2;           // channel tiles of a wave
   constexpr int kHalves = kSplit ? 2 : 1;
   __shared__ _Float16 xt[kHalves][64 * 64], xw[2][64 * 64], hs[kHalves][64 * kN];  // by channel: x, faded x, state
-  __shared__ float tokens[2][4][64], red[4];  // by token, for this block and the next: s, its rest, step, faded step
+  // by token, for this block and the next: s, its rest, step, faded step; totals and scales
+  __shared__ float tokens[2][4][64], red[4];
+  __shared__ float4 sums[2][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
 
@@ -645,73 +712,88 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
   }
 
   // convolution of x: thread (tid / 16, tid % 16) takes four tokens of four channels
-  const int pc = (tid & 15) * 4, tg = (tid >> 4) * 4, c0 = h * a.P + p0 + pc;
-  float cw[4][kScanMaxConv], cb[4];
+  const int pc = (tid & 15) * 4, tg = (tid >> 4) * 4;
+  Four<T> cw[4], cb;  // by channel: the taps, as many as there are; the biases
+  cb = Four<T>{};
+  if (a.conv_bias) cb.load(static_cast<const T*>(a.conv_bias) + h * a.P + p0 + pc, np - pc);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const bool ok = pc + c < np;
-    cb[c] = ok && a.conv_bias ? to_float(static_cast<const T*>(a.conv_bias)[c0 + c]) : 0.f;
-#pragma unroll
-    for (int j = 0; j < kScanMaxConv; ++j)
-      cw[c][j] = ok && j >= kScanMaxConv - a.W
-                     ? to_float(static_cast<const T*>(a.conv_weight)[static_cast<int64_t>(c0 + c) * a.W + j - (kScanMaxConv - a.W)])
-                     : 0.f;
+    cw[c] = Four<T>{};
+    if (pc + c < np) cw[c].load_back(static_cast<const T*>(a.conv_weight) + static_cast<int64_t>(h * a.P + p0 + pc + c) * a.W, a.W);
   }
-  T raw[7][4];  // tokens tg - 3 .. tg + 3 of the block
+  Four<T> raw[7];  // tokens tg - 3 .. tg + 3 of the block
   auto load_raw = [&](int nth) {
     const int L = min(kScanBlock, sq.len - nth * kScanBlock);
-    const T* const x = static_cast<const T*>(a.xbc) + (sq.first + static_cast<int64_t>(nth) * kScanBlock) * a.xbc_stride + c0;
+    // the thread's place as new values: addresses made of them are not kept from one block to the next
+    int t0 = tg - 3, c = pc;
+    asm volatile("" : "+v"(t0), "+v"(c));
+    const T* from = static_cast<const T*>(a.xbc) + (sq.first + static_cast<int64_t>(nth) * kScanBlock + t0) * a.xbc_stride + h * a.P + p0 + c;
 #pragma unroll
-    for (int r = 0; r < 7; ++r) {
-      const int t = tg - 3 + r;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) raw[r][c] = T(0);
-      if (r < 4 - a.W || t >= L) continue;
-      const T* from = x + static_cast<int64_t>(t) * a.xbc_stride;
-      if (t < 0 && nth == 0) {
-        if (slot < 0 || pos + t < 0) continue;
-        from = static_cast<const T*>(a.conv_in) + (static_cast<int64_t>(slot) * a.W + (pos + t) % a.W) * a.C + c0;
+    for (int r = 0; r < 7; ++r, from += a.xbc_stride) {
+      raw[r] = Four<T>{};
+      if (r < 4 - a.W || t0 + r >= L) continue;
+      const T* at_row = from;
+      if (t0 + r < 0 && nth == 0) {
+        if (slot < 0 || pos + t0 + r < 0) continue;
+        at_row = static_cast<const T*>(a.conv_in) + (static_cast<int64_t>(slot) * a.W + (pos + t0 + r) % a.W) * a.C + h * a.P + p0 + c;
       }
-      if (pc + 4 <= np) {
-        __builtin_memcpy(raw[r], from, sizeof(raw[r]));
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (pc + c < np) raw[r][c] = from[c];
-      }
+      raw[r].load(at_row, np - c);
     }
   };
 
   const float skip = a.skip ? a.skip[h] : 0.f;
   double faded = 0.0;
+  // a block's steps (wave 0, by token), totals and scales (wave 1)
+  float4 early = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto operands = [&](int nth) { return w.blocks + (static_cast<int64_t>(sq.block0 + nth) * a.G + g) * Block::kBytes; };
+  auto load_steps = [&](int nth) {
+    const int64_t at_head = static_cast<int64_t>(sq.block0 + nth) * a.H + h;
+    if (wave == 0) early = w.steps[at_head * 64 + lane];
+    if (wave == 1) early = *(lane == 0 ? w.totals + at_head : reinterpret_cast<const float4*>(operands(nth) + Block::kOffScale));
+  };
   load_raw(nb0);
+  load_steps(nb0);
   for (int nth = nb0; nth < nb1; ++nth) {
-    const int block = sq.block0 + nth, L = min(kScanBlock, sq.len - nth * kScanBlock);
+    const int L = min(kScanBlock, sq.len - nth * kScanBlock);
     if (L <= 0) break;  // a sequence without rows
-    const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
-    const char* const in = w.blocks + (static_cast<int64_t>(block) * a.G + g) * Block::kBytes;
+    const char* const in = operands(nth);
     const bool keep = slot >= 0 || nth < sq.blocks - 1;  // whether anybody wants the state behind the block
     float* const ts = tokens[nth & 1][0];
     float* const tl = tokens[nth & 1][1];
     float* const td = tokens[nth & 1][2];
     float* const tw = tokens[nth & 1][3];
     if (wave == 0) {
-      const float4 v = w.steps[at_head * 64 + lane];
-      td[lane] = v.x;
-      ts[lane] = v.y;
-      tl[lane] = v.z;
-      tw[lane] = v.w;
+      td[lane] = early.x;
+      ts[lane] = early.y;
+      tl[lane] = early.z;
+      tw[lane] = early.w;
     }
-    const float4 total = w.totals[at_head], scale = *reinterpret_cast<const float4*>(in + Block::kOffScale);
+    if (wave == 1 && lane < 2) sums[nth & 1][lane] = early;
+    // operands of y: C B^T (of a strip's first 16 (wave 0: 16, 1: 32, 2: 48, 3: 64) tokens) and C
+    f32x4 cbs[2][2];
+    f16x8 chs[kN / 32], cls[kSplit ? kN / 32 : 1];
+    if (!first_run) {
+      const f32x4* const cbf = reinterpret_cast<const f32x4*>(in) + (wave * 2 * 64 + lane) * 2;
+#pragma unroll
+      for (int step = 0; step < 2; ++step)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) cbs[step][half] = cbf[step * 128 + half];
+      const f16x8* const cf = reinterpret_cast<const f16x8*>(in + Block::kOffC) + wave * (kN / 32) * 64 + lane;
+#pragma unroll
+      for (int k = 0; k < kN / 32; ++k) {
+        chs[k] = cf[k * 64];
+        if (kSplit) cls[k] = cf[(4 * (kN / 32) + k) * 64];
+      }
+    }
     float u[4][4], most = 0.f;  // [token][channel]
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         // a tap past the width is left out, not multiplied by zero: its token may be anything
-        float v = cb[c] + cw[c][3] * to_float(raw[t + 3][c]) + cw[c][2] * to_float(raw[t + 2][c]);
-        if (a.W > 2) v += cw[c][1] * to_float(raw[t + 1][c]);
-        if (a.W > 3) v += cw[c][0] * to_float(raw[t][c]);
+        float v = cb.at(c) + cw[c].at(3) * raw[t + 3].at(c) + cw[c].at(2) * raw[t + 2].at(c);
+        if (a.W > 2) v += cw[c].at(1) * raw[t + 1].at(c);
+        if (a.W > 3) v += cw[c].at(0) * raw[t].at(c);
         u[t][c] = (tg + t < L && pc + c < np) ? silu(v) : 0.f;
         most = fmaxf(most, fabsf(u[t][c]));
       }
@@ -719,6 +801,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
     if (lane == 0) red[wave] = most;
     __syncthreads();  // every wave is past the block before: its operands may be overwritten
     most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float4 total = sums[nth & 1][0], scale = sums[nth & 1][1];
     const float fx = scan_scale(most), fw = scan_scale(most * total.z), fh = scan_scale(most_state);
     {
       const float4 left = *reinterpret_cast<const float4*>(tw + tg);
@@ -767,7 +850,24 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
         }
     }
     __syncthreads();
-    if (nth + 1 < nb1) load_raw(nth + 1);
+    if (nth + 1 < nb1) {
+      load_raw(nth + 1);
+      load_steps(nth + 1);
+    }
+    // operands of the state, first step
+    f16x8 bhs[2][kTiles], bls[2][kTiles];
+    auto load_b = [&](int step) {
+      const f16x8* const bf = reinterpret_cast<const f16x8*>(in + Block::kOffB) + lane;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        bhs[step][t] = bf[((tile0 + t) * 2 + step) * 64];
+        bls[step][t] = bf[((kN / 16 + tile0 + t) * 2 + step) * 64];
+      }
+    };
+    if (keep) {
+      load_b(0);
+      load_b(1);
+    }
 
     if (!first_run && 16 * wave < L) {
       const int i = 16 * wave + l16;  // the lane's token
@@ -776,12 +876,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
 #pragma unroll
       for (int m = 0; m < 4; ++m) far[m] = near[m] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (has) {
-        const f16x8* const cf = reinterpret_cast<const f16x8*>(in + Block::kOffC) + wave * (kN / 32) * 64 + lane;
 #pragma unroll
         for (int k = 0; k < kN / 32; ++k) {
-          const f16x8 ch = cf[k * 64];
-          f16x8 cl;
-          if (kSplit) cl = cf[(4 * (kN / 32) + k) * 64];
+          const f16x8 ch = chs[k], cl = cls[kSplit ? k : 0];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3);
@@ -797,9 +894,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
       }
       const float most_mix = fmaxf(scale.z * total.y * __builtin_amdgcn_exp2f(fmaxf(total.x, 0.f)), fabsf(skip));
       const float fm = scan_scale(most_mix);
-      for (int step = 0; step <= wave >> 1; ++step) {
-        const f32x4* const cbf = reinterpret_cast<const f32x4*>(in) + ((wave * 2 + step) * 64 + lane) * 2;
-        const f32x4 c01[2] = {cbf[0], cbf[1]};
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        if (step > wave >> 1) continue;
         f16x8 mh, ml;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -809,7 +906,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = j0 + e;
-            float v = c01[half][e] * (dj[e] * fm) * __builtin_amdgcn_exp2f((si - sj[e]) + (li - lj[e]));
+            float v = cbs[step][half][e] * (dj[e] * fm) * __builtin_amdgcn_exp2f((si - sj[e]) + (li - lj[e]));
             v = j < i ? v : (j == i ? v + skip * fm : 0.f);
             _Float16 vh, vl;
             split_half(v, vh, vl);
@@ -869,13 +966,14 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
 
     if (keep) {
       const float fade = __builtin_amdgcn_exp2f(total.x), uw = scan_unscale(fw), ub = scan_unscale(scale.y);
-      const f16x8* const bf = reinterpret_cast<const f16x8*>(in + Block::kOffB) + lane;
       f32x4 add[kTiles][kCh];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int m = 0; m < kCh; ++m) add[t][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int step = 0; 32 * step < L; ++step) {
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        if (32 * step >= L) continue;
         f16x8 wh[kCh], wl[kCh];
 #pragma unroll
         for (int m = 0; m < kCh; ++m) {
@@ -885,7 +983,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w, i
         }
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          const f16x8 bh = bf[((tile0 + t) * 2 + step) * 64], bl = bf[((kN / 16 + tile0 + t) * 2 + step) * 64];
+          const f16x8 bh = bhs[step][t], bl = bls[step][t];
 #pragma unroll
           for (int m = 0; m < kCh; ++m) {
             add[t][m] = mma16(bh, wh[m], add[t][m]);

@@ -206,14 +206,16 @@ cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pi
       ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), dim3(static_cast<uint32_t>(int64_t(p.max_blocks) * a.G)), dim3(256), kLds, s, a, w);
+  const int parts = 1 + (a.H / a.G + 8 * kScanHeads - 1) / (8 * kScanHeads);
+  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), dim3(static_cast<uint32_t>(int64_t(p.max_blocks) * a.G * parts)), dim3(512), kLds, s,
+                     a, w, parts);
   CDRGE_HIP(hipGetLastError());
   const dim3 grid(static_cast<uint32_t>(int64_t(p.max_pieces) * a.H * p.ptiles));
   if (pieces) {
-    hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit>), grid, dim3(256), 0, s, a, w, 1);
+    hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit, true>), grid, dim3(256), 0, s, a, w);
     CDRGE_HIP(hipGetLastError());
   }
-  hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit>), grid, dim3(256), 0, s, a, w, 0);
+  hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit, false>), grid, dim3(256), 0, s, a, w);
   CDRGE_HIP(hipGetLastError());
   if (a.conv_in) {
     const int cblocks = (a.C + 255) / 256;
@@ -236,7 +238,7 @@ cdrge_status enqueue_prompt(const ScanArgs& a, const Plan& p, const ScanWork& w,
 // Whether the call's sizes fit the kernels' 32-bit counts.
 bool fits(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs) {
   const int64_t blocks = n_tokens / kScanBlock + n_seqs, ptiles = (c->head_dim + 63) / 64;
-  return n_tokens <= (int64_t(1) << 30) && n_seqs <= (1 << 20) && blocks * c->n_heads * ptiles <= kMostBlocks &&
+  return n_tokens <= (int64_t(1) << 30) && n_seqs <= (1 << 20) && blocks * c->n_heads * (ptiles + 1) <= kMostBlocks &&
          int64_t(n_seqs) * ((channels(c) + 255) / 256) <= kMostBlocks;
 }
 
