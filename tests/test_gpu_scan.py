@@ -129,10 +129,21 @@ def test_prompt_equal_lengths_match_offsets():
     c = Case("bf16", 4, 64, 1, 64, 4, tokens=60, seqs=6)
     xbc, dt, z = c.rows()
     layer = c.layer()
-    a = layer.prompt(xbc, dt, c.y(), 6, z=z)
-    assert torch.equal(a, layer.prompt(xbc, dt, c.y(), 6, z=z, offsets=ints(list(range(0, 61, 10)))))
     want, mag, _ = c.expect([(i, i + 10) for i in range(0, 60, 10)])
-    close(c, a, want, mag)
+    close(c, layer.prompt(xbc, dt, c.y(), 6, z=z), want, mag)
+    # the two forms take different kernels, each within its bound of the definition: equal bits are not promised
+    close(c, layer.prompt(xbc, dt, c.y(), 6, z=z, offsets=ints(list(range(0, 61, 10)))), want, mag)
+
+
+@pytest.mark.parametrize("length", [1, 2, 10, 15, 16, 17])
+@pytest.mark.parametrize("shape", SHAPES + [("bf16", 40, 64, 2, 64, 4)])
+def test_prompt_equal_and_short(shape, length):
+    """Short equal sequences without a state, the forward pass of a population."""
+    c = Case(*shape, tokens=5 * length, seqs=5, seed=length, extra=1, gate=length % 2 == 0)
+    xbc, dt, z = c.rows()
+    y = c.layer().prompt(xbc, dt, c.y(), 5, z=z)
+    want, mag, _ = c.expect([(i * length, i * length + length) for i in range(5)])
+    close(c, y, want, mag)
 
 
 @pytest.mark.parametrize("dtype, heads, head_dim, state, tokens", [("bf16", 2, 64, 128, 1500), ("f32", 1, 48, 64, 1025), ("bf16", 1, 16, 16, 4100)])

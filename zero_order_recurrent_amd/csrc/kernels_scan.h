@@ -191,14 +191,12 @@ typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
 
 __device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// A power of two that brings magnitudes of at most `most` below 2^14; its inverse is a float as well.
-__device__ __forceinline__ float scan_scale(float most) {
-  const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
-  return __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+// The power of two that brings magnitudes of at most `most` below 2^14, as its exponent.
+__device__ __forceinline__ int scan_scale(float most) {
+  return 13 - min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -100), 100);
 }
-__device__ __forceinline__ float scan_unscale(float scale) {
-  return __uint_as_float((254u << 23) - __float_as_uint(scale));
-}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // |e| <= 126
+
 // v in two halves. v is pinned as one float first: left to itself the compiler may convert a product to hi
 // exactly in one place and from its rounded value in another, and near a tie the two differ.
 __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) {
@@ -211,7 +209,7 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
 //   cb     [strip 4][step 2][lane][8] float: C_i B_j^T, i = 16 strip + lane % 16, j = 32 step + 8 (lane / 16) + e
 //   c      [strip 4][kN / 32][lane][8] half: C_i, columns 32 step + 8 (lane / 16) + e; then the low halves (float32)
 //   b      [tile kN / 16][step 2][lane][8] half: B_j at column 16 tile + lane % 16; then the low halves
-//   scale  float4: the scales of c and of b, the largest |cb|, the largest |B|
+//   scale  float4: the scales of c and of b (exponents), the largest |cb|, the largest |B|
 template <int kN, bool kSplit>
 struct ScanBlock {
   static constexpr int kCb = 4 * 2 * 64 * 8 * 4;
@@ -223,7 +221,8 @@ struct ScanBlock {
 
 struct ScanWork {  // the workspace
   char* blocks;      // [block][group]
-  float4* steps;     // [block][head][64]: step, s, the rest of s below float32, 2^(s_last - s) step
+  float4* steps;     // [block][head][64]: s, r = s - log2(step), 2^(s_last - s) step, what s lacks below float32
+  float* rests;      // [block][head][64]: what r lacks below float32 (float32 tensors)
   float4* totals;    // [block][head]: s_last, largest step, largest and sum of 2^(s_last - s) step
   int32_t* slots;    // [sequence]: scan_slot
   int32_t* counts;   // blocks and pieces in all
@@ -365,7 +364,7 @@ __device__ __forceinline__ void scan_operand(const float* row, float scale, f16x
 // Steps and decays of a block's heads: a wave takes kScanHeads heads, lane = token, with the loads of all
 // of them in flight together.
 constexpr int kScanHeads = 2;
-template <class T>
+template <class T, bool kRest>
 __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w, int block, int64_t row0, int L, int h0, int h1) {
   const int lane = threadIdx.x & 63;
   float raw[kScanHeads];
@@ -384,10 +383,15 @@ __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w,
       if (lane >= m) sum += o;
     }
     const double last = __shfl(sum, 63);
-    const float s = static_cast<float>(sum), rest = static_cast<float>(sum - static_cast<double>(s));
+    // 2^(s_i - s_j) step_j is 2^(s_i - r_j), r = s - log2(step): infinite for a step of zero, which adds nothing
+    const float s = static_cast<float>(sum);
+    const double less = step > 0.f ? sum - log2(static_cast<double>(step)) : (step == step ? __builtin_inf() : static_cast<double>(step));
+    const float r = static_cast<float>(less);
+    const float rest_s = static_cast<float>(sum - static_cast<double>(s)), rest_r = fabsf(r) < 3e38f ? static_cast<float>(less - static_cast<double>(r)) : 0.f;
     const float left = lane < L ? step * __builtin_amdgcn_exp2f(static_cast<float>(last - sum)) : 0.f;
     const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
-    w.steps[at_head * 64 + lane] = make_float4(step, s, rest, left);
+    w.steps[at_head * 64 + lane] = make_float4(s, r, left, rest_s);
+    if (kRest) w.rests[at_head * 64 + lane] = rest_r;
     const float most_step = wave_max(step), most_left = wave_max(left), all_left = wave_sum(left);
     if (lane == 0) w.totals[at_head] = make_float4(static_cast<float>(last), most_step, most_left, all_left);
   }
@@ -410,7 +414,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);  // zero for a sequence without rows
   if (part > 0) {
     const int each = a.H / a.G, n = ((part - 1) * 8 + wave) * kScanHeads;
-    if (n < each) scan_steps<T>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
+    if (n < each) scan_steps<T, kSplit>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
     return;
   }
   int slot = -1, pos = 0;
@@ -484,7 +488,8 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
     most_b = fmaxf(most_b, red[0][v]);
     most_c = fmaxf(most_c, red[1][v]);
   }
-  const float fb = scan_scale(most_b), fc = scan_scale(most_c);
+  const int eb = scan_scale(most_b), ec = scan_scale(most_c);
+  const float fb = two_to(eb), fc = two_to(ec);
   char* const out = w.blocks + (static_cast<int64_t>(block) * a.G + g) * Block::kBytes;
 
   // C B^T: of the strips of tokens i (16 each) and steps of tokens j (32 each), the six that have j <= i
@@ -516,7 +521,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        acc[t][e] = acc[t][e] * scan_unscale(fb) * scan_unscale(fc);
+        acc[t][e] = ldexpf(acc[t][e], -eb - ec);
         if (32 * step + 8 * q + 4 * t + e <= 16 * strip + l16) most_cb = fmaxf(most_cb, fabsf(acc[t][e]));
       }
     }
@@ -550,7 +555,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   __syncthreads();
   if (tid == 0)
     *reinterpret_cast<float4*>(out + Block::kOffScale) =
-        make_float4(fc, fb, fmaxf(fmaxf(fmaxf(red[2][0], red[2][1]), fmaxf(red[2][2], red[2][3])), fmaxf(red[2][4], red[2][5])), most_b);
+        make_float4(__int_as_float(ec), __int_as_float(eb), fmaxf(fmaxf(fmaxf(red[2][0], red[2][1]), fmaxf(red[2][2], red[2][3])), fmaxf(red[2][4], red[2][5])), most_b);
 }
 
 // Four adjacent elements as they lie in memory.
@@ -615,8 +620,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   constexpr int kCh = kN / 16 >= 4 ? 4 : 2;           // channel tiles of a wave
   constexpr int kHalves = kSplit ? 2 : 1;
   __shared__ _Float16 xt[kHalves][64 * 64], xw[2][64 * 64], hs[kHalves][64 * kN];  // by channel: x, faded x, state
-  // by token, for this block and the next: s, its rest, step, faded step; totals and scales
-  __shared__ float tokens[2][4][64], red[4];
+  // by token, for this block and the next: s, r, faded step, and what s and r lack; totals and scales
+  __shared__ float tokens[2][kSplit ? 5 : 3][64], red[4];
   __shared__ float4 sums[2][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
@@ -745,10 +750,14 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   double faded = 0.0;
   // a block's steps (wave 0, by token), totals and scales (wave 1)
   float4 early = make_float4(0.f, 0.f, 0.f, 0.f);
+  float early_rest = 0.f;
   auto operands = [&](int nth) { return w.blocks + (static_cast<int64_t>(sq.block0 + nth) * a.G + g) * Block::kBytes; };
   auto load_steps = [&](int nth) {
     const int64_t at_head = static_cast<int64_t>(sq.block0 + nth) * a.H + h;
-    if (wave == 0) early = w.steps[at_head * 64 + lane];
+    if (wave == 0) {
+      early = w.steps[at_head * 64 + lane];
+      if (kSplit) early_rest = w.rests[at_head * 64 + lane];
+    }
     if (wave == 1) early = *(lane == 0 ? w.totals + at_head : reinterpret_cast<const float4*>(operands(nth) + Block::kOffScale));
   };
   load_raw(nb0);
@@ -759,14 +768,18 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     const char* const in = operands(nth);
     const bool keep = slot >= 0 || nth < sq.blocks - 1;  // whether anybody wants the state behind the block
     float* const ts = tokens[nth & 1][0];
-    float* const tl = tokens[nth & 1][1];
-    float* const td = tokens[nth & 1][2];
-    float* const tw = tokens[nth & 1][3];
+    float* const tr = tokens[nth & 1][1];
+    float* const tw = tokens[nth & 1][2];
+    float* const tl = tokens[nth & 1][kSplit ? 3 : 0];
+    float* const tq = tokens[nth & 1][kSplit ? 4 : 0];
     if (wave == 0) {
-      td[lane] = early.x;
-      ts[lane] = early.y;
-      tl[lane] = early.z;
-      tw[lane] = early.w;
+      ts[lane] = early.x;
+      tr[lane] = early.y;
+      tw[lane] = early.z;
+      if (kSplit) {
+        tl[lane] = early.w;
+        tq[lane] = early_rest;
+      }
     }
     if (wave == 1 && lane < 2) sums[nth & 1][lane] = early;
     // operands of y: C B^T (of a strip's first 16 (wave 0: 16, 1: 32, 2: 48, 3: 64) tokens) and C
@@ -802,8 +815,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     __syncthreads();  // every wave is past the block before: its operands may be overwritten
     most = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     const float4 total = sums[nth & 1][0], scale = sums[nth & 1][1];
-    const float fx = scan_scale(most), fw = scan_scale(most * total.z), fh = scan_scale(most_state);
+    const int ex = scan_scale(most), ew = scan_scale(most * total.z), eh = scan_scale(most_state);
     {
+      const float fx = two_to(ex), fw = two_to(ew);
       const float4 left = *reinterpret_cast<const float4*>(tw + tg);
       const float l4[4] = {left.x * fw, left.y * fw, left.z * fw, left.w * fw};
 #pragma unroll
@@ -831,6 +845,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
       }
     }
     if (has && !first_run) {
+      const float fh = two_to(eh);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -871,7 +886,19 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 
     if (!first_run && 16 * wave < L) {
       const int i = 16 * wave + l16;  // the lane's token
-      const float si = ts[i], li = tl[i];
+      // Where the operands of the lane's channels lie: chunk 4 k + q of row p at place (4 k + q) ^ f(p), for even k
+      // the first of two places and for odd k the second, moved on by whole rows of eight chunks.
+      int far_at[4][2], near_at[4][2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3), f = scan_place(p);
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+          near_at[m][odd] = p * 64 + (((4 * odd + q) ^ f) << 3);
+          far_at[m][odd] = p * kN + (((4 * odd + q) ^ (f & (kN / 8 - 1))) << 3);
+        }
+      }
+      const float si = ts[i], li = kSplit ? tl[i] : 0.f;
       f32x4 far[4], near[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) far[m] = near[m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -881,8 +908,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           const f16x8 ch = chs[k], cl = cls[kSplit ? k : 0];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3);
-            const int from = p * kN + (((4 * k + q) ^ (scan_place(p) & (kN / 8 - 1))) << 3);
+            const int from = far_at[m][k & 1] + (k >> 1) * 64;
             const f16x8 hh = *reinterpret_cast<const f16x8*>(&hs[0][from]);
             far[m] = mma16(hh, ch, far[m]);
             if (kSplit) {
@@ -893,7 +919,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         }
       }
       const float most_mix = fmaxf(scale.z * total.y * __builtin_amdgcn_exp2f(fmaxf(total.x, 0.f)), fabsf(skip));
-      const float fm = scan_scale(most_mix);
+      const int em = scan_scale(most_mix);
+      const float fm = two_to(em), own = skip * fm;
 #pragma unroll
       for (int step = 0; step < 2; ++step) {
         if (step > wave >> 1) continue;
@@ -901,13 +928,14 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int j0 = 32 * step + 8 * q + 4 * half;
-          const f32x4 sj = *reinterpret_cast<const f32x4*>(ts + j0), lj = *reinterpret_cast<const f32x4*>(tl + j0),
-                      dj = *reinterpret_cast<const f32x4*>(td + j0);
+          const f32x4 rj = *reinterpret_cast<const f32x4*>(tr + j0);
+          f32x4 qj = {0.f, 0.f, 0.f, 0.f};
+          if (kSplit) qj = *reinterpret_cast<const f32x4*>(tq + j0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int j = j0 + e;
-            float v = cbs[step][half][e] * (dj[e] * fm) * __builtin_amdgcn_exp2f((si - sj[e]) + (li - lj[e]));
-            v = j < i ? v : (j == i ? v + skip * fm : 0.f);
+            const float fall = kSplit ? (si - rj[e]) + (li - qj[e]) : si - rj[e];
+            float v = cbs[step][half][e] * fm * __builtin_amdgcn_exp2f(fall);
+            if (step == wave >> 1) v = j0 + e < i ? v : (j0 + e == i ? v + own : 0.f);  // tokens after i, and i itself
             _Float16 vh, vl;
             split_half(v, vh, vl);
             mh[4 * half + e] = vh;
@@ -916,8 +944,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3);
-          const int from = p * 64 + (((4 * step + q) ^ scan_place(p)) << 3);
+          const int from = near_at[m][step];
           const f16x8 xh = *reinterpret_cast<const f16x8*>(&xt[0][from]);
           near[m] = mma16(xh, mh, near[m]);
           if (kSplit) {
@@ -927,14 +954,13 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         }
       }
       if (i < L) {
-        const float es = __builtin_amdgcn_exp2f(si) * scan_unscale(scale.x), uh = scan_unscale(fh);
-        const float um = scan_unscale(fm), ux = scan_unscale(fx);
+        const float es = has ? ldexpf(__builtin_amdgcn_exp2f(si), -__float_as_int(scale.x) - eh) : 0.f;
         const int64_t row = sq.first + static_cast<int64_t>(nth) * kScanBlock + i;
         float v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          v[k] = near[k >> 2][k & 3] * um * ux;
-          if (has) v[k] += far[k >> 2][k & 3] * es * uh;
+          v[k] = ldexpf(near[k >> 2][k & 3], -em - ex);
+          if (has) v[k] += far[k >> 2][k & 3] * es;
         }
         const int p = 16 * q;
         if (a.z) {
@@ -965,7 +991,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     }
 
     if (keep) {
-      const float fade = __builtin_amdgcn_exp2f(total.x), uw = scan_unscale(fw), ub = scan_unscale(scale.y);
+      const float fade = __builtin_amdgcn_exp2f(total.x);
+      const int back = -ew - __float_as_int(scale.y);
       f32x4 add[kTiles][kCh];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
@@ -997,7 +1024,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 #pragma unroll
         for (int m = 0; m < kCh; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st[t][m][e] = st[t][m][e] * fade + add[t][m][e] * uw * ub;
+          for (int e = 0; e < 4; ++e) st[t][m][e] = st[t][m][e] * fade + ldexpf(add[t][m][e], back);
       most_state = most_state * fade + scale.w * most * total.w;
       faded += static_cast<double>(total.x);
       has = true;
@@ -1026,6 +1053,164 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
             if (n + e < a.N) s[e] = st[t][m][e];
         }
       }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Sequences of up to 16 rows each, all equally long, that carry no state: one launch, everything in
+// float32 on the matrix cores. A workgroup takes a sequence and group and up to kScanUnits (head, 64
+// channels); its four waves convolve B and C together and then take the units in turn. Bound by
+// latency and by the convolutions' and gates' exponentials. (1,024 sequences of 10 tokens, 16 heads of
+// 64, state 64, bf16: 210 us by blocks of 64 tokens.)
+// ---------------------------------------------------------------------------------------------
+constexpr int kScanShort = 16, kScanUnits = 16;
+
+template <class T, int kN>
+__global__ __launch_bounds__(256) void k_scan_short(ScanArgs a, int parts) {
+  constexpr int kCols = 2 * kN, kRow = kCols + 4;
+  __shared__ float u[kScanShort * kRow];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, i = blockIdx.x / (parts * a.G);
+  const int len = static_cast<int>(a.n_tokens / a.n_seqs), each = a.H / a.G;
+  const int64_t first = static_cast<int64_t>(i) * len;
+  const T* const xbc = static_cast<const T*>(a.xbc) + first * a.xbc_stride;
+
+  // a unit's loads: x at tokens 4 q - 3 .. 4 q + 3 and channels 4 l16 .. + 3, the taps and biases, the step
+  struct Unit {
+    Four<T> raw[7], cw[4], cb;
+    float dt, bias, decay, skip;
+    int h, p0, np;
+  };
+  const int units = each * a.ptiles, last = min(units, (part + 1) * kScanUnits);
+  auto load = [&](int n, Unit& v) {
+    v.h = g * each + n / a.ptiles;
+    v.p0 = n % a.ptiles * 64;
+    v.np = min(64, a.P - v.p0);
+    const int c0 = v.h * a.P + v.p0 + 4 * l16, ch = v.np - 4 * l16;
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      const int t = 4 * q - 3 + r;
+      v.raw[r] = Four<T>{};
+      if (r >= 4 - a.W && t >= 0 && t < len) v.raw[r].load(xbc + static_cast<int64_t>(t) * a.xbc_stride + c0, ch);
+    }
+    v.cb = Four<T>{};
+    if (a.conv_bias) v.cb.load(static_cast<const T*>(a.conv_bias) + c0, ch);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v.cw[c] = Four<T>{};
+      if (c < ch) v.cw[c].load_back(static_cast<const T*>(a.conv_weight) + static_cast<int64_t>(c0 + c) * a.W, a.W);
+    }
+    v.dt = l16 < len ? to_float(static_cast<const T*>(a.dt)[(first + l16) * a.dt_stride + v.h]) : 0.f;
+    v.bias = a.dt_bias ? a.dt_bias[v.h] : 0.f;
+    v.decay = a.decay[v.h];
+    v.skip = a.skip ? a.skip[v.h] : 0.f;
+  };
+  Unit now;
+  int n = part * kScanUnits + wave;
+  if (n < last) load(n, now);
+
+  {
+    constexpr int kParts = kCols < 256 ? 256 / kCols : 1, kTokens = kScanShort / kParts;
+    const int t0 = kCols < 256 ? tid / kCols * kTokens : 0;
+    for (int col = kCols < 256 ? tid % kCols : tid; col < kCols; col += 256) {
+      const int k = col < kN ? col : col - kN;
+      const int c = a.H * a.P + (col < kN ? 0 : a.G * a.N) + g * a.N + k;
+      float raw[kTokens + 3];
+#pragma unroll
+      for (int r = 0; r < kTokens + 3; ++r) {
+        const int t = t0 - 3 + r;
+        raw[r] = (k < a.N && r >= 4 - a.W && t >= 0 && t < len) ? to_float(xbc[static_cast<int64_t>(t) * a.xbc_stride + c]) : 0.f;
+      }
+      Four<T> cw;
+      float cb = 0.f;
+      if (k < a.N) {
+        cw.load_back(static_cast<const T*>(a.conv_weight) + static_cast<int64_t>(c) * a.W, a.W);
+        if (a.conv_bias) cb = to_float(static_cast<const T*>(a.conv_bias)[c]);
+      }
+#pragma unroll
+      for (int t = 0; t < kTokens; ++t) {
+        float v = cb + cw.at(3) * raw[t + 3] + cw.at(2) * raw[t + 2];
+        if (a.W > 2) v += cw.at(1) * raw[t + 1];
+        if (a.W > 3) v += cw.at(0) * raw[t];
+        u[(t0 + t) * kRow + col] = (k < a.N && t0 + t < len) ? silu(v) : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  // C_i B_j^T at i = l16 and j = 4 q + e; product t of four takes column 4 q + t of sixteen from each lane
+  f32x4 cb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < kN; k += 16) {
+    const f32x4 bj = *reinterpret_cast<const f32x4*>(u + l16 * kRow + k + 4 * q);
+    const f32x4 ci = *reinterpret_cast<const f32x4*>(u + l16 * kRow + kN + k + 4 * q);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) cb = __builtin_amdgcn_mfma_f32_16x16x4f32(bj[t], ci[t], cb, 0, 0, 0);
+  }
+
+  while (n < last) {
+    const int h = now.h, p = now.p0 + 16 * q, np = now.np - 16 * q;  // the lane's channels of y: p .. p + 15
+    const int64_t row = first + l16;
+    T zv[16];
+    if (a.z && l16 < len) {
+      const T* const z = static_cast<const T*>(a.z) + row * a.z_stride + static_cast<int64_t>(h) * a.P + p;
+      if (np >= 16) {
+        __builtin_memcpy(zv, z, sizeof(zv));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) zv[k] = k < np ? z[k] : T(0);
+      }
+    }
+    float x[4][4];  // [token 4 q + t][channel 4 l16 + c]
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float v = now.cb.at(c) + now.cw[c].at(3) * now.raw[t + 3].at(c) + now.cw[c].at(2) * now.raw[t + 2].at(c);
+        if (a.W > 2) v += now.cw[c].at(1) * now.raw[t + 1].at(c);
+        if (a.W > 3) v += now.cw[c].at(0) * now.raw[t].at(c);
+        x[t][c] = (4 * q + t < len && 4 * l16 + c < now.np) ? silu(v) : 0.f;
+      }
+    const float step = l16 < len ? softplus(now.dt + now.bias) : 0.f, skip = now.skip;
+    double s = static_cast<double>(step) * static_cast<double>(now.decay) * 1.4426950408889634;
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+      const double o = __shfl_up(s, m, 16);
+      if (l16 >= m) s += o;
+    }
+    n += 4;
+    if (n < last) load(n, now);
+
+    float mix[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 4 * q + e;
+      const float v = cb[e] * __shfl(step, j) * __builtin_amdgcn_exp2f(static_cast<float>(s - __shfl(s, j)));
+      mix[e] = j < l16 ? v : (j == l16 ? v + skip : 0.f);
+    }
+    f32x4 y[4];  // y[c][e]: channel p + 4 e + c of token l16
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      y[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e][c], mix[e], y[c], 0, 0, 0);
+    }
+    if (l16 < len) {
+      T o[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float v = y[k & 3][k >> 2];
+        if (a.z) v *= silu(to_float(zv[k]));
+        o[k] = from_float<T>(v);
+      }
+      T* const to = static_cast<T*>(a.y) + row * a.y_stride + static_cast<int64_t>(h) * a.P + p;
+      if (np >= 16) {
+        __builtin_memcpy(to, o, sizeof(o));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (k < np) to[k] = o[k];
+      }
+    }
   }
 }
 

@@ -111,7 +111,7 @@ cdrge_status enqueue_step(const ScanArgs& a, hipStream_t s) {
 struct Plan {
   int kn;  // state_dim as the kernels have it
   int ptiles, max_blocks, max_pieces, piece_blocks;
-  size_t blocks, steps, totals, slots, counts, start, bounds, block_of, piece_of, states, fades, total;
+  size_t blocks, steps, rests, totals, slots, counts, start, bounds, block_of, piece_of, states, fades, total;
 };
 
 constexpr int kPieceWorkgroups = 512;  // two for each of 256 compute units
@@ -150,6 +150,7 @@ Plan make_plan(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs, boo
   };
   p.blocks = region(block_bytes(p.kn, c->dtype == CDRGE_F32) * blocks * c->n_groups);
   p.steps = region(sizeof(float4) * 64 * blocks * c->n_heads);
+  if (c->dtype == CDRGE_F32) p.rests = region(sizeof(float) * 64 * blocks * c->n_heads);
   p.totals = region(sizeof(float4) * blocks * c->n_heads);
   p.slots = region(sizeof(int32_t) * n_seqs);
   if (!equal) {
@@ -172,6 +173,7 @@ ScanWork make_work(const Plan& p, void* ws) {
   ScanWork w;
   w.blocks = at + p.blocks;
   w.steps = reinterpret_cast<float4*>(at + p.steps);
+  w.rests = reinterpret_cast<float*>(at + p.rests);
   w.totals = reinterpret_cast<float4*>(at + p.totals);
   w.slots = reinterpret_cast<int32_t*>(at + p.slots);
   w.counts = reinterpret_cast<int32_t*>(at + p.counts);
@@ -235,6 +237,23 @@ cdrge_status enqueue_prompt(const ScanArgs& a, const Plan& p, const ScanWork& w,
   }
 }
 
+template <class T, int kN>
+cdrge_status launch_short(ScanArgs a, hipStream_t s) {
+  a.ptiles = (a.P + 63) / 64;
+  const int parts = (a.H / a.G * a.ptiles + kScanUnits - 1) / kScanUnits;
+  hipLaunchKernelGGL((k_scan_short<T, kN>), dim3(static_cast<uint32_t>(int64_t(a.n_seqs) * a.G * parts)), dim3(256), 0, s, a, parts);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
+}
+
+template <class T>
+cdrge_status enqueue_short(const ScanArgs& a, hipStream_t s) {
+  if (a.N <= 32) return launch_short<T, 32>(a, s);
+  if (a.N <= 64) return launch_short<T, 64>(a, s);
+  if (a.N <= 128) return launch_short<T, 128>(a, s);
+  return launch_short<T, 256>(a, s);
+}
+
 // Whether the call's sizes fit the kernels' 32-bit counts.
 bool fits(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs) {
   const int64_t blocks = n_tokens / kScanBlock + n_seqs, ptiles = (c->head_dim + 63) / 64;
@@ -272,9 +291,11 @@ cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_we
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0)
     return workspace_error("cdrge_scan_prompt", need, workspace ? workspace_bytes : 0);
   const ScanArgs a = make_args(cfg, weights, io);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (equal && !io->ssm_in && io->n_tokens > 0 && io->n_tokens / io->n_seqs <= kScanShort)
+    return cfg->dtype == CDRGE_F32 ? enqueue_short<float>(a, s) : enqueue_short<uint16_t>(a, s);
   const ScanWork w = make_work(p, workspace);
   const bool pieces = cut(p, io->n_tokens, io->n_seqs, equal);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
   return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, p, w, pieces, s) : enqueue_prompt<uint16_t>(a, p, w, pieces, s);
 }
 
