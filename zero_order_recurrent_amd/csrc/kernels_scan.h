@@ -766,6 +766,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     const int L = min(kScanBlock, sq.len - nth * kScanBlock);
     if (L <= 0) break;  // a sequence without rows
     const char* const in = operands(nth);
+    // the lane's place as new values: addresses made of them are not kept in registers from block to block
+    int lo16 = l16, lq = q, pcn = pc, tgn = tg;
+    asm volatile("" : "+v"(lo16), "+v"(lq), "+v"(pcn), "+v"(tgn));
     const bool keep = slot >= 0 || nth < sq.blocks - 1;  // whether anybody wants the state behind the block
     float* const ts = tokens[nth & 1][0];
     float* const tr = tokens[nth & 1][1];
@@ -782,6 +785,32 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
       }
     }
     if (wave == 1 && lane < 2) sums[nth & 1][lane] = early;
+    // operands of the state; the first run has nothing else to do meanwhile, so it asks for them here
+    f16x8 bhs[2][kTiles], bls[2][kTiles];
+    auto load_b = [&]() {
+      const f16x8* const bf = reinterpret_cast<const f16x8*>(in + Block::kOffB) + lane;
+#pragma unroll
+      for (int step = 0; step < 2; ++step)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          bhs[step][t] = bf[((tile0 + t) * 2 + step) * 64];
+          bls[step][t] = bf[((kN / 16 + tile0 + t) * 2 + step) * 64];
+        }
+    };
+    if (first_run && keep) load_b();
+    // z of the lane's token
+    const int zi = min(16 * wave + lo16, L - 1);
+    T zv[16];
+    if (!first_run && a.z) {
+      const T* const z = static_cast<const T*>(a.z) + (sq.first + static_cast<int64_t>(nth) * kScanBlock + zi) * a.z_stride +
+                         static_cast<int64_t>(h) * a.P + p0 + 16 * lq;
+      if (16 * lq + 16 <= np) {
+        __builtin_memcpy(zv, z, sizeof(zv));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) zv[k] = 16 * lq + k < np ? z[k] : T(0);
+      }
+    }
     // operands of y: C B^T (of a strip's first 16 (wave 0: 16, 1: 32, 2: 48, 3: 64) tokens) and C
     f32x4 cbs[2][2];
     f16x8 chs[kN / 32], cls[kSplit ? kN / 32 : 1];
@@ -807,7 +836,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         float v = cb.at(c) + cw[c].at(3) * raw[t + 3].at(c) + cw[c].at(2) * raw[t + 2].at(c);
         if (a.W > 2) v += cw[c].at(1) * raw[t + 1].at(c);
         if (a.W > 3) v += cw[c].at(0) * raw[t].at(c);
-        u[t][c] = (tg + t < L && pc + c < np) ? silu(v) : 0.f;
+        u[t][c] = (tgn + t < L && pcn + c < np) ? silu(v) : 0.f;
         most = fmaxf(most, fabsf(u[t][c]));
       }
     most = wave_max(most);
@@ -818,11 +847,11 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     const int ex = scan_scale(most), ew = scan_scale(most * total.z), eh = scan_scale(most_state);
     {
       const float fx = two_to(ex), fw = two_to(ew);
-      const float4 left = *reinterpret_cast<const float4*>(tw + tg);
+      const float4 left = *reinterpret_cast<const float4*>(tw + tgn);
       const float l4[4] = {left.x * fw, left.y * fw, left.z * fw, left.w * fw};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int p = pc + c, to = p * 64 + (((tg >> 3) ^ scan_place(p)) << 3) + (tg & 7);
+        const int p = pcn + c, to = p * 64 + (((tgn >> 3) ^ scan_place(p)) << 3) + (tgn & 7);
         f16x4 hi, lo, wh, wl;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -850,8 +879,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int m = 0; m < kCh; ++m) {
-          const int p = 16 * (ch0 + m) + l16, chunk = 2 * (tile0 + t) + (q >> 1);
-          const int to = p * kN + ((chunk ^ (scan_place(p) & (kN / 8 - 1))) << 3) + 4 * (q & 1);
+          const int p = 16 * (ch0 + m) + lo16, chunk = 2 * (tile0 + t) + (lq >> 1);
+          const int to = p * kN + ((chunk ^ (scan_place(p) & (kN / 8 - 1))) << 3) + 4 * (lq & 1);
           f16x4 hi, lo;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -869,33 +898,20 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
       load_raw(nth + 1);
       load_steps(nth + 1);
     }
-    // operands of the state, first step
-    f16x8 bhs[2][kTiles], bls[2][kTiles];
-    auto load_b = [&](int step) {
-      const f16x8* const bf = reinterpret_cast<const f16x8*>(in + Block::kOffB) + lane;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        bhs[step][t] = bf[((tile0 + t) * 2 + step) * 64];
-        bls[step][t] = bf[((kN / 16 + tile0 + t) * 2 + step) * 64];
-      }
-    };
-    if (keep) {
-      load_b(0);
-      load_b(1);
-    }
+    if (!first_run && keep) load_b();
 
     if (!first_run && 16 * wave < L) {
-      const int i = 16 * wave + l16;  // the lane's token
-      // Where the operands of the lane's channels lie: chunk 4 k + q of row p at place (4 k + q) ^ f(p), for even k
+      const int i = 16 * wave + lo16;  // the lane's token
+      // Where the operands of the lane's channels lie: chunk 4 k + lq of row p at place (4 k + lq) ^ f(p), for even k
       // the first of two places and for odd k the second, moved on by whole rows of eight chunks.
       int far_at[4][2], near_at[4][2];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int p = 16 * (l16 >> 2) + 4 * m + (l16 & 3), f = scan_place(p);
+        const int p = 16 * (lo16 >> 2) + 4 * m + (lo16 & 3), f = scan_place(p);
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {
-          near_at[m][odd] = p * 64 + (((4 * odd + q) ^ f) << 3);
-          far_at[m][odd] = p * kN + (((4 * odd + q) ^ (f & (kN / 8 - 1))) << 3);
+          near_at[m][odd] = p * 64 + (((4 * odd + lq) ^ f) << 3);
+          far_at[m][odd] = p * kN + (((4 * odd + lq) ^ (f & (kN / 8 - 1))) << 3);
         }
       }
       const float si = ts[i], li = kSplit ? tl[i] : 0.f;
@@ -927,7 +943,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         f16x8 mh, ml;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int j0 = 32 * step + 8 * q + 4 * half;
+          const int j0 = 32 * step + 8 * lq + 4 * half;
           const f32x4 rj = *reinterpret_cast<const f32x4*>(tr + j0);
           f32x4 qj = {0.f, 0.f, 0.f, 0.f};
           if (kSplit) qj = *reinterpret_cast<const f32x4*>(tq + j0);
@@ -962,19 +978,10 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           v[k] = ldexpf(near[k >> 2][k & 3], -em - ex);
           if (has) v[k] += far[k >> 2][k & 3] * es;
         }
-        const int p = 16 * q;
+        const int p = 16 * lq;
         if (a.z) {
-          const T* const z = static_cast<const T*>(a.z) + row * a.z_stride + static_cast<int64_t>(h) * a.P + p0 + p;
-          if (p + 16 <= np) {
-            T zv[16];
-            __builtin_memcpy(zv, z, sizeof(zv));
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] *= silu(to_float(zv[k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (p + k < np) v[k] *= silu(to_float(z[k]));
-          }
+          for (int k = 0; k < 16; ++k) v[k] *= silu(to_float(zv[k]));
         }
         T o[16];
 #pragma unroll
@@ -1004,7 +1011,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         f16x8 wh[kCh], wl[kCh];
 #pragma unroll
         for (int m = 0; m < kCh; ++m) {
-          const int p = 16 * (ch0 + m) + l16, from = p * 64 + (((4 * step + q) ^ scan_place(p)) << 3);
+          const int p = 16 * (ch0 + m) + lo16, from = p * 64 + (((4 * step + lq) ^ scan_place(p)) << 3);
           wh[m] = *reinterpret_cast<const f16x8*>(&xw[0][from]);
           wl[m] = *reinterpret_cast<const f16x8*>(&xw[1][from]);
         }

@@ -38,15 +38,29 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float silu(float x) { return x * __builtin_amdgcn_rcpf(1.f + exp_fast(-x)); }
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 
+// Sum and maximum over a wave, in every lane. Within a row of 16 lanes the partner is reached by a lane
+// permutation of the vector unit (quads, then mirrored halves and rows), across rows by a swap.
+template <int kControl>
+__device__ __forceinline__ float lane_move(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, kControl, 0xf, 0xf, false));
+}
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F op) {
+  v = op(v, lane_move<0xb1>(v));   // lane ^ 1
+  v = op(v, lane_move<0x4e>(v));   // lane ^ 2
+  v = op(v, lane_move<0x141>(v));  // half-row mirror: 7 - lane
+  v = op(v, lane_move<0x140>(v));  // row mirror: 15 - lane
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = op(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+  return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace cdrge
