@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libcdrge.so")
@@ -387,22 +388,42 @@ def cdrge_distill_grad(cfg, logits, ids, teacher, row_grad, row_losses, losses, 
 
 def _row_stride(t) -> int:
     # a single row may have any stride, also one below its length; the library wants at least that
-    return max(t.stride(0), t.shape[1])
+    n = t.shape[1]
+    stride = t.stride(0)
+    return stride if stride > n else n
 
 
-def _tensor(name, t, dtype, shape, device, rows=False):
-    """Checks one argument. rows: a matrix whose rows may lie further apart than their length."""
+def _refuse(name, t, dtype, shape, index, rows):
+    """Says what is wrong with an argument that _rows or _whole has found wrong."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the operator's weights on {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the operator on cuda:{index}")
     if rows:
-        if t.stride(1) != 1 and shape[1] > 1 and shape[0] > 0 or t.stride(0) < shape[1] and shape[0] > 1:
-            raise ValueError(f"{name} needs rows of adjacent elements that do not overlap, not strides {t.stride()}")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} needs rows of adjacent elements that do not overlap, not strides {t.stride()}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _whole(name, t, dtype, shape, index) -> int:
+    """Checks a contiguous argument of the shape, type and device; returns its pointer. The checks are written for the
+    common case: they are a good part of a small call's time."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, index, False)
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, index) -> int:
+    """The same for a matrix whose rows may lie further apart than their length."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(name, t, dtype, shape, index, True)
+    if not t.is_contiguous():
+        n, width = shape
+        row, col = t.stride()
+        if (col != 1 and width > 1 and n > 0) or (row < width and n > 1):
+            _refuse(name, t, dtype, shape, index, True)
+    return t.data_ptr()
 
 
 class _Operator:
@@ -415,23 +436,36 @@ class _Operator:
             raise CdrgeError(1, type(self).__name__)
         self.dtype = torch.float32 if cfg.dtype == CDRGE_F32 else torch.bfloat16
         self.device = device
+        self.index = device.index
+        self._cfg = ctypes.addressof(cfg)
         self._torch = torch
         self._lib = lib()
+        self._current_device = torch._C._cuda_getDevice
+        self._current_stream = torch._C._cuda_getCurrentRawStream
+        self._sizes = {}
+
+    def _bytes(self, query, *sizes) -> int:
+        """The workspace of a call of these sizes, asked once for each of the last few hundred."""
+        n = self._sizes.get(sizes)
+        if n is None:
+            if len(self._sizes) >= 256:
+                self._sizes.clear()
+            n = self._sizes[sizes] = query(self.cfg, *sizes)
+        return n
 
     def _run(self, call, nbytes, stream):
-        """call(workspace, stream handle) on the operator's device. The workspace belongs to the call's
-        stream, so that torch gives its memory to nobody before the call has run."""
+        """call(workspace or None, stream handle) on the operator's device. The workspace belongs to the call's stream,
+        so that torch gives its memory to nobody before the call has run."""
         torch = self._torch
-        cuda = torch.cuda
-        if stream is None and self.device.index == cuda.current_device():
+        if stream is None and self.index == self._current_device():
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
-            call(ws, cuda.current_stream().cuda_stream)
+            call(ws, self._current_stream(self.index))
             return
-        with cuda.device(self.device):
-            on = cuda.current_stream() if stream is None else stream
+        with torch.cuda.device(self.device):
+            on = torch.cuda.current_stream() if stream is None else stream
             if on.device != self.device:
                 raise ValueError(f"the stream is on {on.device}, the operator on {self.device}")
-            with cuda.stream(on):
+            with torch.cuda.stream(on):
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
                 call(ws, on.cuda_stream)
 
@@ -440,6 +474,11 @@ def _cuda_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     return t.device
+
+
+# cdrge_scan_io as bytes: building them is quicker than filling a ctypes structure, and they belong to one call
+_SCAN_IO = struct.Struct("@" + "Pq" * 4 + "qii" + "P" * 7)
+assert _SCAN_IO.size == ctypes.sizeof(cdrge_scan_io)
 
 
 class ScanLayer(_Operator):
@@ -455,68 +494,64 @@ class ScanLayer(_Operator):
         cdrge_scan_workspace_bytes(cfg, 0, 1)  # raises for a configuration that is not valid or supported
         self.width = cfg.n_heads * cfg.head_dim
         self.channels = self.width + 2 * cfg.n_groups * cfg.state_dim
-        _tensor("conv_weight", conv_weight, self.dtype, (self.channels, cfg.conv_width), self.device)
-        if conv_bias is not None:
-            _tensor("conv_bias", conv_bias, self.dtype, (self.channels,), self.device)
-        for name, t in (("decay", decay), ("skip", skip), ("dt_bias", dt_bias)):
-            if t is not None or name == "decay":
-                _tensor(name, t, torch.float32, (cfg.n_heads,), self.device)
         self._held = (conv_weight, conv_bias, decay, skip, dt_bias)
-        self.weights = cdrge_scan_weights(*(None if t is None else t.data_ptr() for t in self._held))
+        f, heads, at = torch.float32, (cfg.n_heads,), self.index
+        self.weights = cdrge_scan_weights(
+            _whole("conv_weight", conv_weight, self.dtype, (self.channels, cfg.conv_width), at),
+            None if conv_bias is None else _whole("conv_bias", conv_bias, self.dtype, (self.channels,), at),
+            _whole("decay", decay, f, heads, at), None if skip is None else _whole("skip", skip, f, heads, at),
+            None if dt_bias is None else _whole("dt_bias", dt_bias, f, heads, at))
+        self._weights = ctypes.addressof(self.weights)
+        self._state_shapes = (cfg.conv_width, self.channels), (cfg.n_heads, cfg.head_dim, cfg.state_dim)
 
     def _io(self, xbc, dt, y, n_seqs, z, offsets, slots, positions, conv_in, ssm_in, conv_out, ssm_out):
-        cfg, torch, dev, n = self.cfg, self._torch, self.device, xbc.shape[0]
-        _tensor("xbc", xbc, self.dtype, (n, self.channels), dev, rows=True)
-        _tensor("dt", dt, self.dtype, (n, cfg.n_heads), dev, rows=True)
-        _tensor("y", y, self.dtype, (n, self.width), dev, rows=True)
-        if z is not None:
-            _tensor("z", z, self.dtype, (n, self.width), dev, rows=True)
-        if offsets is not None:
-            _tensor("offsets", offsets, torch.int32, (n_seqs + 1,), dev)
-        if slots is not None:
-            _tensor("slots", slots, torch.int32, (n_seqs,), dev)
-        if positions is not None:
-            _tensor("positions", positions, torch.int32, (n_seqs,), dev)
-        n_slots = 0
-        if (conv_in is None) != (ssm_in is None):
-            raise ValueError("the convolution's state and the scan's are given together or not at all")
-        if conv_in is not None:
+        at, n, t, heads, width = self.index, xbc.shape[0], self.dtype, self.cfg.n_heads, self.width
+        i32 = self._torch.int32
+        p_xbc = _rows("xbc", xbc, t, (n, self.channels), at)
+        p_dt = _rows("dt", dt, t, (n, heads), at)
+        p_y = _rows("y", y, t, (n, width), at)
+        p_z, z_stride = (0, 0) if z is None else (_rows("z", z, t, (n, width), at), _row_stride(z))
+        p_offsets = 0 if offsets is None else _whole("offsets", offsets, i32, (n_seqs + 1,), at)
+        p_slots = 0 if slots is None else _whole("slots", slots, i32, (n_seqs,), at)
+        p_positions = 0 if positions is None else _whole("positions", positions, i32, (n_seqs,), at)
+        p_ci = p_co = p_si = p_so = n_slots = 0
+        if conv_in is not None and ssm_in is not None:
             n_slots = ssm_in.shape[0]
-            conv_out = conv_in if conv_out is None else conv_out
-            ssm_out = ssm_in if ssm_out is None else ssm_out
-            for name, t in (("the convolution's state", conv_in), ("conv_out", conv_out)):
-                _tensor(name, t, self.dtype, (n_slots, cfg.conv_width, self.channels), dev)
-            for name, t in (("the scan's state", ssm_in), ("ssm_out", ssm_out)):
-                _tensor(name, t, torch.float32, (n_slots, cfg.n_heads, cfg.head_dim, cfg.state_dim), dev)
+            conv, ssm = self._state_shapes
+            f = self._torch.float32
+            p_ci = p_co = _whole("the convolution's state", conv_in, t, (n_slots, *conv), at)
+            p_si = p_so = _whole("the scan's state", ssm_in, f, (n_slots, *ssm), at)
+            if conv_out is not None:
+                p_co = _whole("conv_out", conv_out, t, (n_slots, *conv), at)
+            if ssm_out is not None:
+                p_so = _whole("ssm_out", ssm_out, f, (n_slots, *ssm), at)
+        elif conv_in is not None or ssm_in is not None:
+            raise ValueError("the convolution's state and the scan's are given together or not at all")
         elif conv_out is not None or ssm_out is not None:
             raise ValueError("an output state needs the states that are read")
-        return cdrge_scan_io(xbc.data_ptr(), _row_stride(xbc), dt.data_ptr(), _row_stride(dt),
-                             None if z is None else z.data_ptr(), 0 if z is None else _row_stride(z),
-                             y.data_ptr(), _row_stride(y), n, n_seqs, n_slots,
-                             None if offsets is None else offsets.data_ptr(),
-                             None if slots is None else slots.data_ptr(),
-                             None if positions is None else positions.data_ptr(),
-                             None if conv_in is None else conv_in.data_ptr(),
-                             None if conv_in is None else conv_out.data_ptr(),
-                             None if conv_in is None else ssm_in.data_ptr(),
-                             None if conv_in is None else ssm_out.data_ptr())
+        return _SCAN_IO.pack(p_xbc, _row_stride(xbc), p_dt, _row_stride(dt), p_z, z_stride, p_y, _row_stride(y), n,
+                             n_seqs, n_slots, p_offsets, p_slots, p_positions, p_ci, p_co, p_si, p_so)
 
     def prompt(self, xbc, dt, y, n_seqs, z=None, offsets=None, slots=None, positions=None, conv_state=None,
                ssm_state=None, conv_out=None, ssm_out=None, stream=None):
         """Whole or continued prompts: rows offsets[i] .. offsets[i + 1] - 1 (or equal shares of the rows) belong to
         sequence i. Writes y, and the states in place unless conv_out and ssm_out are given. Returns y."""
         io = self._io(xbc, dt, y, n_seqs, z, offsets, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
-        nbytes = cdrge_scan_workspace_bytes(self.cfg, io.n_tokens, n_seqs)
-        self._run(lambda ws, s: cdrge_scan_prompt(self.cfg, self.weights, io, ws, s), nbytes, stream)
+        n = self._bytes(cdrge_scan_workspace_bytes, xbc.shape[0], n_seqs)
+        call = self._lib.cdrge_scan_prompt
+        self._run(lambda ws, s: _check(call(self._cfg, self._weights, io, 0 if ws is None else ws.data_ptr(), n, s),
+                                       "cdrge_scan_prompt"), n, stream)
         return y
 
     def step(self, xbc, dt, y, positions, conv_state, ssm_state, z=None, slots=None, conv_out=None, ssm_out=None,
              stream=None):
         """One token of each sequence, row i at place positions[i] of the sequence in slot slots[i] (negative: padding).
         Writes y, and the states in place unless conv_out and ssm_out are given. Returns y."""
-        io = self._io(xbc, dt, y, xbc.shape[0], z, None, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
-        if io.n_tokens:
-            self._run(lambda ws, s: cdrge_scan_step(self.cfg, self.weights, io, s), 0, stream)
+        n = xbc.shape[0]
+        io = self._io(xbc, dt, y, n, z, None, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
+        if n:
+            call = self._lib.cdrge_scan_step
+            self._run(lambda ws, s: _check(call(self._cfg, self._weights, io, s), "cdrge_scan_step"), 0, stream)
         return y
 
 
@@ -531,33 +566,33 @@ class AdapterProjection(_Operator):
         super().__init__(cfg, _cuda_device(weight, "weight"))
         cdrge_adapter_workspace_bytes(cfg, 0)
         K, O, A, R = cfg.in_features, cfg.out_features, cfg.n_adapters, cfg.max_rank
-        _tensor("weight", weight, self.dtype, (O, K), self.device, rows=True)
+        t, at = self.dtype, self.index
+        self._held = (weight, bias, down, up, ranks)
+        p = [_rows("weight", weight, t, (O, K), at), None, None, None, None]
         if bias is not None:
-            _tensor("bias", bias, self.dtype, (O,), self.device)
+            p[1] = _whole("bias", bias, t, (O,), at)
         if A > 0:
             if down is None or up is None:
                 raise ValueError("adapters need their down and up weights")
-            _tensor("down", down, self.dtype, (A, R, K), self.device)
-            _tensor("up", up, self.dtype, (A, O, R), self.device)
-            if ranks is not None:
-                _tensor("ranks", ranks, self._torch.int32, (A,), self.device)
-        self._held = (weight, bias, down, up, ranks)
-        p = [None if t is None else t.data_ptr() for t in self._held]
+            p[2:] = (_whole("down", down, t, (A, R, K), at), _whole("up", up, t, (A, O, R), at),
+                     None if ranks is None else _whole("ranks", ranks, self._torch.int32, (A,), at))
         self.weights = cdrge_adapter_weights(p[0], _row_stride(weight), *p[1:])
+        self._weights = ctypes.addressof(self.weights)
 
     def project(self, x, row_adapter, y, row_scale=None, stream=None):
-        """y[r] = weight x[r] + bias + row_scale[r] up_a (down_a x[r]), a = row_adapter[r] (negative, or row_adapter None:
-        no adapter). Returns y."""
-        n, cfg, torch = x.shape[0], self.cfg, self._torch
-        _tensor("x", x, self.dtype, (n, cfg.in_features), self.device, rows=True)
-        _tensor("y", y, self.dtype, (n, cfg.out_features), self.device, rows=True)
-        if row_adapter is not None:
-            _tensor("row_adapter", row_adapter, torch.int32, (n,), self.device)
-        if row_scale is not None:
-            _tensor("row_scale", row_scale, torch.float32, (n,), self.device)
-        nbytes = cdrge_adapter_workspace_bytes(cfg, n)
-        self._run(lambda ws, s: cdrge_adapter_project(cfg, self.weights, n, x, row_adapter, row_scale, y, ws, s), nbytes,
-                  stream)
+        """y[r] = weight x[r] + bias + row_scale[r] up_a (down_a x[r]), a = row_adapter[r] (negative, or row_adapter
+        None: no adapter). Returns y."""
+        n, cfg, torch, at, t = x.shape[0], self.cfg, self._torch, self.index, self.dtype
+        p_x = _rows("x", x, t, (n, cfg.in_features), at)
+        p_y = _rows("y", y, t, (n, cfg.out_features), at)
+        p_who = 0 if row_adapter is None else _whole("row_adapter", row_adapter, torch.int32, (n,), at)
+        p_scale = 0 if row_scale is None else _whole("row_scale", row_scale, torch.float32, (n,), at)
+        nbytes = self._bytes(cdrge_adapter_workspace_bytes, n)
+        call = self._lib.cdrge_adapter_project
+        x_stride, y_stride = _row_stride(x), _row_stride(y)
+        self._run(lambda ws, s: _check(call(self._cfg, self._weights, n, p_x, x_stride, p_who, p_scale, p_y, y_stride,
+                                            0 if ws is None else ws.data_ptr(), nbytes, s), "cdrge_adapter_project"),
+                  nbytes, stream)
         return y
 
 
@@ -574,27 +609,29 @@ class DistillLoss(_Operator):
         super().__init__(cfg, device)
 
     def _inputs(self, logits, ids, teacher, row_losses, losses):
-        n, cfg, torch, dev = logits.shape[0], self.cfg, self._torch, self.device
-        _tensor("logits", logits, self.dtype, (n, cfg.vocab), dev, rows=True)
-        _tensor("ids", ids, torch.int32, (n, cfg.top_k), dev)
-        _tensor("teacher", teacher, torch.float32, (n, cfg.top_k), dev)
-        _tensor("row_losses", row_losses, torch.float32, (n,), dev)
-        if losses is not None:
-            _tensor("losses", losses, torch.float32, (cfg.n_models,), dev)
+        n, cfg, at, f = logits.shape[0], self.cfg, self.index, self._torch.float32
+        return (self._cfg, n, _rows("logits", logits, self.dtype, (n, cfg.vocab), at), _row_stride(logits),
+                _whole("ids", ids, self._torch.int32, (n, cfg.top_k), at),
+                _whole("teacher", teacher, f, (n, cfg.top_k), at),
+                _whole("row_losses", row_losses, f, (n,), at),
+                0 if losses is None else _whole("losses", losses, f, (cfg.n_models,), at))
 
     def losses(self, logits, ids, teacher, row_losses, losses=None, stream=None):
         """Fills row_losses [rows] and, if given, losses [n_models], the means by model (NaN where no row is scored)."""
-        self._inputs(logits, ids, teacher, row_losses, losses)
-        self._run(lambda ws, s: cdrge_distill_losses(self.cfg, logits, ids, teacher, row_losses, losses, s), 0, stream)
+        args = self._inputs(logits, ids, teacher, row_losses, losses)
+        call = self._lib.cdrge_distill_losses
+        self._run(lambda ws, s: _check(call(*args, s), "cdrge_distill_losses"), 0, stream)
         return row_losses
 
     def grad(self, logits, ids, teacher, row_grad, row_losses, losses, dlogits, stream=None):
         """The losses, and dlogits[r] = row_grad[r] d row_loss_r / d logits[r] (row_grad None: 1; losses may be None).
         dlogits may be logits itself. Returns dlogits."""
-        self._inputs(logits, ids, teacher, row_losses, losses)
-        _tensor("dlogits", dlogits, self.dtype, logits.shape, self.device, rows=True)
-        if row_grad is not None:
-            _tensor("row_grad", row_grad, self._torch.float32, (logits.shape[0],), self.device)
-        self._run(lambda ws, s: cdrge_distill_grad(self.cfg, logits, ids, teacher, row_grad, row_losses, losses, dlogits, s),
-                  0, stream)
+        args = self._inputs(logits, ids, teacher, row_losses, losses)
+        n = logits.shape[0]
+        p_up = 0 if row_grad is None else _whole("row_grad", row_grad, self._torch.float32, (n,), self.index)
+        p_d = _rows("dlogits", dlogits, self.dtype, (n, self.cfg.vocab), self.index)
+        d_stride = _row_stride(dlogits)
+        call = self._lib.cdrge_distill_grad
+        self._run(lambda ws, s: _check(call(*args[:6], p_up, *args[6:], p_d, d_stride, s), "cdrge_distill_grad"), 0,
+                  stream)
         return dlogits
