@@ -405,7 +405,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   constexpr int kCols = 2 * kN, kRow = kCols + 2;  // a row's pad: eight rows on lies 16 banks on
   extern __shared__ float u[];                     // [64][kRow]: the convolved B, then C
   __shared__ float red[3][8];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, block = blockIdx.x / (parts * a.G);
   const int2 at = scan_find(a, w, block, false);
   if (at.x < 0) return;
@@ -623,7 +623,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   // by token, for this block and the next: s, r, faded step, and what s and r lack; totals and scales
   __shared__ float tokens[2][kSplit ? 5 : 3][64], red[4];
   __shared__ float4 sums[2][2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
 
   // workgroups go round the eight XCDs: the heads of a piece, which share its blocks' operands, stay on one
@@ -1076,7 +1076,7 @@ template <class T, int kN>
 __global__ __launch_bounds__(256) void k_scan_short(ScanArgs a, int parts) {
   constexpr int kCols = 2 * kN, kRow = kCols + 4;
   __shared__ float u[kScanShort * kRow];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, i = blockIdx.x / (parts * a.G);
   const int len = static_cast<int>(a.n_tokens / a.n_seqs), each = a.H / a.G;
   const int64_t first = static_cast<int64_t>(i) * len;
