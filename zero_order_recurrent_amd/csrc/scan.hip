@@ -98,13 +98,24 @@ cdrge_status launch_step(ScanArgs a, hipStream_t s) {
   return CDRGE_OK;
 }
 
+// Few rows take small tiles: the call's time is then the way of one workgroup, a quarter of the loads long
+// (N 128, one row of 16 heads: 6.6 us against 8.8). Past four workgroups a compute unit the convolution of B
+// and C, which every tile repeats, costs more (8 x 16 heads 7.7 against 9.3 us, 16 x 16 10.0 against 9.9,
+// 64 x 64 95 against 56).
+template <class T, int kLanes, int kRpt>
+cdrge_status launch_step_tiles(const ScanArgs& a, hipStream_t s) {
+  constexpr int kSmall = 256 / kLanes * (kRpt / 4);
+  if (int64_t(a.n_seqs) * a.H * ((a.P + kSmall - 1) / kSmall) <= 1024) return launch_step<T, kLanes, kRpt / 4>(a, s);
+  return launch_step<T, kLanes, kRpt>(a, s);
+}
+
 template <class T>
 cdrge_status enqueue_step(const ScanArgs& a, hipStream_t s) {
   if (a.N <= 16) return launch_step<T, 4, 1>(a, s);
   if (a.N <= 32) return launch_step<T, 8, 2>(a, s);
-  if (a.N <= 64) return launch_step<T, 16, 4>(a, s);
-  if (a.N <= 128) return launch_step<T, 32, 8>(a, s);
-  return launch_step<T, 64, 8>(a, s);
+  if (a.N <= 64) return launch_step_tiles<T, 16, 4>(a, s);
+  if (a.N <= 128) return launch_step_tiles<T, 32, 8>(a, s);
+  return launch_step_tiles<T, 64, 8>(a, s);
 }
 
 // How a prompt call is cut up and where its workspace's parts lie; by sizes alone.
