@@ -68,8 +68,8 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
   p.slice_cols = slice_columns(K, want, p.rows ? 4 * step / 2 : step);
   p.slices = ceil_div(K, p.slice_cols);
   const int v_tiles = ceil_div(n_rows, 64);
-  // beside up to 64 rows: 16 workgroups for the adapters, four for K; otherwise as many as fill the chip
-  p.v_slots = std::max(1, std::min({c->n_adapters, 16, ceil_div(256, v_tiles)}));
+  // as many workgroups for the adapters as fill the chip, beside up to 64 rows one for each that they can name
+  p.v_slots = std::max(1, std::min({c->n_adapters, p.rows ? static_cast<int>(n_rows) : 16, ceil_div(256, v_tiles)}));
   p.v_cols = slice_columns(K, p.rows || p.slices > 1 ? kMostVSlices : 1, 4 * step);
   p.v_slices = ceil_div(K, p.v_cols);
   p.packed = !p.rows && p.slices == 1;

@@ -134,15 +134,38 @@ __device__ __forceinline__ int rank_of(const AdapterArgs& a, int ad) {
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ int vq_columns(int rank) { return (rank + 31) & ~31; }
 
+// A wave's share of the columns k .. k1 - 1 of 16 rows of D times kTiles tiles of rows of x.
+template <class T, int kWaves, int kTiles, int kDeep>
+__device__ __forceinline__ void down_steps(const T* ds, int64_t d, int64_t total, const T* xs, const int64_t (&x)[4], int64_t span, int k, int k1, int q, f32x4 (&acc)[4]) {
+  constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer;
+  for (; k + (kWaves * (kDeep - 1) + 1) * kCols <= k1; k += kWaves * kDeep * kCols) {  // kDeep steps' loads in flight together
+    Frag<T> df[kDeep], xf[kDeep][kTiles];
+#pragma unroll
+    for (int s = 0; s < kDeep; ++s) {
+      const int at = k + kWaves * s * kCols + q * kPer;
+      df[s] = load_frag<T>(ds + d + at);
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
+    }
+#pragma unroll
+    for (int s = 0; s < kDeep; ++s)
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) acc[m] = mma(df[s], xf[s][m], acc[m]);
+  }
+  for (; k < k1; k += kWaves * kCols) {
+    const int at = k + q * kPer;
+    const Frag<T> df = load_cut<T>(ds, d + at, total, k1 - at);
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) acc[m] = mma(df, load_cut<T>(xs, x[m] + at, span, k1 - at), acc[m]);
+  }
+}
+
 template <class T, int kWaves>
 __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile, int slice, int slot, f32x4 (&lds)[kWaves][4][64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t r0 = tile * 64;
   const int ad = r0 + lane < a.n_rows ? a.row_adapter[r0 + lane] : -1;
   const T* const xs = static_cast<const T*>(a.x);
-  int64_t x[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) x[m] = min(r0 + 16 * m + l16, a.n_rows - 1) * a.x_stride;
   const int k0 = slice * a.v_cols, k1 = min(a.K, k0 + a.v_cols);
   uint64_t todo = __ballot(ad >= 0 && ad < a.A);
   const float scale = (a.vq && a.row_scale && r0 + lane < a.n_rows) ? a.row_scale[r0 + lane] : 1.f;
@@ -153,47 +176,39 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
     if (n % a.v_slots != slot) continue;
     // rows of D past the rank give values that are not kept, so with up to 16 of them nothing waits for the rank
     const int rank = rank_of(a, cur), most = a.R <= 16 ? a.R : rank;
-    const bool all = (mine & 0xffffu) && (mine & 0xffff0000u) && (mine >> 32 & 0xffffu) && (mine >> 48);
+    // the adapter's rows side by side: place i holds the i-th of them (of places past the last: the first)
+    const int count = __popcll(mine);
+    const uint64_t below = (uint64_t(1) << lane) - 1;
+    const int place = mine >> lane & 1 ? __popcll(mine & below) : count + __popcll(~mine & below);
+    int from = __builtin_amdgcn_ds_permute(4 * place, lane);  // every lane sends its number to its place
+    if (lane >= count) from = __builtin_ctzll(mine);
+    int64_t x[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) x[m] = (r0 + __shfl(from, 16 * m + l16)) * a.x_stride;
     for (int j0 = 0; j0 < (a.vq ? vq_columns(most) : most); j0 += 16) {
       const T* const ds = static_cast<const T*>(a.down);
       const int64_t d = (static_cast<int64_t>(cur) * a.R + min(j0 + l16, most - 1)) * a.K;
       f32x4 acc[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-      constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer, kDeep = 4;  // steps whose loads are in flight together
-      int k = j0 < most ? k0 + wave * kCols : k1;  // past the rank: zeros
-      if (all) {
-        for (; k + (kWaves * (kDeep - 1) + 1) * kCols <= k1; k += kWaves * kDeep * kCols) {
-          Frag<T> df[kDeep], xf[kDeep][4];
-#pragma unroll
-          for (int s = 0; s < kDeep; ++s) {
-            const int at = k + kWaves * s * kCols + q * kPer;
-            df[s] = load_frag<T>(ds + d + at);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
-          }
-#pragma unroll
-          for (int s = 0; s < kDeep; ++s)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) acc[m] = mma(df[s], xf[s][m], acc[m]);
-        }
-      }
-      for (; k < k1; k += kWaves * kCols) {
-        const int at = k + q * kPer;
-        const Frag<T> df = load_cut<T>(ds, d + at, static_cast<int64_t>(a.A) * a.R * a.K, k1 - at);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if ((mine >> (16 * m)) & 0xffffu) acc[m] = mma(df, load_cut<T>(xs, x[m] + at, span_x(a), k1 - at), acc[m]);
+      if (j0 < most) {  // past the rank: zeros
+        const int64_t total = static_cast<int64_t>(a.A) * a.R * a.K;
+        if (count > 32)
+          down_steps<T, kWaves, 4, 4>(ds, d, total, xs, x, span_x(a), k0 + wave * Frag<T>::kCols, k1, q, acc);
+        else if (count > 16)
+          down_steps<T, kWaves, 2, 4>(ds, d, total, xs, x, span_x(a), k0 + wave * Frag<T>::kCols, k1, q, acc);
+        else
+          down_steps<T, kWaves, 1, kWaves == 4 ? 8 : 4>(ds, d, total, xs, x, span_x(a), k0 + wave * Frag<T>::kCols, k1, q, acc);
       }
 #pragma unroll
       for (int m = 0; m < 4; ++m) lds[wave][m][lane] = acc[m];
       __syncthreads();
       if (wave < 4) {
-        // wave m sums row tile m: rank indexes j0 + 4 q + e of row 16 m + l16
+        // wave m sums row tile m: rank indexes j0 + 4 q + e of the row at place 16 m + l16
         f32x4 sum = lds[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) sum += lds[w][wave][lane];
-        const int row = 16 * wave + l16, j = j0 + 4 * q;
+        const int at = 16 * wave + l16, row = __shfl(from, at), j = j0 + 4 * q;
         if (a.vq) {
           const float s = __shfl(scale, row);
           T hi[4], lo[4];
@@ -204,12 +219,12 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
             // an infinite v has no low half (inf - inf would turn it into NaN)
             lo[e] = from_float<T>(fabsf(f) <= 3.38953139e38f ? f - to_float(hi[e]) : 0.f);
           }
-          if ((mine >> row) & 1) {
+          if (at < count) {
             T* v = static_cast<T*>(a.vq) + (r0 + row) * a.vq_row + j;
             __builtin_memcpy(v, hi, sizeof(hi));
             if (sizeof(T) == 2) __builtin_memcpy(v + a.vq_row / 2, lo, sizeof(lo));
           }
-        } else if ((mine >> row) & 1) {
+        } else if (at < count) {
           float* v = a.vp + (static_cast<int64_t>(slice) * a.n_rows + r0 + row) * a.R + j;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -300,7 +315,7 @@ template <class T>
 __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   constexpr int kPer = Frag<T>::kPer, kCols = Frag<T>::kCols;
   __shared__ f32x4 lds[4][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t r = static_cast<int64_t>(blockIdx.y) * 16 + l16;
   const bool rok = r < a.n_rows;
   const int o0 = blockIdx.x * 64;
@@ -421,9 +436,9 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
 // the down product, which needs nothing from them.
 // ---------------------------------------------------------------------------------------------
 template <class T, int kTiles>
-__global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
+__global__ __launch_bounds__(256, 2) void k_adapter_rows(AdapterArgs a) {
   __shared__ f32x4 lds[4][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int main_blocks = a.tiles_o * a.slices;
   if (static_cast<int>(blockIdx.x) >= main_blocks) {
     const int i = blockIdx.x - main_blocks;
@@ -445,37 +460,45 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer;
+  constexpr int kDeep = 4;  // steps whose loads are in flight together, the next ones' behind the products of these
   int k = k0 + wave * kCols;
-  constexpr int kDeep = kTiles > 2 ? 2 : 4;  // steps whose loads are in flight together
-  for (; k + (4 * (kDeep - 1) + 1) * kCols <= k1; k += 4 * kDeep * kCols) {
-    Frag<T> wf[kDeep][4], xf[kDeep][kTiles];
+  const int whole = max(0, (k1 - k + 3 * kCols) / (4 * kCols));  // steps within the row
+  Frag<T> wf[kDeep][4], xf[kDeep][kTiles];
+  auto load = [&](int s, int n) {
+    const int at = k + 4 * n * kCols + q * kPer;
 #pragma unroll
-    for (int s = 0; s < kDeep; ++s) {
-      const int at = k + 4 * s * kCols + q * kPer;
+    for (int t = 0; t < 4; ++t) wf[s][t] = load_frag<T>(ws + w[t] + at);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) wf[s][t] = load_frag<T>(ws + w[t] + at);
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
-    }
-#pragma unroll
-    for (int s = 0; s < kDeep; ++s)
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[m][t] = mma(wf[s][t], xf[s][m], acc[m][t]);
-  }
-  for (; k < k1; k += 4 * kCols) {
-    const int at = k + q * kPer;
-    Frag<T> wf[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) wf[t] = load_cut<T>(ws, w[t] + at, span_w(a), k1 - at);
-    Frag<T> xf[kTiles];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) xf[m] = load_cut<T>(xs, x[m] + at, span_x(a), k1 - at);
+    for (int m = 0; m < kTiles; ++m) xf[s][m] = load_frag<T>(xs + x[m] + at);
+  };
+  auto multiply = [&](int s) {
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[m][t] = mma(wf[t], xf[m], acc[m][t]);
+      for (int t = 0; t < 4; ++t) acc[m][t] = mma(wf[s][t], xf[s][m], acc[m][t]);
+  };
+  if (whole > 0) {
+#pragma unroll
+    for (int s = 0; s < kDeep; ++s) load(s, min(s, whole - 1));
+    int n = 0;
+    for (; n + kDeep < whole; n += kDeep)
+#pragma unroll
+      for (int s = 0; s < kDeep; ++s) {
+        multiply(s);
+        load(s, min(n + s + kDeep, whole - 1));
+      }
+#pragma unroll
+    for (int s = 0; s < kDeep; ++s)
+      if (n + s < whole) multiply(s);
+  }
+  k += 4 * whole * kCols;
+  if (k < k1) {  // the step that the row ends in
+    const int at = k + q * kPer;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) wf[0][t] = load_cut<T>(ws, w[t] + at, span_w(a), k1 - at);
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) xf[0][m] = load_cut<T>(xs, x[m] + at, span_x(a), k1 - at);
+    multiply(0);
   }
 #pragma unroll
   for (int m = 0; m < kTiles; ++m) {
