@@ -291,7 +291,7 @@ typedef struct {
 } cdrge_scan_io;
 
 /* Workspace, in bytes, of cdrge_scan_prompt for n_tokens tokens in n_seqs sequences (256-byte
- * aligned base required). */
+ * aligned base required). Equal sequences of at most 16 tokens without a state need none. */
 cdrge_status cdrge_scan_workspace_bytes(const cdrge_scan_config* cfg, int64_t n_tokens, int32_t n_seqs,
                                         size_t* bytes_out);
 
@@ -300,7 +300,9 @@ cdrge_status cdrge_scan_workspace_bytes(const cdrge_scan_config* cfg, int64_t n_
  * clamped into a rising row. A sequence whose slot is negative keeps no state (and starts at
  * zero). One whose slot is n_slots or more, or is named by an earlier sequence of the call, gets
  * NaN rows and touches no state. A token that is not finite may spoil outputs of its own sequence
- * from up to 63 tokens before it; other sequences are not affected. */
+ * from up to 63 tokens before it; other sequences are not affected. Products are formed of entries
+ * scaled by the largest of their kind in a head's 64 tokens (22 bits below it are kept, for y in
+ * bf16 11): magnitudes of u or S past 2^100 are treated as infinite, and below 2^-100 as zero. */
 cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_weights* weights,
                                const cdrge_scan_io* io, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -362,7 +364,7 @@ typedef struct {
   int32_t vocab;        /* 1 .. 2^24 */
   int32_t top_k;        /* 1 .. 1024 */
   int32_t n_models;     /* 1 .. 2^20; divides the number of rows */
-  float temperature;    /* > 0 */
+  float temperature;    /* 2^-60 .. 2^60 */
 } cdrge_distill_config;
 
 /* logits: T [n_rows][vocab]; ids: int32 [n_rows][top_k]; teacher: float32 [n_rows][top_k];

@@ -68,6 +68,19 @@ def test_project(case, order):
     assert (y[:, c.O:] == 7).all()
 
 
+@pytest.mark.parametrize("counts", [[64], [40, 24], [33, 17, 14], [1] * 64, [0, 50, 3], [16, 16, 31, 1], [48, 150, 2]])
+@pytest.mark.parametrize("dtype, K, R", [("bf16", 1000, 16), ("bf16", 130, 40), ("f32", 515, 20)])
+def test_rows_of_an_adapter_lie_anywhere(dtype, K, R, counts):
+    """Adapters that few, some and most of a tile's rows name, in any order."""
+    n = sum(counts)
+    c = Case(dtype, n, K, 96, len(counts), R, seed=n)
+    who = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts))
+    c.who = who[torch.randperm(n, generator=torch.Generator().manual_seed(n))].to(torch.int32)
+    x, who, y, scale = c.inputs()
+    c.operator().project(x, who, y[:, :c.O], row_scale=scale)
+    c.check(y[:, :c.O])
+
+
 @pytest.mark.parametrize("dtype, rows, K, O, R, pad", [("bf16", 3333, 192, 3880, 8, 0), ("bf16", 3333, 70, 3880, 40, 3), ("f32", 3100, 64, 4070, 24, 0)])
 def test_many_rows(dtype, rows, K, O, R, pad):
     """The largest tiles, with rows and outputs that end inside one, aligned and not."""

@@ -111,6 +111,11 @@ def test_distill_refuses(lib, kw, status):
     assert _distill(lib, **kw) == status
 
 
+@pytest.mark.parametrize("tau", [2.0 ** -61, 2.0 ** 61, 1e-40])
+def test_distill_refuses_far_temperatures(lib, tau):
+    assert _distill(lib, temperature=tau) == 2
+
+
 def test_distill_grad_refuses(lib):
     c = b.make_distill_config(50, 4, 2, 1.5, "f32")
 

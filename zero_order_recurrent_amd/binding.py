@@ -537,7 +537,9 @@ class ScanLayer(_Operator):
         """Whole or continued prompts: rows offsets[i] .. offsets[i + 1] - 1 (or equal shares of the rows) belong to
         sequence i. Writes y, and the states in place unless conv_out and ssm_out are given. Returns y."""
         io = self._io(xbc, dt, y, n_seqs, z, offsets, slots, positions, conv_state, ssm_state, conv_out, ssm_out)
-        n = self._bytes(cdrge_scan_workspace_bytes, xbc.shape[0], n_seqs)
+        tokens = xbc.shape[0]
+        short = offsets is None and ssm_state is None and 0 < tokens <= 16 * n_seqs  # these need no workspace
+        n = 0 if short else self._bytes(cdrge_scan_workspace_bytes, tokens, n_seqs)
         call = self._lib.cdrge_scan_prompt
         self._run(lambda ws, s: _check(call(self._cfg, self._weights, io, 0 if ws is None else ws.data_ptr(), n, s),
                                        "cdrge_scan_prompt"), n, stream)

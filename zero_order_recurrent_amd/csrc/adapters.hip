@@ -99,8 +99,8 @@ cdrge_status launch_tiles(const AdapterArgs& a, int64_t blocks, hipStream_t s) {
     CDRGE_HIP(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
     ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
   }
-  hipLaunchKernelGGL((k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>), dim3(static_cast<uint32_t>(blocks)),
-                     dim3(64 * kWavesR * kWavesO), kLds, s, a);
+  hipLaunchKernelGGL((k_adapter_tiles<T, kSide, kSide, kWavesR, kWavesO, kDirect>), 
+                     grid_of(blocks, 64 * kWavesR * kWavesO), dim3(64 * kWavesR * kWavesO), kLds, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -136,7 +136,7 @@ cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
   } else {
     if (low && a.slices == 1) {
       const int64_t blocks = int64_t(ceil_div(a.n_rows, 64)) * a.v_slots;
-      hipLaunchKernelGGL(k_adapter_down<T>, dim3(static_cast<uint32_t>(blocks)), dim3(1024), 0, s, a);
+      hipLaunchKernelGGL(k_adapter_down<T>, grid_of(blocks, 1024), dim3(1024), 0, s, a);
       CDRGE_HIP(hipGetLastError());
     }
     constexpr int kPer = 16 / sizeof(T), kStep = 128 / sizeof(T);
@@ -176,7 +176,8 @@ cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_
   if (n_rows == 0) return CDRGE_OK;
   if (!x || !y) return CDRGE_ERR_INVALID_ARG;
   const Cut p = make_cut(cfg, n_rows);
-  if (int64_t(ceil_div(n_rows, 64)) * ceil_div(O, 64) * p.slices > kMostBlocks / 2 ||  int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks / 2)
+  if (int64_t(ceil_div(n_rows, 64)) * ceil_div(O, 64) * p.slices > kMostBlocks / 2 ||
+      int64_t(ceil_div(n_rows, 64)) * p.v_slices * p.v_slots > kMostBlocks / 2)
     return CDRGE_ERR_UNSUPPORTED;
   if (p.total > 0 && (!ws || workspace_bytes < p.total || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return workspace_error("cdrge_adapter_project", p.total, ws ? workspace_bytes : 0);

@@ -19,6 +19,8 @@ cdrge_status check(const cdrge_distill_config* c, int64_t n_rows, const void* lo
   if (!std::isfinite(c->temperature) || !(c->temperature > 0.f)) return CDRGE_ERR_INVALID_ARG;
   if (n_rows % c->n_models != 0 || stride < c->vocab) return CDRGE_ERR_INVALID_ARG;
   if (n_rows > 0 && (!logits || !ids || !teacher || !row_losses)) return CDRGE_ERR_INVALID_ARG;
+  // beyond these the scaled logits or the loss's tau^2 leave float32's range for ordinary logits
+  if (c->temperature < 0x1p-60f || c->temperature > 0x1p60f) return CDRGE_ERR_UNSUPPORTED;
   if (c->vocab > (1 << 24) || c->top_k > 1024 || c->n_models > (1 << 20) || n_rows > (int64_t(1) << 30))
     return CDRGE_ERR_UNSUPPORTED;
   return CDRGE_OK;
@@ -28,7 +30,7 @@ template <class T, bool kGrad, int kTeam, int kPieces>
 void launch(const DistillArgs& a, hipStream_t s) {
   constexpr int kThreads = distill_threads(kTeam), kRows = kThreads / kTeam;
   const size_t lds = size_t(8) * ((a.top_k + 3) & ~3) * kRows;
-  hipLaunchKernelGGL((k_distill<T, kGrad, kTeam, kPieces>), dim3(static_cast<uint32_t>((a.n_rows + kRows - 1) / kRows)),
+  hipLaunchKernelGGL((k_distill<T, kGrad, kTeam, kPieces>), grid_of((a.n_rows + kRows - 1) / kRows, kThreads),
                      dim3(kThreads), lds, s, a);
 }
 

@@ -239,7 +239,8 @@ __device__ __forceinline__ void adapter_down(const AdapterArgs& a, int64_t tile,
 template <class T>
 __global__ __launch_bounds__(1024) void k_adapter_down(AdapterArgs a) {
   __shared__ f32x4 lds[16][4][64];
-  adapter_down<T, 16>(a, blockIdx.x / a.v_slots, 0, blockIdx.x % a.v_slots, lds);
+  const uint32_t block = static_cast<uint32_t>(block_number());
+  adapter_down<T, 16>(a, block / a.v_slots, 0, block % a.v_slots, lds);
 }
 
 // v_r from column j on: the sum over the slices of K, without the row's scale; columns from R on are zero.
@@ -460,7 +461,7 @@ __global__ __launch_bounds__(256, 2) void k_adapter_rows(AdapterArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   constexpr int kCols = Frag<T>::kCols, kPer = Frag<T>::kPer;
-  constexpr int kDeep = 4;  // steps whose loads are in flight together, the next ones' behind the products of these
+  constexpr int kDeep = kTiles < 4 ? 4 : 3;  // steps whose loads are in flight together, the next ones' behind the products of these
   int k = k0 + wave * kCols;
   const int whole = max(0, (k1 - k + 3 * kCols) / (4 * kCols));  // steps within the row
   Frag<T> wf[kDeep][4], xf[kDeep][kTiles];
@@ -563,17 +564,19 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   // Tiles by XCD: workgroups go round the eight XCDs, each of which has its own L2. XCD i gets the
   // i-th eighth of the tiles, walked in columns of up to four row tiles.
   const int n_tiles = a.tiles_r * a.tiles_o;
-  if constexpr (kThreads == 256) {
+  const uint32_t block = static_cast<uint32_t>(block_number());
+  if (block >= static_cast<uint32_t>(n_tiles * a.slices)) {
     // after a product in slices the up product has a launch of its own, and the down product runs beside it
-    const int64_t past = static_cast<int64_t>(blockIdx.x) - static_cast<int64_t>(n_tiles) * a.slices;
-    if (past >= 0) {
-      const int slot = past % a.v_slots, part = past / a.v_slots % a.v_slices;
-      adapter_down<T, 4>(a, past / (a.v_slots * a.v_slices), part, slot, *reinterpret_cast<f32x4(*)[4][4][64]>(stage));
-      return;
+    if constexpr (kThreads == 256) {
+      const uint32_t past = block - n_tiles * a.slices;
+      if (a.slices > 1)
+        adapter_down<T, 4>(a, past / (a.v_slots * a.v_slices), past / a.v_slots % a.v_slices, past % a.v_slots,
+                           *reinterpret_cast<f32x4(*)[4][4][64]>(stage));
     }
+    return;
   }
-  const int slice = blockIdx.x / n_tiles;
-  int id = blockIdx.x % n_tiles;
+  const int slice = block / n_tiles;
+  int id = block % n_tiles;
   {
     const int per = n_tiles >> 3, rest = n_tiles & 7, xcd = id & 7;
     id = xcd * per + min(xcd, rest) + (id >> 3);

@@ -138,7 +138,7 @@ __global__ __launch_bounds__(distill_threads(kTeam), distill_waves(kTeam, kPiece
   constexpr int kRows = distill_threads(kTeam) / kTeam;
   constexpr int kOwn = (kTeam == 16 ? 256 : 1024 + kTeam - 1) / kTeam;  // teacher entries of a thread
   const int lane = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + team;
+  const int64_t row = block_number() * kRows + team;
   if (row >= a.n_rows) return;  // whole teams, of one wave at most, which wait for nobody below
   const int V = a.vocab, k = a.top_k, k4 = (k + 3) & ~3;
   float* prob = lds + 2 * team * k4;

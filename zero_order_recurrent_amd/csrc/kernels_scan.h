@@ -70,7 +70,9 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
   constexpr int kConv = (kTile + 8 * kLanes + 255) / 256;  // channels of the convolution that a thread takes
   __shared__ float sb[kScanMaxState], sc[kScanMaxState], sx[kTile], sy[kTile];
   const int tid = threadIdx.x;
-  const int tile = blockIdx.x % a.ptiles, h = (blockIdx.x / a.ptiles) % a.H, i = blockIdx.x / (a.ptiles * a.H);
+  const uint32_t id = static_cast<uint32_t>(block_number());
+  const int tile = id % a.ptiles, h = id / a.ptiles % a.H, i = id / (a.ptiles * a.H);
+  if (i >= a.n_seqs) return;
   const int slot = a.slots ? a.slots[i] : i, pos = max(a.positions[i], 0);
   if (slot < 0) return;
   const int p0 = tile * kTile, np = min(kTile, a.P - p0);
@@ -434,7 +436,8 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   extern __shared__ float u[];                     // [64][kRow]: the convolved B, then C
   __shared__ float red[3][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
-  const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, block = blockIdx.x / (parts * a.G);
+  const uint32_t id = static_cast<uint32_t>(block_number());
+  const int part = id % parts, g = id / parts % a.G, block = id / (parts * a.G);
   const int2 at = scan_find(a, w, block, false);
   if (at.x < 0) return;
   const ScanSeq sq = scan_seq(a, w, at.x);
@@ -655,9 +658,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
 
   // workgroups go round the eight XCDs: the heads of a piece, which share its blocks' operands, stay on one
-  int id = blockIdx.x;
+  uint32_t id = static_cast<uint32_t>(block_number());
   {
-    const int n = gridDim.x, per = n >> 3, rest = n & 7, xcd = id & 7;
+    const uint32_t n = gridDim.x * gridDim.y, per = n >> 3, rest = n & 7, xcd = id & 7;
     id = xcd * per + min(xcd, rest) + (id >> 3);
   }
   const int tile = id % a.ptiles, h = id / a.ptiles % a.H, piece = id / (a.ptiles * a.H);
@@ -1105,7 +1108,9 @@ __global__ __launch_bounds__(256) void k_scan_short(ScanArgs a, int parts) {
   constexpr int kCols = 2 * kN, kRow = kCols + 4;
   __shared__ float u[kScanShort * kRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
-  const int part = blockIdx.x % parts, g = blockIdx.x / parts % a.G, i = blockIdx.x / (parts * a.G);
+  const uint32_t id = static_cast<uint32_t>(block_number());
+  const int part = id % parts, g = id / parts % a.G, i = id / (parts * a.G);
+  if (i >= a.n_seqs) return;
   const int len = static_cast<int>(a.n_tokens / a.n_seqs), each = a.H / a.G;
   const int64_t first = static_cast<int64_t>(i) * len;
   const T* const xbc = static_cast<const T*>(a.xbc) + first * a.xbc_stride;
@@ -1253,7 +1258,9 @@ __global__ __launch_bounds__(256) void k_scan_short(ScanArgs a, int parts) {
 // done. grid: (channel blocks of 256, sequences).
 template <class T>
 __global__ __launch_bounds__(256) void k_scan_ring(ScanArgs a, ScanWork w, int cblocks) {
-  const int i = blockIdx.x / cblocks, c = (blockIdx.x % cblocks) * 256 + threadIdx.x;
+  const uint32_t id = static_cast<uint32_t>(block_number());
+  const int i = id / cblocks, c = (id % cblocks) * 256 + threadIdx.x;
+  if (i >= a.n_seqs) return;
   const int slot = w.slots[i];
   if (slot < 0 || c >= a.C) return;
   const ScanSeq sq = scan_seq(a, w, i);

@@ -38,6 +38,14 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float silu(float x) { return x * __builtin_amdgcn_rcpf(1.f + exp_fast(-x)); }
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 
+// Workgroups in one row, or in rows of 2^20 where a dimension's limit of 2^32 threads does not hold them; then the
+// last row has some too many, which a kernel sends home by their number.
+inline dim3 grid_of(int64_t blocks, int threads) {
+  if (blocks * threads < (int64_t(1) << 32)) return dim3(static_cast<uint32_t>(blocks));
+  return dim3(1u << 20, static_cast<uint32_t>((blocks + (1 << 20) - 1) >> 20));
+}
+__device__ __forceinline__ int64_t block_number() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 // Sum and maximum over a wave, in every lane. Within a row of 16 lanes the partner is reached by a lane
 // permutation of the vector unit (quads, then mirrored halves and rows), across rows by a swap.
 template <int kControl>

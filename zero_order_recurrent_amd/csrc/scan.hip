@@ -93,7 +93,7 @@ cdrge_status launch_step(ScanArgs a, hipStream_t s) {
   a.ptiles = (a.P + kTile - 1) / kTile;
   const int64_t n = int64_t(a.n_seqs) * a.H * a.ptiles;
   if (n > kMostBlocks) return CDRGE_ERR_UNSUPPORTED;
-  hipLaunchKernelGGL((k_scan_step<T, kLanes, kRpt>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_scan_step<T, kLanes, kRpt>), grid_of(n, 256), dim3(256), 0, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -220,10 +220,9 @@ cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pi
     }
   }
   const int parts = 1 + (a.H / a.G + 8 * kScanHeads - 1) / (8 * kScanHeads);
-  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), dim3(static_cast<uint32_t>(int64_t(p.max_blocks) * a.G * parts)), dim3(512), kLds, s,
-                     a, w, parts);
+  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), grid_of(int64_t(p.max_blocks) * a.G * parts, 512), dim3(512), kLds, s, a, w, parts);
   CDRGE_HIP(hipGetLastError());
-  const dim3 grid(static_cast<uint32_t>(int64_t(p.max_pieces) * a.H * p.ptiles));
+  const dim3 grid = grid_of(int64_t(p.max_pieces) * a.H * p.ptiles, 256);
   if (pieces) {
     hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit, true>), grid, dim3(256), 0, s, a, w);
     CDRGE_HIP(hipGetLastError());
@@ -232,7 +231,7 @@ cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pi
   CDRGE_HIP(hipGetLastError());
   if (a.conv_in) {
     const int cblocks = (a.C + 255) / 256;
-    hipLaunchKernelGGL(k_scan_ring<T>, dim3(static_cast<uint32_t>(int64_t(a.n_seqs) * cblocks)), dim3(256), 0, s, a, w, cblocks);
+    hipLaunchKernelGGL(k_scan_ring<T>, grid_of(int64_t(a.n_seqs) * cblocks, 256), dim3(256), 0, s, a, w, cblocks);
     CDRGE_HIP(hipGetLastError());
   }
   return CDRGE_OK;
@@ -252,7 +251,7 @@ template <class T, int kN>
 cdrge_status launch_short(ScanArgs a, hipStream_t s) {
   a.ptiles = (a.P + 63) / 64;
   const int parts = (a.H / a.G * a.ptiles + kScanUnits - 1) / kScanUnits;
-  hipLaunchKernelGGL((k_scan_short<T, kN>), dim3(static_cast<uint32_t>(int64_t(a.n_seqs) * a.G * parts)), dim3(256), 0, s, a, parts);
+  hipLaunchKernelGGL((k_scan_short<T, kN>), grid_of(int64_t(a.n_seqs) * a.G * parts, 256), dim3(256), 0, s, a, parts);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -295,16 +294,16 @@ cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_we
   if (st != CDRGE_OK) return st;
   if (!fits(cfg, io->n_tokens, io->n_seqs)) return CDRGE_ERR_UNSUPPORTED;
   const bool equal = !io->offsets;
-  const Plan p = make_plan(cfg, io->n_tokens, io->n_seqs, equal);
+  const ScanArgs a = make_args(cfg, weights, io);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (equal && !io->ssm_in && io->n_tokens > 0 && io->n_tokens / io->n_seqs <= kScanShort)
+    return cfg->dtype == CDRGE_F32 ? enqueue_short<float>(a, s) : enqueue_short<uint16_t>(a, s);
   size_t need = 0;
   st = cdrge_scan_workspace_bytes(cfg, io->n_tokens, io->n_seqs, &need);
   if (st != CDRGE_OK) return st;
   if (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % kAlign != 0)
     return workspace_error("cdrge_scan_prompt", need, workspace ? workspace_bytes : 0);
-  const ScanArgs a = make_args(cfg, weights, io);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (equal && !io->ssm_in && io->n_tokens > 0 && io->n_tokens / io->n_seqs <= kScanShort)
-    return cfg->dtype == CDRGE_F32 ? enqueue_short<float>(a, s) : enqueue_short<uint16_t>(a, s);
+  const Plan p = make_plan(cfg, io->n_tokens, io->n_seqs, equal);
   const ScanWork w = make_work(p, workspace);
   const bool pieces = cut(p, io->n_tokens, io->n_seqs, equal);
   return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, p, w, pieces, s) : enqueue_prompt<uint16_t>(a, p, w, pieces, s);
