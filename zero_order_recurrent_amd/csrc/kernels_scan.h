@@ -1103,8 +1103,10 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kScanShort = 16, kScanUnits = 16;
 
+// bf16: four waves a SIMD, at the price of a few spilled registers (three without: 65 us instead of 52 at 1,024 x 10
+// tokens, 16 heads of 64 x 64); float32's do not fit.
 template <class T, int kN>
-__global__ __launch_bounds__(256) void k_scan_short(ScanArgs a, int parts) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(ScanArgs a, int parts) {
   constexpr int kCols = 2 * kN, kRow = kCols + 4;
   __shared__ float u[kScanShort * kRow];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
