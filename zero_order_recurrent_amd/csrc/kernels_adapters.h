@@ -322,6 +322,12 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   const int o0 = blockIdx.x * 64;
   const int ad = (a.row_adapter && rok) ? a.row_adapter[r] : -1;
   const bool narrow = a.R <= kCols;  // one product a tile
+  // what no adapter decides is asked for first
+  const int o = o0 + 16 * q + 4 * wave;
+  float bias[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) bias[e] = a.bias && o + e < a.O ? to_float(static_cast<const T*>(a.bias)[o + e]) : 0.f;
+  const float row_scale = a.row_scale && rok ? a.row_scale[r] : 1.f;
   float vs[kPer];
   if (narrow && a.row_adapter && a.A > 0) v_sums<kPer>(a, r, q * kPer, vs);
   f32x4 sum[4];
@@ -339,7 +345,7 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   if (todo) {
     // two rounds of loads: the adapters of the rows, with the sums; then everything that an adapter names
     const int rank = has ? rank_of(a, ad) : 0;
-    const float scale = has && a.row_scale ? a.row_scale[r] : 1.f;
+    const float scale = has ? row_scale : 1.f;
     while (todo) {
       // the next four of this wave's adapters (every fourth); one that is missing repeats the first
       int cur[4], got = 0;
@@ -412,14 +418,10 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   f32x4 out = lds[0][wave][lane];
 #pragma unroll
   for (int w = 1; w < 4; ++w) out += lds[w][wave][lane];
-  const int o = o0 + 16 * q + 4 * wave;
   if (!rok) return;
   T v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float b = a.bias && o + e < a.O ? to_float(static_cast<const T*>(a.bias)[o + e]) : 0.f;
-    v[e] = from_float<T>(ad >= a.A ? __builtin_nanf("") : out[e] + b);
-  }
+  for (int e = 0; e < 4; ++e) v[e] = from_float<T>(ad >= a.A ? __builtin_nanf("") : out[e] + bias[e]);
   T* y = static_cast<T*>(a.y) + r * a.y_stride + o;
   if (o + 4 <= a.O) {
     __builtin_memcpy(y, v, sizeof(v));
