@@ -68,6 +68,34 @@ def test_project(case, order):
     assert (y[:, c.O:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows, K, O, A, R", [(1, 8, 5, 1, 1), (1, 2047, 33, 3, 30), (4, 1000, 100, 3, 16), (2, 513, 17, 2, 23), (3, 96, 160, 5, 9),
+                                              (4, 1, 1, 2, 7), (16, 300, 70, 0, 1), (1, 4096, 48, 2, 16), (1, 33, 20, 2, 64), (5, 64, 40, 9, 4),
+                                              (2, 4100, 40, 2, 16)])
+def test_a_row_or_a_few(dtype, rows, K, O, A, R):
+    """Either side of the one-launch form's limits, the same adapter twice, ranks of zero, rows without one or with a bad one."""
+    c = Case(dtype, rows, K, O, A, R, seed=rows * K, ranks=[(R + 1) // 2 * (i % 3) for i in range(A)] if A else None)
+    op, (x, who, y, scale) = c.operator(), c.inputs()
+    op.project(x, who, y[:, :c.O], row_scale=scale)
+    if not A:  # every adapter is out of range
+        bad, c.who = c.who >= 0, torch.full_like(c.who, -1)
+        assert bad.any() and y[bad.cuda(), :c.O].isnan().all()
+    c.check(y[:, :c.O], rows=slice(None) if A else ~bad)
+    assert (y[:, c.O:] == 7).all()
+    if A:
+        c.who[:] = A - 1
+        op.project(x, c.who.cuda(), y[:, :c.O], row_scale=scale)
+        c.check(y[:, :c.O])
+        who = c.who.clone()
+        who[0] = A
+        c.down[0] = float("nan")  # an adapter that no row names
+        bad = b.AdapterProjection(op.cfg, op._held[0], op._held[1], c.down.cuda(), op._held[3], op._held[4])
+        bad.project(x, who.cuda(), y[:, :c.O], row_scale=scale)
+        assert y[0, :c.O].isnan().all()
+        if rows > 1 and A > 1:
+            c.check(y[:, :c.O], rows=slice(1, None))
+
+
 @pytest.mark.parametrize("counts", [[64], [40, 24], [33, 17, 14], [1] * 64, [0, 50, 3], [16, 16, 31, 1], [48, 150, 2]])
 @pytest.mark.parametrize("dtype, K, R", [("bf16", 1000, 16), ("bf16", 130, 40), ("f32", 515, 20)])
 def test_rows_of_an_adapter_lie_anywhere(dtype, K, R, counts):

@@ -26,6 +26,7 @@ cdrge_status check(const cdrge_adapter_config* c, int64_t n_rows) {
 
 // How a call is cut up. It goes by the sizes alone, so that the workspace is known without pointers.
 struct Cut {
+  bool few;              // k_adapter_few, which needs no workspace
   bool rows;             // k_adapter_rows (up to 64 rows)
   int side;              // of the tiles of the shared product (k_adapter_tiles)
   int tiles_r, tiles_o, slices, slice_cols;
@@ -47,6 +48,16 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
   const int K = c->in_features, O = c->out_features;
   const int step = c->dtype == CDRGE_F32 ? 32 : 64;  // columns of 128 bytes
   p.o_pad = (O + 63) / 64 * 64;
+  // A row or a few in one launch. Each workgroup repeats the down product (tiles of 16 rows of D), which pays while
+  // that is little: one row of rank 16, K x O = 1024 x 4096 6.6 us against 12.7 in two launches, 4096 x 4096 12.6
+  // against 17.5, but 5888 x 5888 34 against 26; two rows at 4096 x 1024 15.8 against 13.8. Without adapters, 16 rows
+  // at 4096 x 4096 9.9 against 15.5 and at 5888 x 5888 30 against 26; up to four rows 21 against 23 there, and at
+  // 512 x 65536, where W's rows are short, 24.6 against 19.4.
+  const int tiles = c->n_adapters > 0 ? static_cast<int>(std::min<int64_t>(n_rows, kFewTiles + 1)) * ceil_div(c->max_rank, 16) : 0;
+  const int64_t load = int64_t(std::max(tiles, 1)) * K;
+  p.few = n_rows <= 16 && tiles <= kFewTiles &&
+          ((load <= 4096 && load * O <= (1 << 24)) || (tiles == 0 && n_rows <= 4 && K >= 1024));
+  if (p.few) return p;
   p.rows = n_rows <= 64;
   int want;
   if (p.rows) {
@@ -124,6 +135,20 @@ cdrge_status launch_side(AdapterArgs a, int side, bool low, hipStream_t s) {
 template <class T>
 cdrge_status enqueue(const AdapterArgs& a, const Cut& p, hipStream_t s) {
   const bool low = a.row_adapter && a.A > 0;
+  if (p.few) {
+    const int tiles = low ? static_cast<int>(a.n_rows) * ceil_div(a.R, 16) : 0;
+    const dim3 grid(ceil_div(a.O, 16));
+    if (tiles == 0)
+      hipLaunchKernelGGL((k_adapter_few<T, 0>), grid, dim3(512), 0, s, a);
+    else if (tiles == 1)
+      hipLaunchKernelGGL((k_adapter_few<T, 1>), grid, dim3(512), 0, s, a);
+    else if (tiles == 2)
+      hipLaunchKernelGGL((k_adapter_few<T, 2>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_adapter_few<T, kFewTiles>), grid, dim3(512), 0, s, a);
+    CDRGE_HIP(hipGetLastError());
+    return CDRGE_OK;
+  }
   if (p.rows) {
     const int blocks = a.tiles_o * a.slices + (low ? a.v_slices * a.v_slots : 0);
     switch ((a.n_rows + 15) / 16) {
