@@ -63,8 +63,6 @@ __device__ __forceinline__ void team_sync() {
   }
 }
 
-typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4;  // 16 bytes at any element's alignment
-
 // A row as pieces of 16 bytes, wherever it starts (global memory takes such accesses at any element's
 // alignment). Sums group by piece, so a row's results do not depend on where it lies. Elements past
 // the row's end read as minus infinity and are neither loaded nor stored.
@@ -78,12 +76,11 @@ struct DistillRow {
   __device__ __forceinline__ uint4 load(const T* x, int b) const {
     uint4 r;
     if ((b + 1) * kPer <= V) {
-      if (!kOnce) {
+      if (kOnce)
+        load_once(r, x + b * kPer);
+      else
         __builtin_memcpy(&r, x + b * kPer, 16);
-        return r;
-      }
-      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + b * kPer));
-      return make_uint4(v.x, v.y, v.z, v.w);
+      return r;
     }
     T e[kPer];
 #pragma unroll
@@ -93,7 +90,7 @@ struct DistillRow {
   }
   __device__ __forceinline__ void store(T* d, int b, uint4 r) const {
     if ((b + 1) * kPer <= V) {
-      __builtin_nontemporal_store(u32x4{r.x, r.y, r.z, r.w}, reinterpret_cast<u32x4*>(d + b * kPer));
+      store_once(d + b * kPer, r);
       return;
     }
     T e[kPer];

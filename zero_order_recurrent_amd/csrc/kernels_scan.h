@@ -836,7 +836,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
       const T* const z = static_cast<const T*>(a.z) + (sq.first + static_cast<int64_t>(nth) * kScanBlock + zi) * a.z_stride +
                          static_cast<int64_t>(h) * a.P + p0 + 16 * lq;
       if (16 * lq + 16 <= np) {
-        __builtin_memcpy(zv, z, sizeof(zv));
+        load_once(zv, z);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) zv[k] = 16 * lq + k < np ? z[k] : T(0);
@@ -1019,7 +1019,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         for (int k = 0; k < 16; ++k) o[k] = from_float<T>(v[k]);
         T* const to = y + row * a.y_stride + p;
         if (p + 16 <= np) {
-          __builtin_memcpy(to, o, sizeof(o));
+          store_once(to, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -1196,7 +1196,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(Scan
     if (a.z && l16 < len) {
       const T* const z = static_cast<const T*>(a.z) + row * a.z_stride + static_cast<int64_t>(h) * a.P + p;
       if (np >= 16) {
-        __builtin_memcpy(zv, z, sizeof(zv));
+        load_once(zv, z);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) zv[k] = k < np ? z[k] : T(0);
@@ -1246,7 +1246,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(Scan
       }
       T* const to = static_cast<T*>(a.y) + row * a.y_stride + static_cast<int64_t>(h) * a.P + p;
       if (np >= 16) {
-        __builtin_memcpy(to, o, sizeof(o));
+        store_once(to, o);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k)

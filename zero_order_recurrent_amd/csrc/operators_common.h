@@ -38,6 +38,25 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float silu(float x) { return x * __builtin_amdgcn_rcpf(1.f + exp_fast(-x)); }
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 
+// Whole pieces of 16 bytes, at any element's alignment, past the caches: for what is read or written once.
+typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4;
+template <class A>
+__device__ __forceinline__ void load_once(A& to, const void* from) {
+  static_assert(sizeof(A) % 16 == 0, "whole pieces");
+  u32x4 v[sizeof(A) / 16];
+#pragma unroll
+  for (int i = 0; i < int(sizeof(A) / 16); ++i) v[i] = __builtin_nontemporal_load(static_cast<const u32x4*>(from) + i);
+  __builtin_memcpy(&to, v, sizeof(A));
+}
+template <class A>
+__device__ __forceinline__ void store_once(void* to, const A& from) {
+  static_assert(sizeof(A) % 16 == 0, "whole pieces");
+  u32x4 v[sizeof(A) / 16];
+  __builtin_memcpy(v, &from, sizeof(A));
+#pragma unroll
+  for (int i = 0; i < int(sizeof(A) / 16); ++i) __builtin_nontemporal_store(v[i], static_cast<u32x4*>(to) + i);
+}
+
 // Workgroups in one row, or in rows of 2^20 where a dimension's limit of 2^32 threads does not hold them; then the
 // last row has some too many, which a kernel sends home by their number.
 inline dim3 grid_of(int64_t blocks, int threads) {
