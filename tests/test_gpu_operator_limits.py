@@ -93,3 +93,67 @@ def test_scan_short_sequences():
     layer.prompt(xbc, dt, base, m)
     layer.prompt(spread(xbc, n), spread(dt, n), big, n)
     assert base.isfinite().all() and base.any() and repeats(big, base)
+
+
+@pytest.mark.parametrize("form", ["step", "prompt"])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_scan_far_positions(form, width):
+    """The last positions that 32 bits hold: only their place in the ring counts (12 is a multiple of every width)."""
+    heads, slots = 3, 4
+    g = torch.Generator(device="cuda").manual_seed(width)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    layer = b.ScanLayer(b.make_scan_config(heads, 5, 1, 6, width, "f32"), rand(27, width), None, -rand(heads).exp())
+    n = slots * (1 if form == "step" else 70)
+    xbc, dt, conv, ssm = rand(n, 27), rand(n, heads), rand(slots, width, 27), rand(slots, heads, 5, 6)
+    far = torch.tensor([2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 8, 2 ** 30], dtype=torch.int64)
+
+    def run(positions):
+        y, c, s = torch.zeros(n, 15, device="cuda"), conv.clone(), ssm.clone()
+        at = positions.to(torch.int32).cuda()
+        if form == "step":
+            layer.step(xbc, dt, y, at, c, s)
+        else:
+            layer.prompt(xbc, dt, y, slots, positions=at, conv_state=c, ssm_state=s)
+        return y, c, s
+
+    near = run(far % 12 + 12)
+    assert near[0].isfinite().all() and not torch.equal(near[2], ssm)
+    for a, c in zip(run(far), near):
+        assert torch.equal(a, c)
+
+
+def test_two_calls_at_once():
+    """The same operators on two streams: each call has a workspace of its own."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    layer, channels, _ = scan_layer(16, 1, 5)
+    adapters = b.AdapterProjection(b.make_adapter_config(256, 320, 3, 8, "f32"), rand(320, 256), None, rand(3, 8, 256), rand(3, 320, 8))
+    loss = b.DistillLoss(b.make_distill_config(999, 4, 1, 2.0, "f32"))
+    inputs = []
+    for _ in range(2):
+        ids = torch.randint(0, 999, (300, 4), device="cuda", generator=g, dtype=torch.int32)
+        inputs.append((rand(3000, channels).bfloat16(), rand(3000, 16).bfloat16(), rand(300, 256),
+                       torch.randint(-1, 3, (300,), device="cuda", generator=g, dtype=torch.int32), rand(300, 999), ids, rand(300, 4)))
+
+    def run(xbc, dt, x, who, logits, ids, teacher):
+        y, z = torch.empty(3000, 16, device="cuda", dtype=torch.bfloat16), torch.empty(300, 320, device="cuda")
+        few = torch.empty(40, 320, device="cuda")
+        row, d = torch.empty(300, device="cuda"), torch.empty_like(logits)
+        layer.prompt(xbc, dt, y, 3)
+        adapters.project(x, who, z)
+        adapters.project(x[:40], who[:40], few)
+        loss.grad(logits, ids, teacher, None, row, None, d)
+        return y, z, few, row, d
+
+    want = [run(*i) for i in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, i in zip(streams, inputs):
+            with torch.cuda.stream(s):
+                got.append(run(*i))
+        torch.cuda.synchronize()
+        for a, c in zip(got, want):
+            for u, v in zip(a, c):
+                assert torch.equal(u, v)

@@ -208,6 +208,11 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
 // idle, sequences are cut into pieces: a first run of k_scan_heads forms each piece's own state from
 // zero (without y), and in the second run a piece starts from its predecessors' states, each faded
 // by the pieces behind it. This reads x twice but leaves no state in memory but one a piece.
+// One sequence of 8,192 tokens, 64 heads of 64, state 128, bf16, takes 240 us: k_scan_blocks 23, the first run
+// 78, the second 153, k_scan_ring 5 (37.7 ms by the step above, token after token; 44 us for the bytes). It is bound
+// by the vector unit's issue and by what two waves a SIMD leave uncovered: a block costs a wave some 1,300 vector
+// instructions (convolution, gates, decays, splitting operands) beside 72 matrix products, half of the time.
+// Pieces of at least four blocks: with at least 8, 1 x 2048 tokens and 16 heads takes 102 us instead of 74.
 //
 // Products run on the matrix cores in half precision (11 bits), operands scaled by a power of two of
 // the block so that their largest magnitude is below 2^14: for bf16 tensors one product for y (its
@@ -305,7 +310,8 @@ __device__ __forceinline__ int2 scan_find(const ScanArgs& a, const ScanWork& w, 
 }
 
 // Ragged sequences: bounds (offsets clamped into [0, n_tokens] and into a rising row), where blocks and
-// pieces start, and whose each of them is. One workgroup; 1,024 sequences at a time.
+// pieces start, and whose each of them is. One workgroup; 1,024 sequences at a time. 5 us for 33 sequences, the
+// latency of a launch.
 static __global__ __launch_bounds__(1024) void k_scan_map(ScanArgs a, ScanWork w) {
   __shared__ int scan[3][16];
   __shared__ int seq_blocks[1024], seq_pieces[1024], seq_block0[1024], seq_piece0[1024];
@@ -428,7 +434,8 @@ __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w,
 }
 
 // What a block's heads share: one workgroup of eight waves a block and group for B and C, and further ones
-// for the steps of kScanHeads * 8 heads each. kN: state_dim rounded up to 32, 64, 128 or 256.
+// for the steps of kScanHeads * 8 heads each. kN: state_dim rounded up to 32, 64, 128 or 256. Bound by latency
+// (convolution, products, store, one after the other): 128 blocks, state 128, 64 heads 23 us.
 template <class T, int kN, bool kSplit>
 __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int parts) {
   using Block = ScanBlock<kN, kSplit>;
@@ -643,6 +650,7 @@ __device__ __forceinline__ int scan_place(int p) { return ((p ^ (p >> 2)) & 3) |
 // pieces that have a successor. Lane (l16, q) of wave i holds the state at columns 16 tile + 4 q + e and
 // channel 16 m + l16, the tiles shared among the waves, and y at token 16 i + l16 and channels 16 q + 4 m + e.
 // Loads are issued a phase or more before their use: a block's time is otherwise theirs, one after the other.
+// z and y, each met once, go past the caches, which keeps x there for the second run (1 x 8,192 tokens: 250 to 240 us).
 template <class T, int kN, bool kSplit, bool kFirstRun>
 __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   constexpr bool first_run = kFirstRun;
@@ -1098,8 +1106,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 // Sequences of up to 16 rows each, all equally long, that carry no state: one launch, everything in
 // float32 on the matrix cores. A workgroup takes a sequence and group and up to kScanUnits (head, 64
 // channels); its four waves convolve B and C together and then take the units in turn. Bound by
-// latency and by the convolutions' and gates' exponentials. (1,024 sequences of 10 tokens, 16 heads of
-// 64, state 64, bf16: 210 us by blocks of 64 tokens.)
+// latency and by the convolutions' and gates' exponentials: 1,024 sequences of 10 tokens, 16 heads of
+// 64, state 64, bf16, take 50 us (1.3 TB/s), 210 by blocks of 64 tokens. Eight units a workgroup instead of 16: 57.
 // ---------------------------------------------------------------------------------------------
 constexpr int kScanShort = 16, kScanUnits = 16;
 
@@ -1257,7 +1265,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(Scan
 }
 
 // The rings after a prompt call, a launch of its own: in place, every reader of the old rings is
-// done. grid: (channel blocks of 256, sequences).
+// done. Workgroups go by sequence and 256 channels. 5 us for one sequence of 4,352 channels: the latency of a launch.
 template <class T>
 __global__ __launch_bounds__(256) void k_scan_ring(ScanArgs a, ScanWork w, int cblocks) {
   const uint32_t id = static_cast<uint32_t>(block_number());
