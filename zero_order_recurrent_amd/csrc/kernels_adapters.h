@@ -292,28 +292,45 @@ __device__ __forceinline__ void v_frag(const float (&f)[8], Frag<uint16_t>& hi, 
   }
 }
 
-// Columns from j on of the four output tiles of adapter cur's up matrix; up_cut sets those from n on to zero.
+// Columns from j on of the four output tiles of adapter cur's up matrix; up_cut sets those from n on to zero. Where a
+// row is whole pieces a lane's piece is inside or outside, and nothing has to be moved within it; those outside are
+// somebody's, and up_cut has to follow.
 template <class T>
+__device__ __forceinline__ bool up_whole(const AdapterArgs& a) { return a.R % Frag<T>::kPer == 0; }
+template <class T, bool kWhole>
 __device__ __forceinline__ void up_frags(const AdapterArgs& a, int cur, int o0, int j, Frag<T> (&u)[4]) {
   const int l16 = threadIdx.x & 15;
+  const T* const up = static_cast<const T*>(a.up);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int o = min(o0 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), a.O - 1);
-    u[t] = load_cut<T>(static_cast<const T*>(a.up), (static_cast<int64_t>(cur) * a.O + o) * a.R + j, span_up(a), a.R - j);
+    const int64_t row = (static_cast<int64_t>(cur) * a.O + min(o0 + 16 * (l16 >> 2) + 4 * t + (l16 & 3), a.O - 1)) * a.R;
+    u[t] = kWhole ? load_frag<T>(up + row + min(j, a.R - Frag<T>::kPer)) : load_cut<T>(up, row + j, span_up(a), a.R - j);
   }
 }
 template <class T>
 __device__ __forceinline__ void up_cut(int j, int n, Frag<T> (&u)[4]) {
+  constexpr int kEach = 4 / sizeof(T);  // elements of a word
+  uint32_t keep[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int i = 0; i < 4; ++i) {
+    const int left = n - j - kEach * i;
+    keep[i] = left >= kEach ? ~0u : (left > 0 ? 0xffffu : 0u);
+  }
 #pragma unroll
-    for (int i = 0; i < Frag<T>::kPer; ++i) u[t].v[i] = j + i < n ? u[t].v[i] : 0;
+  for (int t = 0; t < 4; ++t) {
+    uint32_t v[4];
+    __builtin_memcpy(v, &u[t].v, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] &= keep[i];
+    __builtin_memcpy(&u[t].v, v, 16);
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
 // After a shared product in slices: 16 rows x 64 outputs by four waves, which share the slices and the
 // adapters among the rows and add up through LDS. The time is the latency of a few loads, so each wave
-// has those of up to four adapters in flight together (48 rows, 5888 outputs, 40 adapters: 9 us; without adapters 4.6).
+// has those of up to four adapters in flight together (48 rows, 5888 outputs, 40 adapters of
+// rank 16: 7.4 us, of rank 12 9; without adapters 4.6).
 // sum[t][e] is output o0 + 16 q + 4 t + e of row l16.
 // ---------------------------------------------------------------------------------------------
 template <class T>
@@ -368,8 +385,13 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
       if (!got) break;
       if (narrow) {
         Frag<T> u[4][4];
+        if (up_whole<T>(a)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) up_frags<T>(a, cur[i], o0, q * kPer, u[i]);
+          for (int i = 0; i < 4; ++i) up_frags<T, true>(a, cur[i], o0, q * kPer, u[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) up_frags<T, false>(a, cur[i], o0, q * kPer, u[i]);
+        }
         Frag<T> vh, vl;
         float f[kPer];
 #pragma unroll
@@ -378,7 +400,7 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
         v_frag(f, vh, vl);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (a.ranks) up_cut<T>(q * kPer, rank_of(a, cur[i]), u[i]);
+          if (a.ranks || up_whole<T>(a)) up_cut<T>(q * kPer, rank_of(a, cur[i]), u[i]);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             f32x4 low = mma(u[i][t], vh, f32x4{0.f, 0.f, 0.f, 0.f});
@@ -397,7 +419,10 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
           for (int j = 0; j < rc; j += kCols) {
             float f[kPer];
             Frag<T> hi, lo, u[4];
-            up_frags<T>(a, c, o0, j + q * kPer, u);
+            if (up_whole<T>(a))
+              up_frags<T, true>(a, c, o0, j + q * kPer, u);
+            else
+              up_frags<T, false>(a, c, o0, j + q * kPer, u);
             v_sums<kPer>(a, r, j + q * kPer, f);
             v_scaled<kPer>(f, j + q * kPer, ad == c ? rc : 0, scale);
             v_frag(f, hi, lo);
