@@ -301,8 +301,8 @@ cdrge_status cdrge_scan_workspace_bytes(const cdrge_scan_config* cfg, int64_t n_
  * zero). One whose slot is n_slots or more, or is named by an earlier sequence of the call, gets
  * NaN rows and touches no state. A token that is not finite may spoil outputs of its own sequence
  * from up to 63 tokens before it; other sequences are not affected. Products are formed of entries
- * scaled by the largest of their kind in a head's 64 tokens (22 bits below it are kept, for y in
- * bf16 11): magnitudes of u or S past 2^100 are treated as infinite, and below 2^-100 as zero. */
+ * rounded to 22 bits, or to 2^-38 of the largest of their kind in a head's 64 tokens where that is
+ * more: magnitudes of u or S past 2^100 are treated as infinite, and below 2^-100 as zero. */
 cdrge_status cdrge_scan_prompt(const cdrge_scan_config* cfg, const cdrge_scan_weights* weights,
                                const cdrge_scan_io* io, void* workspace, size_t workspace_bytes, void* stream);
 

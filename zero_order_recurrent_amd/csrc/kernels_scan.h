@@ -208,16 +208,16 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
 // idle, sequences are cut into pieces: a first run of k_scan_heads forms each piece's own state from
 // zero (without y), and in the second run a piece starts from its predecessors' states, each faded
 // by the pieces behind it. This reads x twice but leaves no state in memory but one a piece.
-// One sequence of 8,192 tokens, 64 heads of 64, state 128, bf16, takes 220 us: k_scan_blocks 23, the first run
+// One sequence of 8,192 tokens, 64 heads of 64, state 128, bf16, takes 250 us: k_scan_blocks 23, the first run
 // 72, the second 142, k_scan_ring 5 (37.7 ms by the step above, token after token; 44 us for the bytes). It is bound
 // by the vector unit's issue and by what two waves a SIMD leave uncovered: a block costs a wave some 1,300 vector
 // instructions (convolution, gates, decays, splitting operands) beside 72 matrix products, 55% of the time.
 // Pieces of at least four blocks: with at least 8, 1 x 2048 tokens and 16 heads takes 102 us instead of 74.
 //
 // Products run on the matrix cores in half precision (11 bits), operands scaled by a power of two of
-// the block so that their largest magnitude is below 2^14: for bf16 tensors one product for y (its
-// operands' rounding, 2^-12, is far below y's own, 2^-9), and for the state, which is float32, operands
-// in two halves each (22 bits) and three products. float32 tensors take every operand in two halves.
+// the block so that their largest magnitude is below 2^14, in two halves each (22 bits) and three
+// products, for either type of tensor. With y's operands in one half, y in bf16 differs from the exact
+// one's nearest by 1.2e-3 of y in the 2-norm, with two by 2e-5; the call above takes 221 us so, and 250.
 // ---------------------------------------------------------------------------------------------
 constexpr int kScanBlock = 64;
 
@@ -242,15 +242,15 @@ __device__ __forceinline__ void split_half(float v, _Float16& hi, _Float16& lo) 
 
 // What k_scan_blocks leaves for a block and group: matrix-core operands, 16 bytes a lane.
 //   cb     [strip 4][step 2][lane][8] float: C_i B_j^T, i = 16 strip + lane % 16, j = 32 step + 8 (lane / 16) + e
-//   c      [strip 4][kN / 32][lane][8] half: C_i, columns 32 step + 8 (lane / 16) + e; then the low halves (float32)
+//   c      [strip 4][kN / 32][lane][8] half: C_i, columns 32 step + 8 (lane / 16) + e; then the low halves
 //   b      [tile kN / 16][step 2][lane][8] half: B_j at column 16 tile + lane % 16; then the low halves
 //   scale  float4: the scales of c and of b (exponents), the largest |cb|, the largest |B|
-template <int kN, bool kSplit>
+template <int kN>
 struct ScanBlock {
   static constexpr int kCb = 4 * 2 * 64 * 8 * 4;
   static constexpr int kC = 4 * (kN / 32) * 64 * 16;
   static constexpr int kB = (kN / 16) * 2 * 64 * 16;
-  static constexpr int kOffC = kCb, kOffB = kOffC + kC * (kSplit ? 2 : 1), kOffScale = kOffB + 2 * kB;
+  static constexpr int kOffC = kCb, kOffB = kOffC + 2 * kC, kOffScale = kOffB + 2 * kB;
   static constexpr int kBytes = kOffScale + 256;
 };
 
@@ -436,9 +436,9 @@ __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w,
 // What a block's heads share: one workgroup of eight waves a block and group for B and C, and further ones
 // for the steps of kScanHeads * 8 heads each. kN: state_dim rounded up to 32, 64, 128 or 256. Bound by latency
 // (convolution, products, store, one after the other): 128 blocks, state 128, 64 heads 23 us.
-template <class T, int kN, bool kSplit>
+template <class T, int kN>
 __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int parts) {
-  using Block = ScanBlock<kN, kSplit>;
+  using Block = ScanBlock<kN>;
   constexpr int kCols = 2 * kN, kRow = kCols + 2;  // a row's pad: eight rows on lies 16 banks on
   extern __shared__ float u[];                     // [64][kRow]: the convolved B, then C
   __shared__ float red[3][8];
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);  // zero for a sequence without rows
   if (part > 0) {
     const int each = a.H / a.G, n = ((part - 1) * 8 + wave) * kScanHeads;
-    if (n < each) scan_steps<T, kSplit>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
+    if (n < each) scan_steps<T, sizeof(T) == 4>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
     return;
   }
   int slot = -1, pos = 0;
@@ -541,7 +541,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
       if (step == 0 && (at.y > 0 || pos > 0)) {
         f16x8* const to = reinterpret_cast<f16x8*>(out + Block::kOffC) + (strip * (kN / 32) + k) * 64 + lane;
         to[0] = ch[k];
-        if (kSplit) to[4 * (kN / 32) * 64] = cl[k];
+        to[4 * (kN / 32) * 64] = cl[k];
       }
     }
     f32x4 acc[2];
@@ -651,16 +651,16 @@ __device__ __forceinline__ int scan_place(int p) { return ((p ^ (p >> 2)) & 3) |
 // channel 16 m + l16, the tiles shared among the waves, and y at token 16 i + l16 and channels 16 q + 4 m + e.
 // Loads are issued a phase or more before their use: a block's time is otherwise theirs, one after the other.
 // z and y, each met once, go past the caches, which keeps x there for the second run (1 x 8,192 tokens: 10 us less).
-template <class T, int kN, bool kSplit, bool kFirstRun>
+template <class T, int kN, bool kFirstRun>
 __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   constexpr bool first_run = kFirstRun;
-  using Block = ScanBlock<kN, kSplit>;
+  using Block = ScanBlock<kN>;
   constexpr int kTiles = kN / 16 >= 4 ? kN / 64 : 1;  // column tiles of a wave
   constexpr int kCh = kN / 16 >= 4 ? 4 : 2;           // channel tiles of a wave
-  constexpr int kHalves = kSplit ? 2 : 1;
-  __shared__ _Float16 xt[kHalves][64 * 64], xw[2][64 * 64], hs[kHalves][64 * kN];  // by channel: x, faded x, state
+  constexpr bool kRests = sizeof(T) == 4;
+  __shared__ _Float16 xt[2][64 * 64], xw[2][64 * 64], hs[2][64 * kN];  // by channel: x, faded x, state
   // by token, for this block and the next: s, r, faded step, and what s and r lack; totals and scales
-  __shared__ float tokens[2][kSplit ? 5 : 3][64], red[4];
+  __shared__ float tokens[2][kRests ? 5 : 3][64], red[4];
   __shared__ float4 sums[2][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
@@ -804,7 +804,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     const int64_t at_head = static_cast<int64_t>(sq.block0 + nth) * a.H + h;
     if (wave == 0) {
       early = w.steps[at_head * 64 + lane];
-      if (kSplit) early_rest = w.rests[at_head * 64 + lane];
+      if (kRests) early_rest = w.rests[at_head * 64 + lane];
     }
     if (wave == 1) early = *(lane == 0 ? w.totals + at_head : reinterpret_cast<const float4*>(operands(nth) + Block::kOffScale));
   };
@@ -821,13 +821,13 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     float* const ts = tokens[nth & 1][0];
     float* const tr = tokens[nth & 1][1];
     float* const tw = tokens[nth & 1][2];
-    float* const tl = tokens[nth & 1][kSplit ? 3 : 0];
-    float* const tq = tokens[nth & 1][kSplit ? 4 : 0];
+    float* const tl = tokens[nth & 1][kRests ? 3 : 0];
+    float* const tq = tokens[nth & 1][kRests ? 4 : 0];
     if (wave == 0) {
       ts[lane] = early.x;
       tr[lane] = early.y;
       tw[lane] = early.z;
-      if (kSplit) {
+      if (kRests) {
         tl[lane] = early.w;
         tq[lane] = early_rest;
       }
@@ -861,7 +861,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     }
     // operands of y: C B^T (of a strip's first 16 (wave 0: 16, 1: 32, 2: 48, 3: 64) tokens) and C
     f32x4 cbs[2][2];
-    f16x8 chs[kN / 32], cls[kSplit ? kN / 32 : 1];
+    f16x8 chs[kN / 32], cls[kN / 32];
     if (!first_run) {
       const f32x4* const cbf = reinterpret_cast<const f32x4*>(in) + (wave * 2 * 64 + lane) * 2;
 #pragma unroll
@@ -872,7 +872,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 #pragma unroll
       for (int k = 0; k < kN / 32; ++k) {
         chs[k] = cf[k * 64];
-        if (kSplit) cls[k] = cf[(4 * (kN / 32) + k) * 64];
+        cls[k] = cf[(4 * (kN / 32) + k) * 64];
       }
     }
     float u[4][4], most = 0.f;  // [token][channel]
@@ -913,7 +913,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         }
         if (!first_run) {
           *reinterpret_cast<f16x4*>(&xt[0][to]) = hi;
-          if (kSplit) *reinterpret_cast<f16x4*>(&xt[kHalves - 1][to]) = lo;
+          *reinterpret_cast<f16x4*>(&xt[1][to]) = lo;
         }
         if (keep) {
           *reinterpret_cast<f16x4*>(&xw[0][to]) = wh;
@@ -938,7 +938,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
             lo[e] = vl;
           }
           *reinterpret_cast<f16x4*>(&hs[0][to]) = hi;
-          if (kSplit) *reinterpret_cast<f16x4*>(&hs[kHalves - 1][to]) = lo;
+          *reinterpret_cast<f16x4*>(&hs[1][to]) = lo;
         }
     }
     __syncthreads();
@@ -962,23 +962,21 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           far_at[m][odd] = p * kN + (((4 * odd + lq) ^ (f & (kN / 8 - 1))) << 3);
         }
       }
-      const float si = ts[i], li = kSplit ? tl[i] : 0.f;
+      const float si = ts[i], li = kRests ? tl[i] : 0.f;
       f32x4 far[4], near[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) far[m] = near[m] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (has) {
 #pragma unroll
         for (int k = 0; k < kN / 32; ++k) {
-          const f16x8 ch = chs[k], cl = cls[kSplit ? k : 0];
+          const f16x8 ch = chs[k], cl = cls[k];
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int from = far_at[m][k & 1] + (k >> 1) * 64;
             const f16x8 hh = *reinterpret_cast<const f16x8*>(&hs[0][from]);
             far[m] = mma16(hh, ch, far[m]);
-            if (kSplit) {
-              far[m] = mma16(hh, cl, far[m]);
-              far[m] = mma16(*reinterpret_cast<const f16x8*>(&hs[kHalves - 1][from]), ch, far[m]);
-            }
+            far[m] = mma16(hh, cl, far[m]);
+            far[m] = mma16(*reinterpret_cast<const f16x8*>(&hs[1][from]), ch, far[m]);
           }
         }
       }
@@ -994,16 +992,16 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           const int j0 = 32 * step + 8 * lq + 4 * half;
           const f32x4 rj = *reinterpret_cast<const f32x4*>(tr + j0);
           f32x4 qj = {0.f, 0.f, 0.f, 0.f};
-          if (kSplit) qj = *reinterpret_cast<const f32x4*>(tq + j0);
+          if (kRests) qj = *reinterpret_cast<const f32x4*>(tq + j0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float fall = kSplit ? (si - rj[e]) + (li - qj[e]) : si - rj[e];
+            const float fall = kRests ? (si - rj[e]) + (li - qj[e]) : si - rj[e];
             float v = cbs[step][half][e] * fm * __builtin_amdgcn_exp2f(fall);
             if (step == wave >> 1) v = j0 + e < i ? v : (j0 + e == i ? v + own : 0.f);  // tokens after i, and i itself
             _Float16 vh, vl;
             split_half(v, vh, vl);
             mh[4 * half + e] = vh;
-            if (kSplit) ml[4 * half + e] = vl;
+            ml[4 * half + e] = vl;
           }
         }
 #pragma unroll
@@ -1011,10 +1009,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           const int from = near_at[m][step];
           const f16x8 xh = *reinterpret_cast<const f16x8*>(&xt[0][from]);
           near[m] = mma16(xh, mh, near[m]);
-          if (kSplit) {
-            near[m] = mma16(xh, ml, near[m]);
-            near[m] = mma16(*reinterpret_cast<const f16x8*>(&xt[kHalves - 1][from]), mh, near[m]);
-          }
+          near[m] = mma16(xh, ml, near[m]);
+          near[m] = mma16(*reinterpret_cast<const f16x8*>(&xt[1][from]), mh, near[m]);
         }
       }
       if (i < L) {

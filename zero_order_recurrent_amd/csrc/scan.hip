@@ -127,12 +127,12 @@ struct Plan {
 
 constexpr int kPieceWorkgroups = 512;  // two for each of 256 compute units
 
-size_t block_bytes(int kn, bool split) {
+size_t block_bytes(int kn) {
   switch (kn) {
-    case 32: return split ? ScanBlock<32, true>::kBytes : ScanBlock<32, false>::kBytes;
-    case 64: return split ? ScanBlock<64, true>::kBytes : ScanBlock<64, false>::kBytes;
-    case 128: return split ? ScanBlock<128, true>::kBytes : ScanBlock<128, false>::kBytes;
-    default: return split ? ScanBlock<256, true>::kBytes : ScanBlock<256, false>::kBytes;
+    case 32: return ScanBlock<32>::kBytes;
+    case 64: return ScanBlock<64>::kBytes;
+    case 128: return ScanBlock<128>::kBytes;
+    default: return ScanBlock<256>::kBytes;
   }
 }
 
@@ -159,7 +159,7 @@ Plan make_plan(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs, boo
     at = align_up(at + bytes);
     return here;
   };
-  p.blocks = region(block_bytes(p.kn, c->dtype == CDRGE_F32) * blocks * c->n_groups);
+  p.blocks = region(block_bytes(p.kn) * blocks * c->n_groups);
   p.steps = region(sizeof(float4) * 64 * blocks * c->n_heads);
   if (c->dtype == CDRGE_F32) p.rests = region(sizeof(float) * 64 * blocks * c->n_heads);
   p.totals = region(sizeof(float4) * blocks * c->n_heads);
@@ -202,7 +202,6 @@ ScanWork make_work(const Plan& p, void* ws) {
 
 template <class T, int kN>
 cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pieces, hipStream_t s) {
-  constexpr bool kSplit = sizeof(T) == 4;
   a.ptiles = p.ptiles;
   if (a.offsets) {
     hipLaunchKernelGGL(k_scan_map, dim3(1), dim3(1024), 0, s, a, w);
@@ -214,20 +213,20 @@ cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pi
     int dev = 0;
     CDRGE_HIP(hipGetDevice(&dev));
     if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
-      CDRGE_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k_scan_blocks<T, kN, kSplit>),
+      CDRGE_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k_scan_blocks<T, kN>),
                                     hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
       ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
     }
   }
   const int parts = 1 + (a.H / a.G + 8 * kScanHeads - 1) / (8 * kScanHeads);
-  hipLaunchKernelGGL((k_scan_blocks<T, kN, kSplit>), grid_of(int64_t(p.max_blocks) * a.G * parts, 512), dim3(512), kLds, s, a, w, parts);
+  hipLaunchKernelGGL((k_scan_blocks<T, kN>), grid_of(int64_t(p.max_blocks) * a.G * parts, 512), dim3(512), kLds, s, a, w, parts);
   CDRGE_HIP(hipGetLastError());
   const dim3 grid = grid_of(int64_t(p.max_pieces) * a.H * p.ptiles, 256);
   if (pieces) {
-    hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit, true>), grid, dim3(256), 0, s, a, w);
+    hipLaunchKernelGGL((k_scan_heads<T, kN, true>), grid, dim3(256), 0, s, a, w);
     CDRGE_HIP(hipGetLastError());
   }
-  hipLaunchKernelGGL((k_scan_heads<T, kN, kSplit, false>), grid, dim3(256), 0, s, a, w);
+  hipLaunchKernelGGL((k_scan_heads<T, kN, false>), grid, dim3(256), 0, s, a, w);
   CDRGE_HIP(hipGetLastError());
   if (a.conv_in) {
     const int cblocks = (a.C + 255) / 256;
