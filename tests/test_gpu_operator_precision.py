@@ -50,3 +50,63 @@ def test_prompts(shape, lengths):
     assert off(y, want) <= bound(c.dtype, SCAN)
     for i in range(n):
         assert off(ssm[i], carried[i][0]) <= SCAN
+
+
+def steps_and_decays(c, steps, decay):
+    """Makes the case's tokens take these steps ([tokens], every head) with one decay; the definition's y in 64 bits, for
+    equal sequences that start at zero. (A softplus that holds for any step, which exp does not from 709 on.)"""
+    H, P, G, N = c.dims
+    raw = torch.as_tensor(steps, dtype=torch.float32).expm1().log().where(torch.as_tensor(steps) < 30, torch.as_tensor(steps, dtype=torch.float32))
+    c.dt.copy_(raw[:, None].expand(-1, H))
+    c.dt_bias, c.decay = None, torch.full((H,), float(decay))
+    dt = c.dt.double()
+    step = dt.clamp(min=0) + torch.log1p(torch.exp(-dt.abs()))
+    y, each = torch.zeros(c.tokens, H, P, dtype=torch.float64), c.tokens // c.n
+    for i in range(c.n):
+        x = torch.cat([torch.zeros(c.width - 1, c.ch, dtype=torch.float64), c.xbc[i * each:i * each + each].double()])
+        u = c.cb.double() + sum(x[j:j + each] * c.cw[:, j].double() for j in range(c.width))
+        u = u * torch.sigmoid(u)
+        S = torch.zeros(H, P, N, dtype=torch.float64)
+        for t in range(each):
+            at = i * each + t
+            X, B, C = u[t, :c.d].view(H, P), *(u[t, o:o + G * N].view(G, N).repeat_interleave(H // G, 0) for o in (c.d, c.d + G * N))
+            S = S * torch.exp(step[at] * c.decay.double())[:, None, None] + (step[at][:, None] * X)[:, :, None] * B[:, None, :]
+            y[at] = (S * C[:, None]).sum(2) + c.skip.double()[:, None] * X
+    gate = c.z.double()
+    return y.view(c.tokens, -1) * gate * torch.sigmoid(gate)
+
+
+@pytest.mark.parametrize("step, decay", [(50, -16), (200, -16), (1000, -16), (5000, -16), (20, -64), (10, -1000), (100, -1000), (1e-3, -0.01)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs, each", [(1, 200), (5, 12)])  # in blocks, and in the kernel for short ones
+def test_prompts_with_long_steps(dtype, step, decay, seqs, each):
+    """Long steps leave nothing of what was before: a token's own weight, its step, has to come out as exact as ever. Token
+    by token the same."""
+    c = Case(dtype, 2, 64, 1, 32, 4, tokens=seqs * each, seqs=seqs, slots=seqs, seed=4)
+    want = steps_and_decays(c, [float(step)] * c.tokens, decay)
+    xbc, dt, z = c.rows()
+    layer = c.layer()
+    y = layer.prompt(xbc, dt, c.y(), seqs, z=z)
+    assert off(y, want) <= bound(dtype, SCAN)
+    conv, ssm, alone = c.conv.cuda(), c.ssm.cuda(), c.y()
+    for t in range(each):
+        at = slice(t, None, each)
+        layer.step(xbc[at], dt[at], alone[at], ints([t] * seqs), conv, ssm, z=z[at])
+    assert off(alone, want) <= bound(dtype, SCAN)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("each, far", [(60, 20), (15, 4)])
+def test_prompt_with_one_far_step(dtype, each, far):
+    """One token of a step beyond all others: the decays behind it are as exact as before it."""
+    c = Case(dtype, 2, 64, 1, 32, 4, tokens=each, seqs=1, seed=5)
+    steps = [1.0] * each
+    steps[far] = 1e20
+    want = steps_and_decays(c, steps, -0.1)
+    xbc, dt, z = c.rows()
+    y = c.layer().prompt(xbc, dt, c.y(), 1, z=z)
+    # What a token's row holds of the far one is e^-4 of it at the least: far above the 2^-38 of the largest weight that
+    # operands are rounded to.
+    for t in range(far, each):
+        err = (y[t].double().cpu() - want[t]).norm() / want[t].norm()
+        assert err <= ref.HALF_STEP[dtype] + 2 * SCAN, t  # 128 outputs scatter more than thousands

@@ -257,7 +257,7 @@ struct ScanBlock {
 struct ScanWork {  // the workspace
   char* blocks;      // [block][group]
   float4* steps;     // [block][head][64]: s, r = s - log2(step), 2^(s_last - s) step, what s lacks below float32
-  float* rests;      // [block][head][64]: what r lacks below float32 (float32 tensors)
+  float* rests;      // [block][head][64]: what r lacks below float32
   float4* totals;    // [block][head]: s_last, largest step, largest and sum of 2^(s_last - s) step
   int32_t* slots;    // [sequence]: scan_slot
   int32_t* counts;   // blocks and pieces in all
@@ -397,10 +397,18 @@ __device__ __forceinline__ void scan_operand(const float* row, float scale, f16x
   }
 }
 
+// A token's decay in units of log 2. Past +-400 the state's factor is zero or infinite in float32 whatever it meets,
+// so it stays there: the sums of a block's tokens are below 2^15 however long a step is, and the differences of two of
+// them, each held as a float32 and what that lacks, are exact to 2^-33.
+__device__ __forceinline__ double scan_log_decay(float step, float decay) {
+  const double a = static_cast<double>(step) * static_cast<double>(decay) * 1.4426950408889634;
+  return a < -400.0 ? -400.0 : (a > 400.0 ? 400.0 : a);
+}
+
 // Steps and decays of a block's heads: a wave takes kScanHeads heads, lane = token, with the loads of all
 // of them in flight together.
 constexpr int kScanHeads = 2;
-template <class T, bool kRest>
+template <class T>
 __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w, int block, int64_t row0, int L, int h0, int h1) {
   const int lane = threadIdx.x & 63;
   float raw[kScanHeads];
@@ -412,7 +420,7 @@ __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w,
     const int h = h0 + n;
     if (h >= h1) break;
     const float step = lane < L ? softplus(raw[n] + (a.dt_bias ? a.dt_bias[h] : 0.f)) : 0.f;
-    double sum = static_cast<double>(step) * static_cast<double>(a.decay[h]) * 1.4426950408889634;
+    double sum = scan_log_decay(step, a.decay[h]);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
       const double o = __shfl_up(sum, m);
@@ -427,7 +435,7 @@ __device__ __forceinline__ void scan_steps(const ScanArgs& a, const ScanWork& w,
     const float left = lane < L ? step * __builtin_amdgcn_exp2f(static_cast<float>(last - sum)) : 0.f;
     const int64_t at_head = static_cast<int64_t>(block) * a.H + h;
     w.steps[at_head * 64 + lane] = make_float4(s, r, left, rest_s);
-    if (kRest) w.rests[at_head * 64 + lane] = rest_r;
+    w.rests[at_head * 64 + lane] = rest_r;
     const float most_step = wave_max(step), most_left = wave_max(left), all_left = wave_sum(left);
     if (lane == 0) w.totals[at_head] = make_float4(static_cast<float>(last), most_step, most_left, all_left);
   }
@@ -452,7 +460,7 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);  // zero for a sequence without rows
   if (part > 0) {
     const int each = a.H / a.G, n = ((part - 1) * 8 + wave) * kScanHeads;
-    if (n < each) scan_steps<T, sizeof(T) == 4>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
+    if (n < each) scan_steps<T>(a, w, block, row0, L, g * each + n, min(g * each + n + kScanHeads, g * each + each));
     return;
   }
   int slot = -1, pos = 0;
@@ -657,10 +665,9 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   using Block = ScanBlock<kN>;
   constexpr int kTiles = kN / 16 >= 4 ? kN / 64 : 1;  // column tiles of a wave
   constexpr int kCh = kN / 16 >= 4 ? 4 : 2;           // channel tiles of a wave
-  constexpr bool kRests = sizeof(T) == 4;
   __shared__ _Float16 xt[2][64 * 64], xw[2][64 * 64], hs[2][64 * kN];  // by channel: x, faded x, state
   // by token, for this block and the next: s, r, faded step, and what s and r lack; totals and scales
-  __shared__ float tokens[2][kRests ? 5 : 3][64], red[4];
+  __shared__ float tokens[2][5][64], red[4];
   __shared__ float4 sums[2][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
   const int tile0 = kN / 16 >= 4 ? wave * kTiles : wave & 1, ch0 = kN / 16 >= 4 ? 0 : (wave >> 1) * 2;
@@ -804,7 +811,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     const int64_t at_head = static_cast<int64_t>(sq.block0 + nth) * a.H + h;
     if (wave == 0) {
       early = w.steps[at_head * 64 + lane];
-      if (kRests) early_rest = w.rests[at_head * 64 + lane];
+      early_rest = w.rests[at_head * 64 + lane];
     }
     if (wave == 1) early = *(lane == 0 ? w.totals + at_head : reinterpret_cast<const float4*>(operands(nth) + Block::kOffScale));
   };
@@ -821,16 +828,14 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     float* const ts = tokens[nth & 1][0];
     float* const tr = tokens[nth & 1][1];
     float* const tw = tokens[nth & 1][2];
-    float* const tl = tokens[nth & 1][kRests ? 3 : 0];
-    float* const tq = tokens[nth & 1][kRests ? 4 : 0];
+    float* const tl = tokens[nth & 1][3];
+    float* const tq = tokens[nth & 1][4];
     if (wave == 0) {
       ts[lane] = early.x;
       tr[lane] = early.y;
       tw[lane] = early.z;
-      if (kRests) {
-        tl[lane] = early.w;
-        tq[lane] = early_rest;
-      }
+      tl[lane] = early.w;
+      tq[lane] = early_rest;
     }
     if (wave == 1 && lane < 2) sums[nth & 1][lane] = early;
     // operands of the state; the first run has nothing else to do meanwhile, so it asks for them here
@@ -962,7 +967,7 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
           far_at[m][odd] = p * kN + (((4 * odd + lq) ^ (f & (kN / 8 - 1))) << 3);
         }
       }
-      const float si = ts[i], li = kRests ? tl[i] : 0.f;
+      const float si = ts[i], li = tl[i];
       f32x4 far[4], near[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) far[m] = near[m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -991,11 +996,10 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
         for (int half = 0; half < 2; ++half) {
           const int j0 = 32 * step + 8 * lq + 4 * half;
           const f32x4 rj = *reinterpret_cast<const f32x4*>(tr + j0);
-          f32x4 qj = {0.f, 0.f, 0.f, 0.f};
-          if (kRests) qj = *reinterpret_cast<const f32x4*>(tq + j0);
+          const f32x4 qj = *reinterpret_cast<const f32x4*>(tq + j0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float fall = kRests ? (si - rj[e]) + (li - qj[e]) : si - rj[e];
+            const float fall = (si - rj[e]) + (li - qj[e]);
             float v = cbs[step][half][e] * fm * __builtin_amdgcn_exp2f(fall);
             if (step == wave >> 1) v = j0 + e < i ? v : (j0 + e == i ? v + own : 0.f);  // tokens after i, and i itself
             _Float16 vh, vl;
@@ -1226,7 +1230,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(Scan
         x[t][c] = (4 * q + t < len && 4 * l16 + c < now.np) ? silu(v) : 0.f;
       }
     const float step = l16 < len ? softplus(now.dt + now.bias) : 0.f, skip = now.skip;
-    double s = static_cast<double>(step) * static_cast<double>(now.decay) * 1.4426950408889634;
+    double s = scan_log_decay(step, now.decay);
 #pragma unroll
     for (int m = 1; m < 16; m <<= 1) {
       const double o = __shfl_up(s, m, 16);

@@ -161,7 +161,7 @@ Plan make_plan(const cdrge_scan_config* c, int64_t n_tokens, int32_t n_seqs, boo
   };
   p.blocks = region(block_bytes(p.kn) * blocks * c->n_groups);
   p.steps = region(sizeof(float4) * 64 * blocks * c->n_heads);
-  if (c->dtype == CDRGE_F32) p.rests = region(sizeof(float) * 64 * blocks * c->n_heads);
+  p.rests = region(sizeof(float) * 64 * blocks * c->n_heads);
   p.totals = region(sizeof(float4) * blocks * c->n_heads);
   p.slots = region(sizeof(int32_t) * n_seqs);
   if (!equal) {
