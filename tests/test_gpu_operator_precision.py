@@ -10,6 +10,7 @@ import torch
 
 import operators_ref as ref
 from test_gpu_scan import Case, ints
+from zero_order_recurrent_amd import binding as b
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,52 @@ def test_prompt_with_one_far_step(dtype, each, far):
     for t in range(far, each):
         err = (y[t].double().cpu() - want[t]).norm() / want[t].norm()
         assert err <= ref.HALF_STEP[dtype] + 2 * SCAN, t  # 128 outputs scatter more than thousands
+
+
+def distill(logits, ids, teacher, tau):
+    n, V = logits.shape
+    op = b.DistillLoss(b.make_distill_config(V, ids.shape[1], 1, tau, "bf16" if logits.dtype == torch.bfloat16 else "f32"))
+    row, d = torch.empty(n, device="cuda"), torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
+    op.grad(logits.cuda(), ids.cuda(), teacher.cuda(), None, row, None, d)
+    z, t = logits.double() / tau, teacher.double() / tau
+    logq, logp = torch.log_softmax(z, 1), torch.log_softmax(t, 1)
+    q, p = torch.exp(logq), torch.exp(logp)
+    at = torch.gather(logq, 1, ids.long())
+    want = tau * tau * torch.where(p > 0, p * (logp - at), torch.zeros_like(p)).sum(1)
+    grad = tau * q.scatter_add(1, ids.long(), -p)
+    # A logit's distance from the largest is rounded once, scaled by a factor that is off by two roundings and rounded
+    # again: four of 2^-24 of the exponent, four of the teacher's. Sums of V and k terms, their logarithms, products:
+    # V / 64 + 64 more. An exponential is off by its exponent's error times itself.
+    near = lambda v: torch.where(torch.isfinite(v), v.abs(), torch.zeros_like(v))  # noqa: E731
+    each = 4 * (near(at) + near(logp)) + V / 64 + 64 + near(at) + near(logp)
+    tol = tau * tau * 2 ** -24 * torch.where(p > 0, p * (4 * near(logp) + 1) * each, torch.zeros_like(p)).sum(1) + 1e-38
+    assert ((row.double().cpu() - want).abs() <= tol).all()
+    mass = torch.zeros_like(q).scatter_add(1, ids.long(), p * (4 * near(logp) + V / 64 + 64))
+    gtol = ref.HALF_STEP["bf16" if logits.dtype == torch.bfloat16 else "f32"] * grad.abs() + tau * 2 ** -24 * (
+        q * (4 * near(logq) + V / 64 + 64) + mass) + 1e-38
+    assert ((d.double().cpu() - grad).abs() <= gtol).all()
+
+
+@pytest.mark.parametrize("tau", [2.0 ** e for e in (-60, -40, -30, -28, -20, -10, 10, 20, 40, 60)])
+@pytest.mark.parametrize("V", [50, 3000, 140000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_distill_at_every_temperature(dtype, V, tau):
+    g = torch.Generator().manual_seed(V)
+    logits = (torch.randn(4, V, generator=g) * 2).to(dtype)
+    ids = torch.stack([torch.randperm(V, generator=g)[:7] for _ in range(4)]).to(torch.int32)
+    ids[0, 0] = logits[0].float().argmax()
+    ids[0, 1:] = (ids[0, 0] + torch.arange(1, 7)) % V
+    teacher = torch.randn(4, 7, generator=g) * 3
+    teacher[0, 0] = 20.0  # the teacher is as sure as the student, and of the same
+    distill(logits, ids, teacher, tau)
+
+
+@pytest.mark.parametrize("offset", [3e4, -3e4, 1.1e10, -3.3e10, 1.7e18])
+def test_distill_far_from_zero(offset):
+    """What all logits have in common does not count."""
+    g = torch.Generator().manual_seed(1)
+    logits = torch.randn(5, 700, generator=g) * 2 + offset
+    ids = torch.stack([torch.randperm(700, generator=g)[:9] for _ in range(5)]).to(torch.int32)
+    ids[:, 0] = logits.argmax(1)
+    ids[:, 1:] = (ids[:, :1] + torch.arange(1, 9)) % 700
+    distill(logits, ids, torch.randn(5, 9, generator=g), 1.0)

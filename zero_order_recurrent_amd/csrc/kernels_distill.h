@@ -109,21 +109,21 @@ __device__ __forceinline__ void piece_max(uint4 r, float& m) {
   for (int i = 0; i < int(16 / sizeof(T)); ++i) m = fmaxf(m, to_float(e[i]));
 }
 template <class T>
-__device__ __forceinline__ float piece_sum(uint4 r, float shift, float scale) {
+__device__ __forceinline__ float piece_sum(uint4 r, float most, float scale) {
   T e[16 / sizeof(T)];
   __builtin_memcpy(e, &r, 16);
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < int(16 / sizeof(T)); ++i) s += __builtin_amdgcn_exp2f(__builtin_fmaf(to_float(e[i]), scale, shift));
+  for (int i = 0; i < int(16 / sizeof(T)); ++i) s += __builtin_amdgcn_exp2f((to_float(e[i]) - most) * scale);
   return s;
 }
 template <class T>
-__device__ __forceinline__ uint4 piece_grad(uint4 r, float shift, float scale, float up) {
+__device__ __forceinline__ uint4 piece_grad(uint4 r, float most, float scale, float up) {
   T e[16 / sizeof(T)];
   __builtin_memcpy(e, &r, 16);
 #pragma unroll
   for (int i = 0; i < int(16 / sizeof(T)); ++i)
-    e[i] = from_float<T>(up * __builtin_amdgcn_exp2f(__builtin_fmaf(to_float(e[i]), scale, shift)));
+    e[i] = from_float<T>(up * __builtin_amdgcn_exp2f((to_float(e[i]) - most) * scale));
   __builtin_memcpy(&r, e, 16);
   return r;
 }
@@ -188,24 +188,25 @@ __global__ __launch_bounds__(distill_threads(kTeam), distill_waves(kTeam, kPiece
   team_reduce<kTeam, true, 4>(most, part);
   const bool present = most[2] > 0.f, bad = most[3] > 0.f;
   const float tmax = most[0];
-  // logits enter as x scale + shift: in units of log 2, the largest at (about) zero
-  const float shift = most[1] == ninf ? 0.f : -(most[1] * scale);
+  // Logits enter as (x - M) scale, in units of log 2, the largest at zero. As x scale - M scale, one instruction less,
+  // all would be off by the rounding of M scale, which at |M| / tau of 2^31 passes the exponents' whole range.
+  const float top = most[1] == ninf ? 0.f : most[1];
 
   float sums[2] = {0.f, 0.f};  // the student's exponentials, the teacher's
   if (kPieces > 0) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      if (lane + i * kTeam < at.pieces) sums[0] += piece_sum<T>(held[i], shift, scale);
+      if (lane + i * kTeam < at.pieces) sums[0] += piece_sum<T>(held[i], top, scale);
       __builtin_amdgcn_sched_barrier(0);  // piece by piece: temporaries of one, not of all
     }
   } else {
-    for (int b = lane; b < at.pieces; b += kTeam) sums[0] += piece_sum<T>(at.load(x, b), shift, scale);
+    for (int b = lane; b < at.pieces; b += kTeam) sums[0] += piece_sum<T>(at.load(x, b), top, scale);
   }
   for (int j = lane; j < k; j += kTeam) sums[1] += id[j] >= 0 ? expf((prob[j] - tmax) * inv_tau) : 0.f;
   team_reduce<kTeam, false, 2>(sums, part + 4 * 16);
   const float log_sum = logf(sums[0]), log_mass = logf(sums[1]);
 
-  float loss[1] = {0.f}, mine[kOwn];  // mine: x scale + shift at this thread's teacher entries
+  float loss[1] = {0.f}, mine[kOwn];  // mine: (x - M) scale at this thread's teacher entries
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int j = lane + i * kTeam;
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(distill_threads(kTeam), distill_waves(kTeam, kPiece
     const float lp = (prob[j] - tmax) * inv_tau - log_mass;
     const float p = id[j] >= 0 ? expf(lp) : 0.f;
     if (id[j] >= 0 && id[j] < V) {
-      mine[i] = __builtin_fmaf(to_float(x[id[j]]), scale, shift);
+      mine[i] = (to_float(x[id[j]]) - top) * scale;
       // a probability that underflows contributes its limit, zero
       if (!(p == 0.f)) loss[0] += p * (lp - mine[i] * 0.693147180559945309417f + log_sum);
     }
@@ -237,11 +238,11 @@ __global__ __launch_bounds__(distill_threads(kTeam), distill_waves(kTeam, kPiece
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int b = lane + i * kTeam;
-        if (b < at.pieces) at.store(d, b, piece_grad<T>(held[i], shift, scale, up_q));
+        if (b < at.pieces) at.store(d, b, piece_grad<T>(held[i], top, scale, up_q));
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      for (int b = lane; b < at.pieces; b += kTeam) at.store(d, b, piece_grad<T>(at.load(x, b), shift, scale, up_q));
+      for (int b = lane; b < at.pieces; b += kTeam) at.store(d, b, piece_grad<T>(at.load(x, b), top, scale, up_q));
     }
     team_sync<kTeam>();
 #pragma unroll
