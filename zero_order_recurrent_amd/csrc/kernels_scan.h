@@ -40,6 +40,7 @@ struct ScanArgs {
   int n_seqs, n_slots;
   int H, P, G, N, W, C;  // C: channels = H P + 2 G N
   int ptiles;            // column tiles of a head
+  bool owned;            // whether k_scan_owners or k_scan_mark looks for slots that are named twice
 };
 
 // Slot of sequence i: -1 if it keeps no state, -2 if the slot is out of range or an earlier
@@ -52,6 +53,59 @@ __device__ __forceinline__ int scan_slot(const ScanArgs& a, int i) {
   if (a.slots)
     for (int j = threadIdx.x; j < i; j += blockDim.x) taken |= a.slots[j] == s;
   return __syncthreads_or(taken) ? -2 : s;
+}
+
+// Slots that are named twice, in calls of many sequences, are looked for in a launch of its own; in others every
+// workgroup reads the earlier slots for itself, beside its other loads: by scan_owned, from 2^28 pairs of a workgroup
+// and a sequence on. 16 heads of 16 x 16, single tokens: 4,096 rows 182 us in two launches and 210 in one, 2,048 95 in
+// one, 262,144 12.6 and 137 ms; one head of 4 x 4: 4,096 rows 26 and 18 us, 16,384 65 and 82; prompts of one token:
+// 262,144 sequences 9.9 and 23.9 ms. Every pair is compared, 0.3 ms for 65,536 rows.
+constexpr int kScanOwnerWaves = 16;
+inline bool scan_owned(const int32_t* slots, int n_seqs, int64_t readers) {
+  return slots && readers * n_seqs >= (int64_t(1) << 28);
+}
+
+// Of the 64 sequences from i0 on (a multiple of 64), those whose slots earlier ones of the call name, a bit each: lane =
+// sequence, and the waves share the earlier slots, which are the same for all lanes and compared as scalars.
+__device__ __forceinline__ uint64_t scan_taken(const ScanArgs& a, int i0, int slot) {
+  __shared__ uint64_t found[kScanOwnerWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint64_t taken = 0;
+  for (int j = 16 * wave; j < i0; j += 16 * kScanOwnerWaves) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) taken |= __ballot(slot == a.slots[j + e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 64 / kScanOwnerWaves; ++e) {
+    const int j = wave * (64 / kScanOwnerWaves) + e;
+    taken |= __ballot(slot == __builtin_amdgcn_readlane(slot, j) && j < lane);
+  }
+  if (lane == 0) found[wave] = taken;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kScanOwnerWaves; ++v) taken |= found[v];
+  return taken;
+}
+
+// Prompts: the sequences' slots as scan_slot has them.
+static __global__ __launch_bounds__(64 * kScanOwnerWaves) void k_scan_owners(ScanArgs a, int32_t* slots) {
+  const int i0 = blockIdx.x * 64, lane = threadIdx.x & 63, i = i0 + lane;
+  const int slot = i < a.n_seqs ? a.slots[i] : -1;
+  const uint64_t taken = scan_taken(a, i0, slot);
+  if (threadIdx.x < 64 && i < a.n_seqs) slots[i] = slot < 0 ? -1 : (slot >= a.n_slots || (taken >> lane & 1) ? -2 : slot);
+}
+
+// Single tokens, which have no workspace: each workgroup of k_scan_step finds in its own first place of y, which it
+// writes afterwards, NaN if an earlier row has the slot and zero if none has.
+template <class T>
+__global__ __launch_bounds__(64 * kScanOwnerWaves) void k_scan_mark(ScanArgs a, int tile) {
+  const int i0 = blockIdx.x * 64, lane = threadIdx.x & 63, i = i0 + lane;
+  const int slot = i < a.n_seqs ? a.slots[i] : -1;
+  const uint64_t taken = scan_taken(a, i0, slot);
+  if (slot < 0) return;
+  T* const y = static_cast<T*>(a.y) + i * a.y_stride;
+  for (int n = threadIdx.x >> 6; n < a.H * a.ptiles; n += kScanOwnerWaves)
+    y[n / a.ptiles * a.P + n % a.ptiles * tile] = from_float<T>(taken >> lane & 1 ? __builtin_nanf("") : 0.f);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -84,7 +138,9 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
   }
   // Everything that is read is requested at once; whether the slot is taken is known only further down.
   int taken = 0;
-  if (a.slots)
+  if (a.owned)
+    taken = !(to_float(y[0]) == 0.f);
+  else if (a.slots)
     for (int j = tid; j < i; j += 256) taken |= a.slots[j] == slot;
   const int N = a.N, g = h / (a.H / a.G);
   const bool owns_bc = tile == 0 && h % (a.H / a.G) == 0;
@@ -465,9 +521,9 @@ __global__ __launch_bounds__(512) void k_scan_blocks(ScanArgs a, ScanWork w, int
   }
   int slot = -1, pos = 0;
   if (a.ssm_in) {
-    slot = scan_slot(a, at.x);
+    slot = a.owned ? w.slots[at.x] : scan_slot(a, at.x);
     if (slot >= 0 && a.positions) pos = max(a.positions[at.x], 0);
-    if (at.y == 0 && g == 0 && tid == 0) w.slots[at.x] = slot;
+    if (!a.owned && at.y == 0 && g == 0 && tid == 0) w.slots[at.x] = slot;
   }
 
   // convolution: a thread takes one column of B or C and an equal share of the block's tokens

@@ -82,6 +82,7 @@ ScanArgs make_args(const cdrge_scan_config* c, const cdrge_scan_weights* w, cons
   a.W = c->conv_width;
   a.C = static_cast<int>(channels(c));
   a.ptiles = 1;
+  a.owned = false;
   return a;
 }
 
@@ -93,6 +94,11 @@ cdrge_status launch_step(ScanArgs a, hipStream_t s) {
   a.ptiles = (a.P + kTile - 1) / kTile;
   const int64_t n = int64_t(a.n_seqs) * a.H * a.ptiles;
   if (n > kMostBlocks) return CDRGE_ERR_UNSUPPORTED;
+  a.owned = scan_owned(a.slots, a.n_seqs, n);
+  if (a.owned) {
+    hipLaunchKernelGGL(k_scan_mark<T>, dim3((a.n_seqs + 63) / 64), dim3(64 * kScanOwnerWaves), 0, s, a, kTile);
+    CDRGE_HIP(hipGetLastError());
+  }
   hipLaunchKernelGGL((k_scan_step<T, kLanes, kRpt>), grid_of(n, 256), dim3(256), 0, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
@@ -205,6 +211,11 @@ cdrge_status launch_prompt(ScanArgs a, const Plan& p, const ScanWork& w, bool pi
   a.ptiles = p.ptiles;
   if (a.offsets) {
     hipLaunchKernelGGL(k_scan_map, dim3(1), dim3(1024), 0, s, a, w);
+    CDRGE_HIP(hipGetLastError());
+  }
+  a.owned = scan_owned(a.slots, a.n_seqs, int64_t(p.max_blocks) * a.G);
+  if (a.owned) {
+    hipLaunchKernelGGL(k_scan_owners, dim3((a.n_seqs + 63) / 64), dim3(64 * kScanOwnerWaves), 0, s, a, w.slots);
     CDRGE_HIP(hipGetLastError());
   }
   constexpr size_t kLds = sizeof(float) * kScanBlock * (2 * kN + 2);
