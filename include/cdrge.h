@@ -284,9 +284,10 @@ typedef struct {
   const int32_t* slots;     /* [n_seqs]; NULL: sequence i has slot i */
   const int32_t* positions; /* [n_seqs]: tokens that the slot has seen before this call; zero (or
                                less) starts the sequence at zero whatever the slot holds */
-  const void* conv_in;      /* T [n_slots][conv_width][channels], 16-byte aligned */
+  const void* conv_in;      /* T [n_slots][conv_width][channels] */
   void* conv_out;
-  const float* ssm_in;      /* [n_slots][n_heads][head_dim][state_dim], 16-byte aligned */
+  const float* ssm_in;      /* [n_slots][n_heads][head_dim][state_dim], 16-byte aligned where
+                               state_dim is a multiple of 4 */
   float* ssm_out;
 } cdrge_scan_io;
 

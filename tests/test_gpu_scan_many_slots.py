@@ -86,3 +86,31 @@ def test_many_sequences_take_their_own_time(form, n, heads):
 
     without = seconds(None)
     assert seconds(slots) <= 2 * without + 1e-3
+
+
+@pytest.mark.parametrize("form", ["step", "prompt"])
+@pytest.mark.parametrize("heads, head_dim, state, dtype", [(1, 5, 7, "bf16"), (3, 7, 4, "bf16"), (1, 5, 7, "f32")])
+def test_states_are_a_layer_of_a_cache(form, heads, head_dim, state, dtype):
+    """Layer 1 of a cache of three, which starts at no multiple of 16 bytes: as a cache of its own."""
+    n = 3
+    layer, channels, t, rand = layer_of(heads, head_dim, state, dtype)
+    conv, ssm = rand(3, n, 3, channels).to(t), rand(3, n, heads, head_dim, state)
+    assert conv[1].data_ptr() % 16 != 0 and (ssm[1].data_ptr() % 16 != 0 or state % 4 == 0)
+    rows = n if form == "step" else n * 70
+    xbc, dt = rand(rows, channels).to(t), rand(rows, heads).to(t)
+    positions = torch.tensor([0, 2, 9], device="cuda", dtype=torch.int32)
+
+    def run(c, s):
+        y = torch.empty(rows, heads * head_dim, device="cuda", dtype=t)
+        if form == "step":
+            layer.step(xbc, dt, y, positions, c, s)
+        else:
+            layer.prompt(xbc, dt, y, n, positions=positions, conv_state=c, ssm_state=s)
+        return y
+
+    alone = conv[1].clone(), ssm[1].clone()
+    others = conv[[0, 2]].clone(), ssm[[0, 2]].clone()
+    want = run(*alone)
+    assert torch.isfinite(want).all() and torch.equal(run(conv[1], ssm[1]), want)
+    assert torch.equal(conv[1], alone[0]) and torch.equal(ssm[1], alone[1])
+    assert torch.equal(conv[[0, 2]], others[0]) and torch.equal(ssm[[0, 2]], others[1])

@@ -28,7 +28,7 @@ cdrge_status check_config(const cdrge_scan_config* c) {
   return CDRGE_OK;
 }
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 cdrge_status check_io(const cdrge_scan_config* c, const cdrge_scan_weights* w, const cdrge_scan_io* io) {
   if (!w || !io || !w->conv_weight || !w->decay) return CDRGE_ERR_INVALID_ARG;
@@ -42,7 +42,9 @@ cdrge_status check_io(const cdrge_scan_config* c, const cdrge_scan_weights* w, c
   if (states == 0 && (io->slots || io->positions)) return CDRGE_ERR_INVALID_ARG;
   if (states == 4) {
     if (io->n_slots < 1 || (!io->slots && io->n_slots < io->n_seqs)) return CDRGE_ERR_INVALID_ARG;
-    if (!aligned16(io->conv_in) || !aligned16(io->conv_out) || !aligned16(io->ssm_in) || !aligned16(io->ssm_out))
+    // rings are read by element; rows of whole pieces of the state by piece
+    const size_t element = c->dtype == CDRGE_F32 ? 4 : 2, piece = c->state_dim % 4 == 0 ? 16 : 4;
+    if (!aligned(io->conv_in, element) || !aligned(io->conv_out, element) || !aligned(io->ssm_in, piece) || !aligned(io->ssm_out, piece))
       return CDRGE_ERR_INVALID_ARG;
   }
   if (!io->offsets && io->n_tokens % io->n_seqs != 0) return CDRGE_ERR_INVALID_ARG;
