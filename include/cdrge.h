@@ -236,7 +236,8 @@ size_t cdrge_noalloc_max_workspace_bytes(void);
  * Per token, a row of xbc holds n_heads * head_dim inputs, then n_groups * state_dim entries B,
  * then as many entries C (`channels` in all); dt holds n_heads step sizes before their bias and
  * softplus. Head h belongs to group h / (n_heads / n_groups). With q the token's place in its
- * sequence (positions + index within the call), e = conv_width and sequences starting at zero:
+ * sequence (positions + index within the call), e = conv_width and sequences starting at zero (rows
+ * of xbc before the first are zeros, so a weight that is not finite makes NaN of them):
  *
  *   u_q     = silu(conv_bias + sum_{j < e} conv_weight[:, j] xbc_{q - e + 1 + j})     (x, B, C = u)
  *   step_q  = softplus(dt_q + dt_bias)                                               (by head)

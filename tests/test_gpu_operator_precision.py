@@ -160,3 +160,41 @@ def test_distill_far_from_zero(offset):
     ids[:, 0] = logits.argmax(1)
     ids[:, 1:] = (ids[:, :1] + torch.arange(1, 9)) % 700
     distill(logits, ids, torch.randn(5, 9, generator=g), 1.0)
+
+
+@pytest.mark.parametrize("shape", [("bf16", 2, 64, 1, 32, 4), ("f32", 1, 40, 1, 100, 3), ("bf16", 1, 5, 1, 7, 2)])
+def test_rows_before_a_sequence_are_zeros_in_every_form(shape):
+    """One token at the start of a sequence, weights of the rows before it that are not finite: the same in the kernel for
+    short prompts, in blocks and token by token."""
+    n = 4
+    c = Case(*shape, tokens=n, seqs=n, slots=n, seed=2)
+    c.cw[3, 0], c.cw[c.d + 1, 0], c.cw[-1, -2] = float("inf"), float("nan"), -float("inf")  # in x, in B and in C
+    xbc, dt, z = c.rows()
+    layer, fresh = c.layer(), ints([0] * n)
+    got = [layer.prompt(xbc, dt, c.y(), n, z=z)]
+    for form in ("blocks", "step"):
+        conv, ssm, y = c.conv.cuda(), c.ssm.cuda(), c.y()
+        if form == "blocks":
+            layer.prompt(xbc, dt, y, n, z=z, positions=fresh, conv_state=conv, ssm_state=ssm)
+        else:
+            layer.step(xbc, dt, y, fresh, conv, ssm, z=z)
+        got.append(y)
+    assert torch.isnan(got[0]).any()
+    for y in got[1:]:
+        assert torch.equal(torch.isnan(y), torch.isnan(got[0]))
+
+
+@pytest.mark.parametrize("channel", [3, -1])
+def test_a_channel_that_is_not_finite_stays_alone(channel):
+    """Of x, one channel's weight spoils that channel's outputs alone; of C every output of the group."""
+    c = Case("f32", 2, 20, 2, 24, 4, tokens=2, seqs=2, slots=2, seed=3)
+    c.cw[channel, 0] = float("inf")
+    xbc, dt, z = c.rows()
+    conv, ssm = c.conv.cuda(), c.ssm.cuda()
+    y = c.layer().step(xbc, dt, c.y(), ints([0, 0]), conv, ssm, z=z)
+    bad = torch.zeros(2, 40, dtype=torch.bool)
+    if channel == 3:
+        bad[:, 3] = True
+    else:
+        bad[:, 20:] = True
+    assert torch.equal(torch.isnan(y).cpu(), bad)

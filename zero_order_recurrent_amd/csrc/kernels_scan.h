@@ -192,8 +192,8 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
     if (idx >= np + 2 * N) continue;
     float u = to_float(cb[k]);
 #pragma unroll
-    for (int j = 1; j < kScanMaxConv; ++j)  // a tap before the sequence's start is left out: its weight may be anything
-      if (j < a.W && pos >= j) u += to_float(cw[k][j]) * to_float(past[k][j - 1]);
+    for (int j = 1; j < kScanMaxConv; ++j)  // rows before the sequence's start are zeros
+      if (j < a.W) u += to_float(cw[k][j]) * to_float(past[k][j - 1]);
     u = silu(u + to_float(cw[k][0]) * to_float(now[k]));
     (idx < np ? sx[idx] : (idx < np + N ? sb[idx - np] : sc[idx - np - N])) = u;
   }
