@@ -685,7 +685,7 @@ constexpr int kWaitLoads = 0x0f70;
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, uint4* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)to)));
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(at) : "memory", "m0");
 }
 
 __device__ __forceinline__ int place_x(int row) { return row & 7; }
