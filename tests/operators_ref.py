@@ -60,10 +60,11 @@ def scan(xbc, dt, conv_weight, conv_bias, decay, skip, dt_bias, heads, head_dim,
     return y, mag, carried
 
 
-# A product of operands that are both rounded to bf16 is off by (1 + 2^-8)^2 - 1 of itself; one of operands split
-# in two bf16 halves by the halves' own rounding (2^-16 each) and the product of the low halves (2^-16). The second
-# kind comes twice in a row in y (B C^T, then its weights times x). Sums, exponentials and the convolution add less
-# than 2^-17 of the magnitudes: a few hundred additions of 2^-24 and exponents of at most some hundreds off by 2^-23.
+# Bounds of each element by the magnitudes of its terms, which hold for any inputs and are wide: what a matrix product of
+# operands in bf16 (both off by 2^-8: (1 + 2^-8)^2 - 1), and one of operands in two bf16 halves (2^-16 each and 2^-16 for
+# the low halves' product, twice in a row in y), may be off by; sums, exponentials and the convolution add less than 2^-17.
+# The kernels round operands to 22 bits in two half precision halves. That they do is held by the 2-norm of the errors,
+# in test_gpu_operator_precision.py: a sum of random terms is far below its magnitudes.
 SCAN_Y = {"bf16": 2 ** -7 + 2 ** -14, "f32": 8 * 2 ** -16}
 SCAN_STATE = 4 * 2 ** -16
 HALF_STEP = {"bf16": 2 ** -8, "f32": 2 ** -24}

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import operators_ref as ref
+from test_gpu_adapters import Case as Adapters
 from test_gpu_scan import Case, ints
 from zero_order_recurrent_amd import binding as b
 
@@ -198,3 +199,22 @@ def test_a_channel_that_is_not_finite_stays_alone(channel):
     else:
         bad[:, 20:] = True
     assert torch.equal(torch.isnan(y).cpu(), bad)
+
+
+@pytest.mark.parametrize("dtype, rows, K, O, A, R", [
+    ("bf16", 1, 1024, 4096, 1, 16), ("bf16", 48, 512, 640, 40, 16), ("bf16", 48, 512, 640, 7, 40), ("bf16", 300, 640, 512, 3, 8),
+    ("bf16", 3333, 192, 3880, 5, 8), ("bf16", 300, 70, 515, 9, 33), ("f32", 1, 1024, 4096, 1, 16), ("f32", 40, 515, 640, 6, 12),
+    ("f32", 300, 256, 320, 6, 64), ("f32", 1279, 129, 515, 23, 12), ("f32", 3100, 64, 4070, 5, 24)])
+def test_adapters(dtype, rows, K, O, A, R):
+    """float32: nothing is rounded but sums of K and of R terms, whose partial sums' squares grow evenly, 2^-24 / sqrt 3 each.
+    bf16: the low-rank value enters its product in two halves, rounded by at most 2^-16."""
+    c = Adapters(dtype, rows, K, O, A, R, seed=K)
+    x, who, y, scale = c.inputs()
+    c.operator().project(x, who, y[:, :O], row_scale=scale)
+    want, _, _ = ref.adapters(c.x, c.w, c.bias, c.down, c.up, c.ranks, c.who, c.scale)
+    shared, _, _ = ref.adapters(c.x, c.w, c.bias, c.down, c.up, c.ranks, None, c.scale)
+    low = float((want - shared).norm() / want.norm())
+    assert rows == 1 or low > 0.1
+    sums = ((K + R) / 6) ** 0.5 * 2 ** -24 + 2 ** -24
+    e = 2 * sums if dtype == "f32" else 2 * sums + 2 ** -16 / 3 ** 0.5 * low
+    assert off(y[:, :O], want) <= bound(dtype, e)
