@@ -824,7 +824,7 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
   // The up product: for each adapter among the tile's rows, steps of 32 rank columns at the end of the
   // reduction, x rows holding v (bf16: its high halves, then its low ones) or zero, W rows holding U
   // (bf16: twice). Zeros keep an adapter out of other rows unless it holds an infinity or NaN: such
-  // entries are staged as zero, and the adapter's rows are noted and computed one by one at the end.
+  // entries are staged as zero, and the adapter's rows are noted and get those entries' products at the end.
   __shared__ uint32_t spoiled[kRowsT / 32];
   constexpr int kIds = (kRowsT + 63) / 64;
   constexpr int kSplit = sizeof(T) == 2 ? 4 : 8;  // chunks of a row before the columns repeat
@@ -970,7 +970,7 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
     for (int m = 0; m < kMT; ++m) {
       const int row = (wr * kMT + m) * 16 + l16;
       const int64_t r = r0 + row;
-      if (r >= a.n_rows || (noted && (spoiled[row >> 5] >> (row & 31) & 1u))) continue;
+      if (r >= a.n_rows) continue;
       const bool out_of_range = a.row_adapter && a.row_adapter[r] >= a.A;
       T out[16];
 #pragma unroll
@@ -986,19 +986,27 @@ __global__ __launch_bounds__(64 * kWavesR * kWavesO, 2) void k_adapter_tiles(Ada
     }
   }
   if (noted) {
+    // A product with an infinity or NaN is one itself, so it may be added to what is stored already: outputs without
+    // such an entry keep their value, the others become what they have to be. 8,192 x 4,096 x 4,096 with an infinity in
+    // one up row 0.68 ms, in every one 1.2 (rows computed one by one: 150 and 347).
+    __syncthreads();  // the rows are stored, by whichever wave
     for (int row = 0; row < kRowsT; ++row) {
       if (!(spoiled[row >> 5] >> (row & 31) & 1u)) continue;
       const int64_t r = r0 + row;
       const int ad = a.row_adapter[r], rank = rank_of(a, ad);
-      const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+      const T* const v = static_cast<const T*>(a.vq) + r * a.vq_row;
       for (int o = o0 + tid; o < min(o0 + kOutsT, a.O); o += kThreads) {
-        const T* w = static_cast<const T*>(a.weight) + static_cast<int64_t>(o) * a.weight_stride;
-        const T* u = static_cast<const T*>(a.up) + (static_cast<int64_t>(ad) * a.O + o) * a.R;
-        float s = a.bias ? to_float(static_cast<const T*>(a.bias)[o]) : 0.f;
-        for (int k = 0; k < a.K; ++k) s += to_float(x[k]) * to_float(w[k]);
-        const T* v = static_cast<const T*>(a.vq) + r * a.vq_row;
-        for (int j = 0; j < rank; ++j) s += (to_float(v[j]) + (sizeof(T) == 2 ? to_float(v[a.vq_row / 2 + j]) : 0.f)) * to_float(u[j]);
-        static_cast<T*>(a.y)[r * a.y_stride + o] = from_float<T>(s);
+        const T* const u = static_cast<const T*>(a.up) + (static_cast<int64_t>(ad) * a.O + o) * a.R;
+        float s = 0.f;
+        bool wild = false;
+        for (int j = 0; j < rank; ++j) {
+          const float e = to_float(u[j]);
+          if (fabsf(e) <= 3.4028235e38f) continue;
+          wild = true;
+          s += (to_float(v[j]) + (sizeof(T) == 2 ? to_float(v[a.vq_row / 2 + j]) : 0.f)) * e;
+        }
+        T* const y = static_cast<T*>(a.y) + r * a.y_stride + o;
+        if (wild) *y = from_float<T>(to_float(*y) + s);
       }
     }
   }
