@@ -682,11 +682,15 @@ constexpr int kWaitLoads = 0x0f70;
 // the whole wave). The load has no register result. It is written as an instruction because the
 // compiler, which cannot tell the two buffers apart, would wait for every load of this kind before any
 // read of LDS; the wait that is needed stands before the step's barrier.
+// m0 is written, and named so that no other use of it is moved across; clang warns that it never allocates m0 itself.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, uint4* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)to)));
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(at) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ int place_x(int row) { return row & 7; }
 __device__ __forceinline__ int place_w(int row) { return (row & 3) | ((row >> 2) & 4); }
