@@ -13,10 +13,13 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dtype, rows, K, O, R", [
     ("bf16", 3, 64, 70, 8), ("bf16", 200, 96, 320, 8), ("bf16", 3333, 192, 3880, 8), ("bf16", 3333, 70, 3880, 40), ("f32", 150, 64, 300, 24),
-    ("f32", 3100, 64, 4070, 8), ("f32", 30, 64, 300, 24)])
+    ("f32", 3100, 64, 4070, 8), ("f32", 30, 64, 300, 24),
+    # after a product in slices, by a launch that joins them: ranks of one product and of several, whole pieces and not
+    ("bf16", 60, 200, 130, 12), ("bf16", 60, 200, 130, 16), ("bf16", 30, 300, 70, 40), ("bf16", 150, 2048, 200, 33)])
 def test_entries_that_are_not_finite(dtype, rows, K, O, R):
     """Outputs that meet such an entry become what the formula gives; every other one keeps its value to the bit."""
     c = Case(dtype, rows, K, O, 5, R, seed=rows, ranks=[R, R, max(R - 3, 1), 0, R])
+    c.x[0], c.x[-1] = 0.0, torch.eye(1, K)  # a value of zero meets infinity as NaN, one that bf16 holds exactly as infinity
     x, who, y, scale = c.inputs()
     clean = c.operator().project(x, who, y[:, :O], row_scale=scale).clone()
     g = torch.Generator().manual_seed(1)

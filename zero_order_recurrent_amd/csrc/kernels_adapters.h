@@ -352,18 +352,21 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
   float vs[kPer];
   if (narrow && a.row_adapter && a.A > 0) v_sums<kPer>(a, r, q * kPer, vs);
   f32x4 sum[4];
+  auto add_slices = [&]() {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (rok) {
+    for (int t = 0; t < 4; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!rok) return;
     const float* p = a.partial + r * a.o_pad + o0 + 16 * q;
 #pragma unroll 2
     for (int s = wave; s < a.slices; s += 4)
 #pragma unroll
       for (int t = 0; t < 4; ++t) sum[t] += *reinterpret_cast<const f32x4*>(p + s * a.n_rows * a.o_pad + 4 * t);
-  }
+  };
+  add_slices();
   const bool has = ad >= 0 && ad < a.A;
   uint32_t todo = static_cast<uint32_t>(__ballot(has)) & 0xffffu;
   if (todo) {
+    bool here = false;  // whether this wave takes the row's adapter
     // two rounds of loads: the adapters of the rows, with the sums; then everything that an adapter names
     const int rank = has ? rank_of(a, ad) : 0;
     const float scale = has ? row_scale : 1.f;
@@ -383,6 +386,8 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
         }
       }
       if (!got) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) here |= i < got && ad == cur[i];
       if (narrow) {
         Frag<T> u[4][4];
         if (up_whole<T>(a)) {
@@ -438,6 +443,36 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[t][e] = ad == c ? sum[t][e] + low[t][e] : sum[t][e];
         }
+      }
+    }
+    if constexpr (sizeof(T) == 2) {
+      // Where U holds an infinity, the two halves of v give infinities of either sign, or one of them is zero, and NaN comes
+      // out: such sums are formed anew of the whole v.
+      bool lost = false;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lost |= !(sum[t][e] == sum[t][e]);
+      if (__any(lost && here)) {
+        f32x4 old[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) old[t] = sum[t];
+        add_slices();
+        for (int j = 0; j < (here ? rank : 0); ++j) {
+          float v[1];
+          v_sums<1>(a, r, j, v);
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = min(o0 + 16 * q + 4 * t + e, a.O - 1);
+              sum[t][e] += v[0] * scale * to_float(static_cast<const T*>(a.up)[(static_cast<int64_t>(ad) * a.O + at) * a.R + j]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[t][e] = here && !(old[t][e] == old[t][e]) ? sum[t][e] : old[t][e];
       }
     }
   }
