@@ -217,8 +217,10 @@ size_t cdrge_noalloc_max_workspace_bytes(void);
  * the same evaluation to models that differ by a low-rank term instead of a full sign probe, that
  * recur through a state space instead of an LSTM cell, and that learn from a teacher instead of
  * the next token: a projection shared by all rows with a low-rank adapter by row, a selective
- * scan with its short causal convolution, and a distillation loss whose mean by model is what
- * cdrge_update takes as a model's loss.
+ * scan with its short causal convolution, and a distillation loss with its mean by model. They
+ * compose with each other; the calls above do not take their results: cdrge_update moves an LSTM's
+ * tensors along full sign probes that it draws from seeds, of which losses of other models say
+ * nothing.
  *
  * They need no context. Every call enqueues on `stream` (a hipStream_t; NULL is the default
  * stream) and returns; pointers are device memory of the current device, which must be the
@@ -343,7 +345,8 @@ cdrge_status cdrge_adapter_workspace_bytes(const cdrge_adapter_config* cfg, int6
 /* x: T [n_rows][K]; row_adapter: int32 [n_rows], negative for no adapter, or NULL (no row has
  * one); row_scale: float32 [n_rows] or NULL (1); y: T [n_rows][O]. n_rows may be 0, up to 2^30. A row
  * whose adapter is A or more gets NaN. A row's result does not depend on what other rows' inputs
- * or adapters hold, nor on their order. */
+ * or adapters hold, nor on their order. In bf16 and from a few rows on, scale_r down_a x_r enters
+ * its product with up_a rounded to 16 bits. */
 cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_adapter_weights* weights,
                                    int64_t n_rows, const void* x, int64_t x_stride, const int32_t* row_adapter,
                                    const float* row_scale, void* y, int64_t y_stride, void* workspace,
@@ -358,8 +361,8 @@ cdrge_status cdrge_adapter_project(const cdrge_adapter_config* cfg, const cdrge_
  *
  * A row without a present entry is not scored: its loss and gradient are zero. An id of vocab or
  * more makes its row NaN. An id may come twice. losses[m] is the mean of the scored rows of model
- * m, which owns the rows m (n_rows / n_models) onwards (NaN if it has none): the layout that
- * cdrge_update reads for 2K perturbed models. Sums run in a fixed order. */
+ * m, which owns the rows m (n_rows / n_models) onwards (NaN if it has none). Sums run in a fixed
+ * order. */
 typedef struct {
   uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
   int32_t dtype;        /* type T of the logits and their gradient */

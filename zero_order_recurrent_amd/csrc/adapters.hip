@@ -68,7 +68,7 @@ Cut make_cut(const cdrge_adapter_config* c, int64_t n_rows) {
     // four waves share a slice: at least two steps of 64 bytes each for every wave
     want = std::min(want, ceil_div(K, 4 * step));
   } else {
-    // 256 x 256 tiles where they fill the chip (rows x K x O of 8192 x 4096 x 4096 in bf16: 258 us, 330 with 128 x 128;
+    // 256 x 256 tiles where they fill the chip (rows x K x O of 8192 x 4096 x 4096 in bf16: 263 us, 330 with 128 x 128;
     // 4096 x 2048 x 3584: 85 against 109); 128 x 128, in slices of at least 8 steps where the tiles alone
     // leave compute units idle; 64 x 64 where K is too short for slices (1279 x 128 x 512: 17 against 27)
     auto tiles = [&](int side) { return int64_t(ceil_div(n_rows, side)) * ceil_div(O, side); };

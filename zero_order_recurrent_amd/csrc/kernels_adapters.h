@@ -330,7 +330,7 @@ __device__ __forceinline__ void up_cut(int j, int n, Frag<T> (&u)[4]) {
 // After a shared product in slices: 16 rows x 64 outputs by four waves, which share the slices and the
 // adapters among the rows and add up through LDS. The time is the latency of a few loads, so each wave
 // has those of up to four adapters in flight together (48 rows, 5888 outputs, 40 adapters of
-// rank 16: 7.4 us, of rank 12 9; without adapters 4.6).
+// rank 16: 7.7 us, of rank 12 10.4; without adapters 4.6).
 // sum[t][e] is output o0 + 16 q + 4 t + e of row l16.
 // ---------------------------------------------------------------------------------------------
 template <class T>
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(256) void k_adapter_finish(AdapterArgs a) {
 // and beside W's rows it reads those of D that the rows' adapters name (kD tiles of 16: every workgroup repeats that
 // product, out of the caches), so that the up product can follow from shared memory. The latter runs in float32 on
 // the vector unit, a thread an output. Bound by latency: one row, 1024 -> 4096 with an adapter of rank 16 in bf16, 6.1
-// us, of which 3.6 are a launch.
+// us, of which 3.6 are a launch; in float32 9.5.
 // ---------------------------------------------------------------------------------------------
 constexpr int kFewTiles = 4;  // tiles of D at most
 
@@ -604,7 +604,7 @@ __global__ __launch_bounds__(512) void k_adapter_few(AdapterArgs a) {
 
 // ---------------------------------------------------------------------------------------------
 // Up to 64 rows (kTiles tiles of 16): bound by reading W once, and by x, which every workgroup reads from the caches.
-// K and O 5888, bf16: 18 us for one row (3.8 TB/s of W), 21 for 16, 28 for 48. Reading W past the caches is slower (48 rows
+// K and O 5888, bf16: 16 us for one row (4.3 TB/s of W), 17 for 16, 23 for 48; in float32 74 for 48. Reading W past the caches is slower (48 rows
 // and joining 41 us instead of 35), two adjacent steps a wave are no faster. A workgroup takes 64 outputs and one
 // slice of K; its four waves take its steps in turn, each with all rows and outputs, straight from
 // global memory into the matrix cores' registers, and add up through LDS. Workgroups past those run
@@ -703,8 +703,8 @@ __global__ __launch_bounds__(256, 2) void k_adapter_rows(AdapterArgs a) {
 // conflicts. kDirect (rows of x and W 16-byte aligned, K a multiple of a step) loads straight into
 // LDS; otherwise the chunks pass through registers and are cut at K.
 //
-// 8,192 rows of 4,096 to 4,096 outputs, bf16, four adapters of rank 8: 232 us with the up product, 1,185 TFLOP/s (a
-// large library product reaches 1,500, and takes 183 us for the shared part alone). The matrix cores are busy in half
+// 8,192 rows of 4,096 to 4,096 outputs, bf16, four adapters of rank 8: 238 us with the up product, 1,155 TFLOP/s (a
+// large library product reaches 1,500, and takes 183 us for the shared part alone). The matrix cores are busy in 57%
 // of the cycles; the reads and writes of LDS of a step take as long as its products, with few cycles to hide either
 // in. Waves of 128 x 128, which would read a third less, keep their sums in the second half of the register file and
 // lost more to the moves there.

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(64 * kScanOwnerWaves) void k_scan_mark(ScanArgs a, 
 // written in whole lines. Bound by memory: the state is read and written once, past the caches (nobody
 // reads it again before the next token). All loads of a workgroup are in flight together, the check for a
 // repeated slot beside them. 256 rows, 64 heads of 64 x 128, bf16: 197 us, 5.4 TB/s (233 through the caches;
-// 286 with the convolution's loads one after the other). One row of 16 heads: 6.6 us, the latency of a launch and
+// 286 with the convolution's loads one after the other). One row of 16 heads: 7.1 us, the latency of a launch and
 // two loads.
 // ---------------------------------------------------------------------------------------------
 template <class T, int kLanes, int kRpt>
@@ -265,10 +265,11 @@ __global__ __launch_bounds__(256) void k_scan_step(ScanArgs a) {
 // zero (without y), and in the second run a piece starts from its predecessors' states, each faded
 // by the pieces behind it. This reads x twice but leaves no state in memory but one a piece.
 // One sequence of 8,192 tokens, 64 heads of 64, state 128, bf16, takes 250 us: k_scan_blocks 23, the first run
-// 72, the second 142, k_scan_ring 5 (37.7 ms by the step above, token after token; 44 us for the bytes). It is bound
-// by the vector unit's issue and by what two waves a SIMD leave uncovered: a block costs a wave some 1,300 vector
-// instructions (convolution, gates, decays, splitting operands) beside 72 matrix products, 55% of the time.
-// Pieces of at least four blocks: with at least 8, 1 x 2048 tokens and 16 heads takes 102 us instead of 74.
+// 62, the second 161, k_scan_ring 5 (37.7 ms by the step above, token after token; 44 us for the bytes); float32 296. It
+// is bound by the vector unit's issue and by what two waves a SIMD leave uncovered: a block costs a wave 640 vector
+// instructions beside 48 matrix products in the first run and 1,570 beside 114 in the second (convolution, gates, decays,
+// splitting operands), 60% of the time in both.
+// Pieces of at least four blocks: with at least 8, 1 x 2048 tokens and 16 heads takes 107 us instead of 73.
 //
 // Products run on the matrix cores in half precision (11 bits), operands scaled by a power of two of
 // the block so that their largest magnitude is below 2^14, in two halves each (22 bits) and three
@@ -714,7 +715,7 @@ __device__ __forceinline__ int scan_place(int p) { return ((p ^ (p >> 2)) & 3) |
 // pieces that have a successor. Lane (l16, q) of wave i holds the state at columns 16 tile + 4 q + e and
 // channel 16 m + l16, the tiles shared among the waves, and y at token 16 i + l16 and channels 16 q + 4 m + e.
 // Loads are issued a phase or more before their use: a block's time is otherwise theirs, one after the other.
-// z and y, each met once, go past the caches, which keeps x there for the second run (1 x 8,192 tokens: 10 us less).
+// z and y, each met once, go past the caches, which keeps x there for the second run (1 x 8,192 tokens in bf16: 250 us, 262 through them).
 template <class T, int kN, bool kFirstRun>
 __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
   constexpr bool first_run = kFirstRun;
@@ -828,8 +829,8 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
     cw[c] = Four<T>{};
     if (pc + c < np) cw[c].load_back(static_cast<const T*>(a.conv_weight) + static_cast<int64_t>(h * a.P + p0 + pc + c) * a.W, a.W);
   }
-  // Whole blocks of whole heads are loaded without conditions: 217 us instead of 232 at 1 x 8,192 tokens in bf16. Where
-  // registers are short (float32, wide states) the second way costs more than it gives (state 256: 180 against 169 us).
+  // Whole blocks of whole heads are loaded without conditions: 250 us instead of 261 at 1 x 8,192 tokens in bf16. Where
+  // registers are short (float32, wide states) the second way costs more than it gives (state 256: 544 against 525 us).
   const bool whole = sizeof(T) == 2 && kN <= 128 && np == 64;
   Four<T> raw[7];  // tokens tg - 3 .. tg + 3 of the block
   auto load_raw = [&](int nth) {
@@ -1172,11 +1173,11 @@ __global__ __launch_bounds__(256, 2) void k_scan_heads(ScanArgs a, ScanWork w) {
 // float32 on the matrix cores. A workgroup takes a sequence and group and up to kScanUnits (head, 64
 // channels); its four waves convolve B and C together and then take the units in turn. Bound by
 // latency and by the convolutions' and gates' exponentials: 1,024 sequences of 10 tokens, 16 heads of
-// 64, state 64, bf16, take 50 us (1.3 TB/s), 210 by blocks of 64 tokens. Eight units a workgroup instead of 16: 57.
+// 64, state 64, bf16, take 50 us (1.3 TB/s), 291 by blocks of 64 tokens; in float32 66. Eight units a workgroup instead of 16: 55.
 // ---------------------------------------------------------------------------------------------
 constexpr int kScanShort = 16, kScanUnits = 16;
 
-// bf16: four waves a SIMD, at the price of a few spilled registers (three without: 65 us instead of 52 at 1,024 x 10
+// bf16: four waves a SIMD, at the price of a few spilled registers (three without: 68 us instead of 50 at 1,024 x 10
 // tokens, 16 heads of 64 x 64); float32's do not fit.
 template <class T, int kN>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) void k_scan_short(ScanArgs a, int parts) {
