@@ -114,3 +114,51 @@ def test_states_are_a_layer_of_a_cache(form, heads, head_dim, state, dtype):
     assert torch.isfinite(want).all() and torch.equal(run(conv[1], ssm[1]), want)
     assert torch.equal(conv[1], alone[0]) and torch.equal(ssm[1], alone[1])
     assert torch.equal(conv[[0, 2]], others[0]) and torch.equal(ssm[[0, 2]], others[1])
+
+
+@pytest.mark.parametrize("form, n", [("step", 6000), ("prompt", 17000)])
+def test_many_slots_replay_and_on_another_stream(form, n):
+    """The launch that looks for slots named twice, captured and replayed with other slots in the same place."""
+    layer, channels, t, rand = layer_of(16, 4, 4, "bf16")
+    xbc, dt, y = rand(n, channels).to(t), rand(n, 16).to(t), torch.empty(n, 64, device="cuda", dtype=t)
+    conv, ssm = rand(n, 3, channels).to(t), rand(n, 16, 4, 4)
+    co, so = torch.empty_like(conv), torch.empty_like(ssm)
+    positions = torch.full((n,), 3, device="cuda", dtype=torch.int32)
+    orders = [torch.randperm(n, generator=torch.Generator().manual_seed(i)).to(torch.int32).cuda() for i in range(3)]
+    orders[1][n // 2] = orders[1][5]
+    slots = orders[0].clone()
+
+    def run(stream=None):
+        if form == "step":
+            layer.step(xbc, dt, y, positions, conv, ssm, slots=slots, conv_out=co, ssm_out=so, stream=stream)
+        else:
+            layer.prompt(xbc, dt, y, n, slots=slots, positions=positions, conv_state=conv, ssm_state=ssm, conv_out=co, ssm_out=so, stream=stream)
+
+    want = []
+    for order in orders:
+        slots.copy_(order)
+        for out in (y, co, so):
+            out.zero_()
+        run()
+        want.append([out.clone() for out in (y, co, so)])
+    assert torch.isnan(want[1][0][n // 2]).all() and torch.isfinite(want[0][0]).all() and not torch.isnan(want[1][0][5]).any()
+    same = lambda got, w: all(torch.equal(a.nan_to_num(9.0), c.nan_to_num(9.0)) for a, c in zip(got, w))  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for out in (y, co, so):
+        out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    run(side)
+    side.synchronize()
+    assert same((y, co, so), want[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in (1, 0, 2, 1):
+        slots.copy_(orders[i])
+        for out in (y, co, so):
+            out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        assert same((y, co, so), want[i])
+        torch.ones(1000, device="cuda").sum().item()
