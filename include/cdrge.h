@@ -386,6 +386,149 @@ cdrge_status cdrge_distill_grad(const cdrge_distill_config* cfg, int64_t n_rows,
                                 const float* row_grad, float* row_losses, float* losses, void* dlogits,
                                 int64_t dlogits_stride, void* stream);
 
+/* ---- Gated delta rule -----------------------------------------------------------------------
+ * A recurrence beside the scan, with the same cache of slots. Per token and head, a row of v holds
+ * value_dim entries, rows of q and k key_dim entries for each of n_groups groups (head h belongs to
+ * group h / (n_heads / n_groups)), dt and beta one entry a head before their functions:
+ *
+ *   q' = q_scale q / sqrt(q.q + norm_eps),   k' = k / sqrt(k.k + norm_eps)
+ *   a_t = exp(decay softplus(dt_t + dt_bias)),   b_t = 1 / (1 + exp(-beta_t))                 (by head)
+ *   S_t = a_t S_{t-1} + b_t (v_t - a_t S_{t-1} k'_t) k'_t^T                            [value_dim][key_dim]
+ *   y_t = S_t q'_t
+ *
+ * The squares of a row of q or k must sum to less than 2^127 (magnitudes up to 2^59 always do); a row
+ * past that counts as not finite. */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* CDRGE_F32 or CDRGE_BF16 */
+  int32_t n_heads;
+  int32_t value_dim;    /* 1 .. 256 */
+  int32_t n_groups;     /* divides n_heads */
+  int32_t key_dim;      /* 1 .. 256 */
+  float q_scale;        /* finite, magnitude up to 2^60; key_dim^-0.5 is usual */
+  float norm_eps;       /* 2^-60 .. 1 */
+} cdrge_delta_config;
+
+typedef struct {
+  const float* decay;   /* [n_heads], negative for a state that fades */
+  const float* dt_bias; /* [n_heads], or NULL */
+} cdrge_delta_weights;
+
+/* state_in is read and state_out written; they may be the same pointer (update in place), and
+ * otherwise state_out gets the slot's whole contents, while slots that no sequence of the call names
+ * are left as they are. Both are given, or none (every sequence starts at zero, nothing is kept; slots
+ * and positions must be NULL then). */
+typedef struct {
+  const void* q;            /* T [n_tokens][n_groups * key_dim] */
+  int64_t q_stride;
+  const void* k;            /* T [n_tokens][n_groups * key_dim] */
+  int64_t k_stride;
+  const void* v;            /* T [n_tokens][n_heads * value_dim] */
+  int64_t v_stride;
+  const void* dt;           /* T [n_tokens][n_heads] */
+  int64_t dt_stride;
+  const void* beta;         /* T [n_tokens][n_heads] */
+  int64_t beta_stride;
+  void* y;                  /* T [n_tokens][n_heads * value_dim] */
+  int64_t y_stride;
+  int64_t n_tokens;         /* 0 .. 2^30 */
+  int32_t n_seqs;           /* 1 .. 2^20 */
+  int32_t n_slots;
+  const int32_t* offsets;   /* as in cdrge_scan_io */
+  const int32_t* slots;     /* as in cdrge_scan_io */
+  const int32_t* positions; /* [n_seqs]: zero (or less) starts the sequence at zero whatever the slot holds */
+  const float* state_in;    /* [n_slots][n_heads][value_dim][key_dim], 16-byte aligned where key_dim is a
+                               multiple of 4 */
+  float* state_out;
+} cdrge_delta_io;
+
+/* Workspace, in bytes, of cdrge_delta_prompt for n_tokens tokens in n_seqs sequences (256-byte
+ * aligned base required). */
+cdrge_status cdrge_delta_workspace_bytes(const cdrge_delta_config* cfg, int64_t n_tokens, int32_t n_seqs,
+                                         size_t* bytes_out);
+
+/* Whole prompts, or continued ones. Offsets, slots that are negative, out of range or named twice, and
+ * rows outside every sequence: as for cdrge_scan_prompt. A token that is not finite may spoil outputs of
+ * its own sequence from up to 63 tokens before it; other sequences are not affected. */
+cdrge_status cdrge_delta_prompt(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
+                                const cdrge_delta_io* io, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of n_seqs = n_tokens sequences (offsets must be NULL, the state and positions
+ * given). A row with a negative slot is padding: its y row and every state are left as they are. */
+cdrge_status cdrge_delta_step(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
+                              const cdrge_delta_io* io, void* stream);
+
+/* ---- Scores of given tokens -----------------------------------------------------------------
+ * With tau the temperature, p the softmax of a row's logits / tau and t its given token:
+ *
+ *   logprob = log p_t,   entropy = -sum_v p_v log p_v   (a v of p_v = 0 adds nothing)
+ *   d logprob / d logit_v = ((v == t) - p_v) / tau,   d entropy / d logit_v = -p_v (log p_v + entropy) / tau
+ *
+ * and the top_k alternatives are the largest logits, in falling order, equal ones by their place.
+ * A negative token is padding: its logprob is zero, the row's entropy and alternatives are as for any
+ * other. A token of vocab or more makes its logprob NaN. A logit of minus infinity has p = 0 and is no
+ * alternative: places that are left over have the id -1 and the logprob minus infinity, which a
+ * distillation loss takes for absent. A row with a NaN, plus infinity, or nothing but minus infinity
+ * has NaN for its token's logprob, its entropy and its alternatives' logprobs, and -1 for their ids. */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* type T of the logits and their gradient */
+  int32_t vocab;        /* 1 .. 2^24 */
+  int32_t top_k;        /* 0 .. 1024, at most vocab */
+  float temperature;    /* 2^-60 .. 2^60 */
+} cdrge_score_config;
+
+/* logits: T [n_rows][vocab]; tokens: int32 [n_rows], or NULL where logprobs is; logprobs, entropy:
+ * float32 [n_rows], either may be NULL; top_ids: int32 [n_rows][top_k] and top_logprobs: float32
+ * [n_rows][top_k], NULL where top_k is 0. n_rows may be 0, up to 2^30. */
+cdrge_status cdrge_token_scores(const cdrge_score_config* cfg, int64_t n_rows, const void* logits,
+                                int64_t logits_stride, const int32_t* tokens, float* logprobs, float* entropy,
+                                int32_t* top_ids, float* top_logprobs, void* stream);
+
+/* dlogits[r] = d_logprob[r] * d logprob_r / d logits_r + d_entropy[r] * d entropy_r / d logits_r in T.
+ * d_logprob, d_entropy: float32 [n_rows], either may be NULL (0; tokens may be NULL where d_logprob
+ * is); d_logprob counts as zero where the token is padding. Where both are zero the row's gradient is
+ * zero whatever it holds; otherwise a row that has NaN above, or a token of vocab or more with a
+ * d_logprob that is not zero, gives NaN. dlogits may be logits itself (same pointer and stride). */
+cdrge_status cdrge_token_scores_grad(const cdrge_score_config* cfg, int64_t n_rows, const void* logits,
+                                     int64_t logits_stride, const int32_t* tokens, const float* d_logprob,
+                                     const float* d_entropy, void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* ---- Weights in microscaled 4-bit floating point ----------------------------------------------
+ * A row of `in_features` values is kept as blocks of 32 (the last may be short): for each a scale
+ * byte e and 16 bytes of codes, two values to a byte, the first in its low half, zeros past the end.
+ * A code is a sign (8) and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6; the value is 2^(e - 127) times that.
+ * Quantisation takes e so that the block's largest magnitude is in [4, 8) 2^(e - 127), or e = 0 where
+ * that is too small, and the nearest code, ties to the even one, magnitudes past 6 becoming 6. A block
+ * with a NaN or an infinity has e = 255, which stands for NaN in all of it. (OCP Microscaling Formats,
+ * MXFP4: E2M1 elements, E8M0 scales.) */
+typedef struct {
+  uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
+  int32_t dtype;        /* type T of rows that are not quantised: CDRGE_F32 or CDRGE_BF16 */
+  int32_t in_features;  /* K, 1 .. 2^20 */
+  int32_t out_features; /* O, 1 .. 2^20 (cdrge_mx_project only) */
+} cdrge_mx_config;
+
+/* x: T [n_rows][K]; codes: uint8 [n_rows][16 * ceil(K / 32)], 16-byte aligned; scales: uint8 [n_rows]
+ * [ceil(K / 32)]. n_rows may be 0, up to 2^30. */
+cdrge_status cdrge_mx_quantize(const cdrge_mx_config* cfg, int64_t n_rows, const void* x, int64_t x_stride,
+                               uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for (either type holds all that quantisation makes exactly;
+ * e = 253 and 254 may stand for more than T holds, and become infinite). */
+cdrge_status cdrge_mx_dequantize(const cdrge_mx_config* cfg, int64_t n_rows, const uint8_t* codes,
+                                 const uint8_t* scales, void* x, int64_t x_stride, void* stream);
+
+/* Workspace, in bytes, of cdrge_mx_project for n_rows rows (256-byte aligned base required). */
+cdrge_status cdrge_mx_workspace_bytes(const cdrge_mx_config* cfg, int64_t n_rows, size_t* bytes_out);
+
+/* y_r = W Q(x_r) + bias, with W the values of w_codes and w_scales [O][K] and Q(x_r) those of the row
+ * quantised as by cdrge_mx_quantize. bias: T [O], or NULL; y: T [n_rows][O]. Products of codes are
+ * exact and summed in float32. A row with a NaN or an infinity gives NaN; other rows are not affected. */
+cdrge_status cdrge_mx_project(const cdrge_mx_config* cfg, const uint8_t* w_codes, const uint8_t* w_scales,
+                              const void* bias, int64_t n_rows, const void* x, int64_t x_stride, void* y,
+                              int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -77,6 +77,36 @@ class cdrge_distill_config(ctypes.Structure):
                 ("top_k", ctypes.c_int32), ("n_models", ctypes.c_int32), ("temperature", ctypes.c_float)]
 
 
+class cdrge_delta_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("key_dim", ctypes.c_int32),
+                ("q_scale", ctypes.c_float), ("norm_eps", ctypes.c_float)]
+
+
+class cdrge_delta_weights(ctypes.Structure):
+    _fields_ = [("decay", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
+class cdrge_delta_io(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64),
+                ("dt", ctypes.c_void_p), ("dt_stride", ctypes.c_int64), ("beta", ctypes.c_void_p),
+                ("beta_stride", ctypes.c_int64), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("n_slots", ctypes.c_int32),
+                ("offsets", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p)]
+
+
+class cdrge_score_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
+class cdrge_mx_config(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32)]
+
+
 _OPERATOR_DTYPES = {"f32": CDRGE_F32, "bf16": CDRGE_BF16}
 
 
@@ -93,6 +123,20 @@ def make_adapter_config(in_features, out_features, n_adapters, max_rank, dtype) 
 def make_distill_config(vocab, top_k, n_models, temperature, dtype) -> cdrge_distill_config:
     return cdrge_distill_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), vocab, top_k, n_models,
                                 temperature)
+
+
+def make_delta_config(n_heads, n_groups, key_dim, value_dim, dtype, q_scale=None, norm_eps=1e-6) -> cdrge_delta_config:
+    """q_scale None: key_dim^-0.5."""
+    return cdrge_delta_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), n_heads, value_dim, n_groups, key_dim,
+                              max(key_dim, 1) ** -0.5 if q_scale is None else q_scale, norm_eps)
+
+
+def make_score_config(vocab, top_k, temperature, dtype) -> cdrge_score_config:
+    return cdrge_score_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), vocab, top_k, temperature)
+
+
+def make_mx_config(in_features, out_features, dtype) -> cdrge_mx_config:
+    return cdrge_mx_config(CDRGE_ABI_VERSION, _OPERATOR_DTYPES.get(dtype, dtype), in_features, out_features)
 
 
 def config_from_preset(p) -> cdrge_config:
@@ -144,6 +188,25 @@ EXPORTS = {
     "cdrge_distill_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "cdrge_delta_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
+    "cdrge_delta_prompt": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]),
+    "cdrge_delta_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "cdrge_token_scores": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "cdrge_token_scores_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                               ctypes.c_int64, ctypes.c_void_p]),
+    "cdrge_mx_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "cdrge_mx_dequantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "cdrge_mx_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+    "cdrge_mx_project": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -386,6 +449,58 @@ def cdrge_distill_grad(cfg, logits, ids, teacher, row_grad, row_losses, losses, 
            "cdrge_distill_grad")
 
 
+def cdrge_delta_workspace_bytes(cfg: cdrge_delta_config, n_tokens: int, n_seqs: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().cdrge_delta_workspace_bytes(ctypes.byref(cfg), n_tokens, n_seqs, ctypes.byref(out)),
+           "cdrge_delta_workspace_bytes")
+    return int(out.value)
+
+
+def cdrge_delta_prompt(cfg, weights: cdrge_delta_weights, io: cdrge_delta_io, workspace, stream: int):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().cdrge_delta_prompt(ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(io), _ptr(workspace), nbytes,
+                                    stream), "cdrge_delta_prompt")
+
+
+def cdrge_delta_step(cfg, weights: cdrge_delta_weights, io: cdrge_delta_io, stream: int):
+    _check(lib().cdrge_delta_step(ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(io), stream), "cdrge_delta_step")
+
+
+def cdrge_token_scores(cfg, logits, tokens, logprobs, entropy, top_ids, top_logprobs, stream: int):
+    _check(lib().cdrge_token_scores(ctypes.byref(cfg), logits.shape[0], logits.data_ptr(), _row_stride(logits), _ptr(tokens),
+                                    _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), stream),
+           "cdrge_token_scores")
+
+
+def cdrge_token_scores_grad(cfg, logits, tokens, d_logprob, d_entropy, dlogits, stream: int):
+    _check(lib().cdrge_token_scores_grad(ctypes.byref(cfg), logits.shape[0], logits.data_ptr(), _row_stride(logits),
+                                         _ptr(tokens), _ptr(d_logprob), _ptr(d_entropy), dlogits.data_ptr(),
+                                         _row_stride(dlogits), stream), "cdrge_token_scores_grad")
+
+
+def cdrge_mx_quantize(cfg, x, codes, scales, stream: int):
+    _check(lib().cdrge_mx_quantize(ctypes.byref(cfg), x.shape[0], x.data_ptr(), _row_stride(x), codes.data_ptr(),
+                                   scales.data_ptr(), stream), "cdrge_mx_quantize")
+
+
+def cdrge_mx_dequantize(cfg, codes, scales, x, stream: int):
+    _check(lib().cdrge_mx_dequantize(ctypes.byref(cfg), x.shape[0], codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+                                     _row_stride(x), stream), "cdrge_mx_dequantize")
+
+
+def cdrge_mx_workspace_bytes(cfg: cdrge_mx_config, n_rows: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().cdrge_mx_workspace_bytes(ctypes.byref(cfg), n_rows, ctypes.byref(out)), "cdrge_mx_workspace_bytes")
+    return int(out.value)
+
+
+def cdrge_mx_project(cfg, w_codes, w_scales, bias, n_rows, x, y, workspace, stream: int):
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().cdrge_mx_project(ctypes.byref(cfg), w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), n_rows, x.data_ptr(),
+                                  _row_stride(x), y.data_ptr(), _row_stride(y), _ptr(workspace), nbytes, stream),
+           "cdrge_mx_project")
+
+
 def _row_stride(t) -> int:
     # a single row may have any stride, also one below its length; the library wants at least that
     n = t.shape[1]
@@ -474,6 +589,16 @@ def _cuda_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     return t.device
+
+
+def _gpu(device):
+    import torch
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("the operator runs on a GPU")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
 
 
 # cdrge_scan_io as bytes: building them is quicker than filling a ctypes structure, and they belong to one call
@@ -602,13 +727,7 @@ class DistillLoss(_Operator):
     """Distillation from a teacher's top logits (cdrge_distill_losses, cdrge_distill_grad)."""
 
     def __init__(self, cfg: cdrge_distill_config, device=None):
-        import torch
-        device = torch.device("cuda" if device is None else device)
-        if device.type != "cuda":
-            raise ValueError("the operator runs on a GPU")
-        if device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
-        super().__init__(cfg, device)
+        super().__init__(cfg, _gpu(device))
 
     def _inputs(self, logits, ids, teacher, row_losses, losses):
         n, cfg, at, f = logits.shape[0], self.cfg, self.index, self._torch.float32
@@ -637,3 +756,159 @@ class DistillLoss(_Operator):
         self._run(lambda ws, s: _check(call(*args[:6], p_up, *args[6:], p_d, d_stride, s), "cdrge_distill_grad"), 0,
                   stream)
         return dlogits
+
+
+# cdrge_delta_io as bytes, as _SCAN_IO
+_DELTA_IO = struct.Struct("@" + "Pq" * 6 + "qii" + "P" * 5)
+assert _DELTA_IO.size == ctypes.sizeof(cdrge_delta_io)
+
+
+class DeltaLayer(_Operator):
+    """Gated delta rule (cdrge_delta_prompt, cdrge_delta_step). decay and dt_bias [n_heads] in float32, the latter or None.
+    """
+
+    def __init__(self, cfg: cdrge_delta_config, decay, dt_bias=None):
+        super().__init__(cfg, _cuda_device(decay, "decay"))
+        cdrge_delta_workspace_bytes(cfg, 0, 1)  # raises for a configuration that is not valid or supported
+        f, heads, at = self._torch.float32, (cfg.n_heads,), self.index
+        self.keys, self.values = cfg.n_groups * cfg.key_dim, cfg.n_heads * cfg.value_dim
+        self._held = (decay, dt_bias)
+        self.weights = cdrge_delta_weights(_whole("decay", decay, f, heads, at),
+                                           None if dt_bias is None else _whole("dt_bias", dt_bias, f, heads, at))
+        self._weights = ctypes.addressof(self.weights)
+        self._state_shape = (cfg.n_heads, cfg.value_dim, cfg.key_dim)
+
+    def _io(self, q, k, v, dt, beta, y, n_seqs, offsets, slots, positions, state, state_out):
+        at, n, t, heads = self.index, q.shape[0], self.dtype, self.cfg.n_heads
+        i32, f = self._torch.int32, self._torch.float32
+        keys, values = (n, self.keys), (n, self.values)
+        p_in = p_out = n_slots = 0
+        if state is not None:
+            n_slots = state.shape[0]
+            p_in = p_out = _whole("the state", state, f, (n_slots, *self._state_shape), at)
+            if state_out is not None:
+                p_out = _whole("state_out", state_out, f, (n_slots, *self._state_shape), at)
+        elif state_out is not None:
+            raise ValueError("an output state needs the state that is read")
+        return _DELTA_IO.pack(
+            _rows("q", q, t, keys, at), _row_stride(q), _rows("k", k, t, keys, at), _row_stride(k),
+            _rows("v", v, t, values, at), _row_stride(v), _rows("dt", dt, t, (n, heads), at), _row_stride(dt),
+            _rows("beta", beta, t, (n, heads), at), _row_stride(beta), _rows("y", y, t, values, at), _row_stride(y),
+            n, n_seqs, n_slots, 0 if offsets is None else _whole("offsets", offsets, i32, (n_seqs + 1,), at),
+            0 if slots is None else _whole("slots", slots, i32, (n_seqs,), at),
+            0 if positions is None else _whole("positions", positions, i32, (n_seqs,), at), p_in, p_out)
+
+    def prompt(self, q, k, v, dt, beta, y, n_seqs, offsets=None, slots=None, positions=None, state=None, state_out=None,
+               stream=None):
+        """Whole or continued prompts: rows offsets[i] .. offsets[i + 1] - 1 (or equal shares of the rows) belong to
+        sequence i. Writes y, and the state in place unless state_out is given. Returns y."""
+        io = self._io(q, k, v, dt, beta, y, n_seqs, offsets, slots, positions, state, state_out)
+        n = self._bytes(cdrge_delta_workspace_bytes, q.shape[0], n_seqs)
+        call = self._lib.cdrge_delta_prompt
+        self._run(lambda ws, s: _check(call(self._cfg, self._weights, io, 0 if ws is None else ws.data_ptr(), n, s),
+                                       "cdrge_delta_prompt"), n, stream)
+        return y
+
+    def step(self, q, k, v, dt, beta, y, positions, state, slots=None, state_out=None, stream=None):
+        """One token of each sequence, row i at place positions[i] of the sequence in slot slots[i] (negative: padding).
+        Writes y, and the state in place unless state_out is given. Returns y."""
+        n = q.shape[0]
+        io = self._io(q, k, v, dt, beta, y, n, None, slots, positions, state, state_out)
+        if n:
+            call = self._lib.cdrge_delta_step
+            self._run(lambda ws, s: _check(call(self._cfg, self._weights, io, s), "cdrge_delta_step"), 0, stream)
+        return y
+
+
+class TokenScores(_Operator):
+    """Log probabilities of given tokens, entropy and top alternatives (cdrge_token_scores, cdrge_token_scores_grad)."""
+
+    def __init__(self, cfg: cdrge_score_config, device=None):
+        super().__init__(cfg, _gpu(device))
+
+    def scores(self, logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, stream=None):
+        """Fills logprobs and, if given, entropy [rows], and top_ids (int32) and top_logprobs [rows, top_k], which are
+        needed unless top_k is 0. tokens and logprobs may be None together. Returns logprobs."""
+        n, cfg, at, f, i32 = logits.shape[0], self.cfg, self.index, self._torch.float32, self._torch.int32
+        top = (n, cfg.top_k)
+        args = (self._cfg, n, _rows("logits", logits, self.dtype, (n, cfg.vocab), at), _row_stride(logits),
+                0 if tokens is None else _whole("tokens", tokens, i32, (n,), at),
+                0 if logprobs is None else _whole("logprobs", logprobs, f, (n,), at),
+                0 if entropy is None else _whole("entropy", entropy, f, (n,), at),
+                0 if top_ids is None else _whole("top_ids", top_ids, i32, top, at),
+                0 if top_logprobs is None else _whole("top_logprobs", top_logprobs, f, top, at))
+        call = self._lib.cdrge_token_scores
+        self._run(lambda ws, s: _check(call(*args, s), "cdrge_token_scores"), 0, stream)
+        return logprobs
+
+    def grad(self, logits, tokens, d_logprob, d_entropy, dlogits, stream=None):
+        """dlogits[r] = d_logprob[r] d logprob_r / d logits[r] + d_entropy[r] d entropy_r / d logits[r]; either factor may
+        be None. dlogits may be logits itself. Returns dlogits."""
+        n, cfg, at, f = logits.shape[0], self.cfg, self.index, self._torch.float32
+        args = (self._cfg, n, _rows("logits", logits, self.dtype, (n, cfg.vocab), at), _row_stride(logits),
+                0 if tokens is None else _whole("tokens", tokens, self._torch.int32, (n,), at),
+                0 if d_logprob is None else _whole("d_logprob", d_logprob, f, (n,), at),
+                0 if d_entropy is None else _whole("d_entropy", d_entropy, f, (n,), at),
+                _rows("dlogits", dlogits, self.dtype, (n, cfg.vocab), at), _row_stride(dlogits))
+        call = self._lib.cdrge_token_scores_grad
+        self._run(lambda ws, s: _check(call(*args, s), "cdrge_token_scores_grad"), 0, stream)
+        return dlogits
+
+
+class MxFormat(_Operator):
+    """Rows in microscaled 4-bit floating point and back (cdrge_mx_quantize, cdrge_mx_dequantize)."""
+
+    def __init__(self, cfg: cdrge_mx_config, device=None):
+        super().__init__(cfg, _gpu(device))
+        cdrge_mx_workspace_bytes(cfg, 0)
+        self.blocks = (cfg.in_features + 31) // 32
+
+    def empty(self, n_rows: int):
+        """codes and scales for n_rows rows, not filled."""
+        e, u8 = self._torch.empty, self._torch.uint8
+        return e((n_rows, 16 * self.blocks), dtype=u8, device=self.device), e((n_rows, self.blocks), dtype=u8, device=self.device)
+
+    def _args(self, x, codes, scales):
+        n, at, u8 = x.shape[0], self.index, self._torch.uint8
+        return (n, _rows("x", x, self.dtype, (n, self.cfg.in_features), at), _row_stride(x),
+                _whole("codes", codes, u8, (n, 16 * self.blocks), at), _whole("scales", scales, u8, (n, self.blocks), at))
+
+    def quantize(self, x, codes, scales, stream=None):
+        """Fills codes and scales from the rows of x. Returns both."""
+        n, p_x, x_stride, p_codes, p_scales = self._args(x, codes, scales)
+        call = self._lib.cdrge_mx_quantize
+        self._run(lambda ws, s: _check(call(self._cfg, n, p_x, x_stride, p_codes, p_scales, s), "cdrge_mx_quantize"), 0, stream)
+        return codes, scales
+
+    def dequantize(self, codes, scales, x, stream=None):
+        """Fills the rows of x with the values that codes and scales stand for. Returns x."""
+        n, p_x, x_stride, p_codes, p_scales = self._args(x, codes, scales)
+        call = self._lib.cdrge_mx_dequantize
+        self._run(lambda ws, s: _check(call(self._cfg, n, p_codes, p_scales, p_x, x_stride, s), "cdrge_mx_dequantize"), 0, stream)
+        return x
+
+
+class MxProjection(_Operator):
+    """A projection by weights in microscaled 4-bit floating point (cdrge_mx_project): codes and scales as MxFormat makes
+    them of the [out, in] weights, bias [out] in the operator's type or None."""
+
+    def __init__(self, cfg: cdrge_mx_config, codes, scales, bias=None):
+        super().__init__(cfg, _cuda_device(codes, "codes"))
+        cdrge_mx_workspace_bytes(cfg, 0)
+        O, blocks, at, u8 = cfg.out_features, (cfg.in_features + 31) // 32, self.index, self._torch.uint8
+        self._held = (codes, scales, bias)
+        self._weights = (_whole("codes", codes, u8, (O, 16 * blocks), at), _whole("scales", scales, u8, (O, blocks), at),
+                         0 if bias is None else _whole("bias", bias, self.dtype, (O,), at))
+
+    def project(self, x, y, stream=None):
+        """y[r] = weight Q(x[r]) + bias, with Q the row in four bits. Returns y."""
+        n, cfg, at, t = x.shape[0], self.cfg, self.index, self.dtype
+        p_x = _rows("x", x, t, (n, cfg.in_features), at)
+        p_y = _rows("y", y, t, (n, cfg.out_features), at)
+        nbytes = self._bytes(cdrge_mx_workspace_bytes, n)
+        call = self._lib.cdrge_mx_project
+        x_stride, y_stride = _row_stride(x), _row_stride(y)
+        self._run(lambda ws, s: _check(call(self._cfg, *self._weights, n, p_x, x_stride, p_y, y_stride,
+                                            0 if ws is None else ws.data_ptr(), nbytes, s), "cdrge_mx_project"),
+                  nbytes, stream)
+        return y

@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libcdrge.so")
 ARCH = "gfx950"
 
-SOURCES = ("cdrge.hip", "scan.hip", "adapters.hip", "distill.hip")
+SOURCES = ("cdrge.hip", "scan.hip", "adapters.hip", "distill.hip", "delta.hip", "scores.hip", "mx.hip")
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
