@@ -2,6 +2,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "cdrge.h"
@@ -83,12 +84,25 @@ DeltaArgs make_args(const cdrge_delta_config* c, const cdrge_delta_weights* w, c
 
 // How a prompt call is cut up and where its workspace's parts lie; by sizes alone.
 struct Plan {
+  bool tokens;  // k_delta_tokens
+  int kn;       // key_dim as the kernels of blocks have it
   int max_blocks;
-  size_t slots, counts, start, bounds, block_of, piece_of, total;
+  size_t slots, counts, start, bounds, block_of, piece_of, groups, heads, total;
 };
 
-Plan make_plan(int64_t n_tokens, int32_t n_seqs, bool equal) {
+// Short sequences are taken token by token.
+constexpr int kShort = 16;
+
+template <class T>
+void block_bytes(int kn, size_t* group, size_t* head) {
+  *group = kn == 128 ? DeltaBlock<T, 128>::kGroupBytes : DeltaBlock<T, 256>::kGroupBytes;
+  *head = kn == 128 ? DeltaBlock<T, 128>::kHeadBytes : DeltaBlock<T, 256>::kHeadBytes;
+}
+
+Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bool equal) {
   Plan p{};
+  p.tokens = n_tokens <= int64_t(kShort) * n_seqs;
+  p.kn = c->key_dim <= 128 ? 128 : 256;
   const int64_t blocks = equal ? int64_t(n_seqs) * scan_blocks_of(n_tokens / n_seqs) : n_tokens / kScanBlock + n_seqs;
   p.max_blocks = static_cast<int>(blocks);
   size_t at = 0;
@@ -104,6 +118,15 @@ Plan make_plan(int64_t n_tokens, int32_t n_seqs, bool equal) {
     p.bounds = region(sizeof(int2) * n_seqs);
     p.block_of = region(sizeof(int2) * blocks);
     p.piece_of = region(sizeof(int2) * n_seqs);
+  }
+  if (!p.tokens) {
+    size_t group = 0, head = 0;
+    if (c->dtype == CDRGE_F32)
+      block_bytes<float>(p.kn, &group, &head);
+    else
+      block_bytes<uint16_t>(p.kn, &group, &head);
+    p.groups = region(group * c->n_groups * blocks);
+    p.heads = region(head * c->n_heads * blocks);
   }
   p.total = at;
   return p;
@@ -151,13 +174,44 @@ cdrge_status enqueue_tokens(const DeltaArgs& a, const ScanWork& w, hipStream_t s
   return launch_tokens<T, 64, 8, kStep>(a, w, s);
 }
 
+template <class T, int kN>
+cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, hipStream_t s) {
+  using Block = DeltaBlock<T, kN>;
+  a.s.ptiles = (a.s.P + 15) / 16;
+  const int64_t n = int64_t(a.s.n_seqs) * a.s.H * a.s.ptiles;
+  a.s.owned = scan_owned(a.s.slots, a.s.n_seqs, n);
+  if (a.s.owned) {
+    hipLaunchKernelGGL(k_scan_owners, dim3((a.s.n_seqs + 63) / 64), dim3(64 * kScanOwnerWaves), 0, s, a.s, w.slots);
+    CDRGE_HIP(hipGetLastError());
+  }
+  constexpr size_t kLds = 1024 * 4 * (kN / 32) * Block::kRaw + sizeof(float) * 2 * 64 * kDeltaRow;
+  if (kLds > 64 * 1024) {
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use this much LDS
+    int dev = 0;
+    CDRGE_HIP(hipGetDevice(&dev));
+    if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+      CDRGE_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k_delta_blocks<T, kN>),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
+      ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
+    }
+  }
+  hipLaunchKernelGGL((k_delta_blocks<T, kN>), grid_of(int64_t(w.max_blocks) * a.s.H, 256), dim3(256), kLds, s, a, w, d);
+  CDRGE_HIP(hipGetLastError());
+  hipLaunchKernelGGL((k_delta_heads<T, kN>), grid_of(n, 256), dim3(256), 0, s, a, w, d);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
+}
+
 template <class T>
-cdrge_status enqueue_prompt(const DeltaArgs& a, const ScanWork& w, hipStream_t s) {
+cdrge_status enqueue_prompt(const DeltaArgs& a, const Plan& p, void* ws, hipStream_t s) {
+  const ScanWork w = make_work(p, ws);
   if (a.s.offsets) {
     hipLaunchKernelGGL(k_scan_map, dim3(1), dim3(1024), 0, s, a.s, w);
     CDRGE_HIP(hipGetLastError());
   }
-  return enqueue_tokens<T, false>(a, w, s);
+  if (p.tokens) return enqueue_tokens<T, false>(a, w, s);
+  const DeltaWork d{static_cast<char*>(ws) + p.groups, static_cast<char*>(ws) + p.heads};
+  return p.kn == 128 ? launch_blocks<T, 128>(a, w, d, s) : launch_blocks<T, 256>(a, w, d, s);
 }
 
 // Whether the call's sizes fit the kernels' 32-bit counts.
@@ -176,8 +230,8 @@ cdrge_status cdrge_delta_workspace_bytes(const cdrge_delta_config* cfg, int64_t 
   const cdrge_status st = check_config(cfg);
   if (st != CDRGE_OK) return st;
   if (!fits(cfg, n_tokens, n_seqs)) return CDRGE_ERR_UNSUPPORTED;
-  *bytes_out = make_plan(n_tokens, n_seqs, false).total;
-  if (n_tokens % n_seqs == 0) *bytes_out = std::max(*bytes_out, make_plan(n_tokens, n_seqs, true).total);
+  *bytes_out = make_plan(cfg, n_tokens, n_seqs, false).total;
+  if (n_tokens % n_seqs == 0) *bytes_out = std::max(*bytes_out, make_plan(cfg, n_tokens, n_seqs, true).total);
   return CDRGE_OK;
 }
 
@@ -192,9 +246,9 @@ cdrge_status cdrge_delta_prompt(const cdrge_delta_config* cfg, const cdrge_delta
   if (!workspace || workspace_bytes < need || !aligned(workspace, kAlign))
     return workspace_error("cdrge_delta_prompt", need, workspace ? workspace_bytes : 0);
   const DeltaArgs a = make_args(cfg, weights, io);
-  const ScanWork w = make_work(make_plan(io->n_tokens, io->n_seqs, !io->offsets), workspace);
+  const Plan p = make_plan(cfg, io->n_tokens, io->n_seqs, !io->offsets);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, w, s) : enqueue_prompt<uint16_t>(a, w, s);
+  return cfg->dtype == CDRGE_F32 ? enqueue_prompt<float>(a, p, workspace, s) : enqueue_prompt<uint16_t>(a, p, workspace, s);
 }
 
 cdrge_status cdrge_delta_step(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
