@@ -87,6 +87,8 @@ struct Plan {
   bool tokens;  // k_delta_tokens
   int kn;       // key_dim as the kernels of blocks have it
   int max_blocks;
+  bool direct;  // as in DeltaWork
+  size_t group_bytes;
   size_t slots, counts, start, bounds, block_of, piece_of, groups, heads, total;
 };
 
@@ -94,8 +96,8 @@ struct Plan {
 constexpr int kShort = 16;
 
 template <class T>
-void block_bytes(int kn, size_t* group, size_t* head) {
-  *group = kn == 128 ? DeltaBlock<T, 128>::kGroupBytes : DeltaBlock<T, 256>::kGroupBytes;
+void block_bytes(int kn, size_t* keys, size_t* head) {
+  *keys = kn == 128 ? DeltaBlock<T, 128>::kKeys : DeltaBlock<T, 256>::kKeys;
   *head = kn == 128 ? DeltaBlock<T, 128>::kHeadBytes : DeltaBlock<T, 256>::kHeadBytes;
 }
 
@@ -120,12 +122,14 @@ Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bo
     p.piece_of = region(sizeof(int2) * n_seqs);
   }
   if (!p.tokens) {
-    size_t group = 0, head = 0;
+    size_t keys = 0, head = 0;
     if (c->dtype == CDRGE_F32)
-      block_bytes<float>(p.kn, &group, &head);
+      block_bytes<float>(p.kn, &keys, &head);
     else
-      block_bytes<uint16_t>(p.kn, &group, &head);
-    p.groups = region(group * c->n_groups * blocks);
+      block_bytes<uint16_t>(p.kn, &keys, &head);
+    p.direct = c->dtype == CDRGE_BF16 && c->key_dim == p.kn;
+    p.group_bytes = (p.direct ? 1 : 3) * keys;
+    p.groups = region(p.group_bytes * c->n_groups * blocks);
     p.heads = region(head * c->n_heads * blocks);
   }
   p.total = at;
@@ -197,7 +201,10 @@ cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, h
   }
   hipLaunchKernelGGL((k_delta_blocks<T, kN>), grid_of(int64_t(w.max_blocks) * a.s.H, 256), dim3(256), kLds, s, a, w, d);
   CDRGE_HIP(hipGetLastError());
-  hipLaunchKernelGGL((k_delta_heads<T, kN>), grid_of(n, 256), dim3(256), 0, s, a, w, d);
+  if (sizeof(T) == 2 && d.direct)
+    hipLaunchKernelGGL((k_delta_heads<T, kN, sizeof(T) == 2>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
+  else
+    hipLaunchKernelGGL((k_delta_heads<T, kN, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -210,7 +217,7 @@ cdrge_status enqueue_prompt(const DeltaArgs& a, const Plan& p, void* ws, hipStre
     CDRGE_HIP(hipGetLastError());
   }
   if (p.tokens) return enqueue_tokens<T, false>(a, w, s);
-  const DeltaWork d{static_cast<char*>(ws) + p.groups, static_cast<char*>(ws) + p.heads};
+  const DeltaWork d{static_cast<char*>(ws) + p.groups, static_cast<char*>(ws) + p.heads, static_cast<int64_t>(p.group_bytes), p.direct};
   return p.kn == 128 ? launch_blocks<T, 128>(a, w, d, s) : launch_blocks<T, 256>(a, w, d, s);
 }
 

@@ -184,40 +184,53 @@ __global__ __launch_bounds__(256) void k_delta_tokens(DeltaArgs a, ScanWork w) {
 //
 //   N' = U (V - diag(e^G r) K S^T),  Y = diag(e^G s) Q S^T + P N',  S' = e^G_last S + (diag(e^(G_last - G)) N')^T K
 //
-// k_delta_blocks forms U, P, the factors, and K and Q as operands, for all blocks at once; k_delta_heads walks a
-// sequence's blocks for 16 values of one head, with S in the registers of four waves that share the keys. What a block's
-// products leave is joined through LDS three times: the waves' parts of K S^T and Q S^T, V's rest, and N'.
+// k_delta_blocks forms U, P and the factors for all blocks at once, and K and Q as operands where they are not such as
+// they lie; k_delta_heads walks a sequence's blocks for 16 values of one head. Four of its waves share the keys and hold S
+// in their registers; what a block's products leave is joined through LDS three times: the waves' parts of K S^T, V's
+// rest, and N'. Four further waves form y from S and N', beside that chain.
 //
 // Operands of the matrix cores are bf16 (K, Q of bf16 tensors as they are), others the sum of three bf16 parts, which
 // hold 24 bits whatever the magnitude; of two such operands the six products that reach 2^-24 are taken. For y in bf16 two
 // parts (16 bits) do: they move it by 2e-5 of it.
 //
-// Along a reduction the order is free if both operands have it: entry e of lane group q stands for index
-// 16 (e / 4) + 4 q + e % 4 of 32, so that a product's result is the next one's operand in the lane where it lies.
+// Along a reduction the order is free if both operands have it, and so is that of a result's rows. Keys: entry e of lane
+// group q is key 8 q + e of 32, and row m of a state's tile t is key 8 (m / 4) + 4 t + m % 4. Tokens: entry e of lane
+// group q is token 16 (e / 4) + 4 q + e % 4. So a product's result is the next one's operand in the lane where it lies.
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ f32x4 mma_bf16(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-// Entry e of the parts of v; v is pinned as one float (see split_half).
+// An operand as the sum of kParts of bf16, two entries to a word.
 template <int kParts>
-__device__ __forceinline__ void split_bf16(float v, bf16x8 (&to)[kParts], int e) {
-  asm("" : "+v"(v));
+struct Parts {
+  uint32_t w[kParts][4];
+  __device__ __forceinline__ void set(int pair, float v0, float v1) {
 #pragma unroll
-  for (int p = 0; p < kParts; ++p) {
-    const __bf16 part = static_cast<__bf16>(v);
-    to[p][e] = part;
-    v -= static_cast<float>(part);
+    for (int p = 0; p < kParts; ++p) {
+      w[p][pair] = bf16_pair(v0, v1);
+      if (p + 1 < kParts) asm("" : "+v"(w[p][pair]));  // one conversion, not another for each half
+      v0 -= __uint_as_float(w[p][pair] << 16);
+      v1 -= __uint_as_float(w[p][pair] & 0xffff0000u);
+    }
   }
-}
+  __device__ __forceinline__ bf16x8 part(int p) const {
+    bf16x8 v;
+    __builtin_memcpy(&v, w[p], 16);
+    return v;
+  }
+};
 
-// c + a b, the products of parts that reach the last part's bits; small ones first.
-template <int kA, int kB, int kReach>
-__device__ __forceinline__ f32x4 mma_parts(const bf16x8 (&a)[kA], const bf16x8 (&b)[kB], f32x4 c) {
+// c[m] + a[m] b for kM operands a, the products of parts that reach 2^(-8 kReach), small ones first. Products that do not
+// wait for each other stand next to each other: one that takes the sum of the one before it waits three times as long as
+// it takes.
+template <int kReach, int kM, int kA, int kB>
+__device__ __forceinline__ void mma_parts(const bf16x8 (&a)[kM][kA], const Parts<kB>& b, f32x4 (&c)[kM]) {
 #pragma unroll
   for (int s = kReach - 1; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < kA; ++i)
-      if (s - i >= 0 && s - i < kB) c = mma_bf16(a[i], b[s - i], c);
-  return c;
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+        if (s - i >= 0 && s - i < kB) c[m] = mma_bf16(a[m][i], b.part(s - i), c[m]);
 }
 
 template <class T>
@@ -232,23 +245,24 @@ struct DeltaParts<uint16_t> {
 };
 
 // What k_delta_blocks leaves, as operands of 1 KB (16 bytes a lane).
-//   for a block and group  k, q   [step kN / 32][strip 4][part]: token 16 strip + l16, keys of the step
-//                          kt     [tile kN / 16][step 2][part]: key 16 tile + l16, tokens of the step
+//   for a block and group  kt     [tile kN / 16][step 2][part]: keys of a state's tile, tokens of the step
+//                          k, q   [strip 4][step kN / 32][part]: token 16 strip + l16, keys of the step (not for `direct`)
 //   for a block and head   u, p   [pair 6][part]: token 16 strip + l16, tokens of the step; pairs (strip, step) with
 //                                 step <= strip / 2, in order
 //                          factors: e^G r, e^G s and e^(G_last - G) of 64 tokens each, e^G_last
 template <class T, int kN>
 struct DeltaBlock {
   static constexpr int kRaw = DeltaParts<T>::kRaw, kOut = DeltaParts<T>::kOut;
-  static constexpr int kKeys = 1024 * (kN / 32) * 4 * kRaw;  // of k, of q and of kt
-  static constexpr int kGroupBytes = 3 * kKeys;
+  static constexpr int kKeys = 1024 * (kN / 32) * 4 * kRaw;  // of kt, of k and of q
   static constexpr int kOffP = 6 * 3 * 1024, kOffFactors = kOffP + 6 * kOut * 1024, kHeadBytes = kOffFactors + 1024;
 };
 __host__ __device__ constexpr int delta_pair(int strip, int step) { return strip + (strip > 2) + step; }
 
 struct DeltaWork {
   char* groups;  // [block][group]
-  char* heads;   // [block][head]
+  char* heads;   // [block][head]; with a head's blocks together the call below takes 363 us instead of 332
+  int64_t group_bytes;
+  bool direct;  // K and Q in bf16 with rows of kN keys are operands as they lie: k_delta_heads reads the tensors
 };
 
 constexpr int kDeltaRow = 68;  // floats of a row of a 64 x 64 matrix in LDS
@@ -288,51 +302,55 @@ __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, D
   const int64_t row0 = sq.first + static_cast<int64_t>(at.y) * kScanBlock;
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);
   if (L <= 0) return;  // a sequence without rows
-  char* const group = d.groups + (static_cast<int64_t>(block) * s.G + g) * Block::kGroupBytes;
+  char* const group = d.groups + (static_cast<int64_t>(block) * s.G + g) * d.group_bytes;
   char* const head = d.heads + (static_cast<int64_t>(block) * s.H + h) * Block::kHeadBytes;
   const bool first = h % rep == 0;
 
   // this wave's rows of K and Q
   const int i = 16 * wave + l16, N = s.N;
-  bf16x8 kf[kSteps][kRaw], qf[kSteps][kRaw];
-  float kk = 0.f, qq = 0.f;
+  bf16x8 kf[kSteps][kRaw];
+  Parts<kRaw> kq[kSteps], qq[kSteps];
+  float k2 = 0.f, q2 = 0.f;
   {
     const int64_t row = row0 + min(i, L - 1);
     const T* const kp = static_cast<const T*>(a.k) + row * a.k_stride + static_cast<int64_t>(g) * N;
     const T* const qp = static_cast<const T*>(a.q) + row * a.q_stride + static_cast<int64_t>(g) * N;
 #pragma unroll
-    for (int n = 0; n < kSteps; ++n)
+    for (int n = 0; n < kSteps; ++n) {
+      const int c = 32 * n + 8 * q, have = i < L ? N - c : 0;
+      Four<T> kv[2], qv[2];
+      kv[0].load(kp + c, have);
+      kv[1].load(kp + c + 4, have - 4);
+      qv[0].load(qp + c, have);
+      qv[1].load(qp + c + 4, have - 4);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int c = 32 * n + 16 * half + 4 * q, have = i < L ? N - c : 0;
-        Four<T> kv, qv;
-        kv.load(kp + c, have);
-        qv.load(qp + c, have);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kk += kv.at(e) * kv.at(e);
-          qq += qv.at(e) * qv.at(e);
-          split_bf16<kRaw>(kv.at(e), kf[n], 4 * half + e);
-          split_bf16<kRaw>(qv.at(e), qf[n], 4 * half + e);
-        }
+      for (int e = 0; e < 8; e += 2) {
+        const float k0 = kv[e >> 2].at(e & 3), k1 = kv[e >> 2].at((e & 3) + 1);
+        const float q0 = qv[e >> 2].at(e & 3), q1 = qv[e >> 2].at((e & 3) + 1);
+        k2 += k0 * k0 + k1 * k1;
+        q2 += q0 * q0 + q1 * q1;
+        kq[n].set(e >> 1, k0, k1);
+        qq[n].set(e >> 1, q0, q1);
       }
+    }
   }
 #pragma unroll
   for (int n = 0; n < kSteps; ++n)
 #pragma unroll
     for (int p = 0; p < kRaw; ++p) {
+      kf[n][p] = kq[n].part(p);
       kl[((wave * kSteps + n) * kRaw + p) * 64 + lane] = kf[n][p];
-      if (first) {
-        bf16x8* const to = reinterpret_cast<bf16x8*>(group) + ((n * 4 + wave) * kRaw + p) * 64 + lane;
+      if (first && !d.direct) {
+        bf16x8* const to = reinterpret_cast<bf16x8*>(group + Block::kKeys) + ((wave * kSteps + n) * kRaw + p) * 64 + lane;
         to[0] = kf[n][p];
-        to[Block::kKeys / 16] = qf[n][p];
+        to[Block::kKeys / 16] = qq[n].part(p);
       }
     }
-  kk += __shfl_xor(kk, 16);
-  qq += __shfl_xor(qq, 16);
-  kk += __shfl_xor(kk, 32);
-  qq += __shfl_xor(qq, 32);
-  const float rk = i < L ? delta_norm(kk, a.norm_eps) : 0.f, rq = i < L ? a.q_scale * delta_norm(qq, a.norm_eps) : 0.f;
+  k2 += __shfl_xor(k2, 16);
+  q2 += __shfl_xor(q2, 16);
+  k2 += __shfl_xor(k2, 32);
+  q2 += __shfl_xor(q2, 32);
+  const float rk = i < L ? delta_norm(k2, a.norm_eps) : 0.f, rq = i < L ? a.q_scale * delta_norm(q2, a.norm_eps) : 0.f;
   if (q == 0) {
     srk[i] = rk;
     srq[i] = rq;
@@ -369,43 +387,55 @@ __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, D
     for (int strip = 0; strip <= (wave | 1); ++strip) {
       f32x4 kkt = {0.f, 0.f, 0.f, 0.f}, qkt = kkt;
       if (strip <= wave) {
+        f32x4 sum[2][2] = {{kkt, kkt}, {kkt, kkt}};
 #pragma unroll
         for (int n = 0; n < kSteps; ++n) {
           bf16x8 kj[kRaw];
 #pragma unroll
           for (int p = 0; p < kRaw; ++p) kj[p] = kl[((strip * kSteps + n) * kRaw + p) * 64 + lane];
-          kkt = mma_parts<kRaw, kRaw, kRaw>(kj, kf[n], kkt);
-          qkt = mma_parts<kRaw, kRaw, kRaw>(kj, qf[n], qkt);
+#pragma unroll
+          for (int p = kRaw - 1; p >= 0; --p)
+#pragma unroll
+            for (int o = 0; o < kRaw; ++o)
+              if (p - o >= 0) {
+                sum[0][n & 1] = mma_bf16(kj[o], kq[n].part(p - o), sum[0][n & 1]);
+                sum[1][n & 1] = mma_bf16(kj[o], qq[n].part(p - o), sum[1][n & 1]);
+              }
         }
+        kkt = sum[0][0] + sum[0][1];
+        qkt = sum[1][0] + sum[1][1];
       }
       f32x4 low;
-      bf16x8 p[kOut];
+      float p[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * strip + 4 * q + r;
         const float fall = j <= i ? __builtin_amdgcn_exp2f((gi - sg[j]) + (gli - sgl[j])) : 0.f;
         low[r] = j < i ? bi * srk[j] * kkt[r] * fall : 0.f;
-        split_bf16<kOut>(j <= i ? rq * qkt[r] * fall : 0.f, p, r);
+        p[r] = j <= i ? rq * qkt[r] * fall : 0.f;
       }
       if (strip <= wave) *reinterpret_cast<f32x4*>(lm + i * kDeltaRow + 16 * strip + 4 * q) = low;
+      Parts<kOut> pp;
+      pp.set(0, p[0], p[1]);
+      pp.set(1, p[2], p[3]);
 #pragma unroll
       for (int o = 0; o < kOut; ++o)
-        __builtin_memcpy(head + Block::kOffP + (delta_pair(wave, strip >> 1) * kOut + o) * 1024 + lane * 16 + 8 * (strip & 1), &p[o], 8);
+        __builtin_memcpy(head + Block::kOffP + (delta_pair(wave, strip >> 1) * kOut + o) * 1024 + lane * 16 + 8 * (strip & 1), pp.w[o], 8);
     }
   }
   if (first) {  // K on its side
     const uint16_t* const kb = reinterpret_cast<const uint16_t*>(kl);
     for (int f = wave; f < kN / 8; f += 4) {
-      const int n = 16 * (f >> 1) + l16;
+      const int tile = f >> 1, nn = 8 * (l16 >> 2) + 4 * (tile & 1) + (l16 & 3);  // of the step's 32 keys
 #pragma unroll
       for (int p = 0; p < kRaw; ++p) {
         uint16_t v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int t = 32 * (f & 1) + 16 * (e >> 2) + 4 * q + (e & 3);
-          v[e] = kb[((((t >> 4) * kSteps + (n >> 5)) * kRaw + p) * 64 + (t & 15) + 16 * ((n & 15) >> 2)) * 8 + 4 * (n >> 4 & 1) + (n & 3)];
+          v[e] = kb[((((t >> 4) * kSteps + (tile >> 1)) * kRaw + p) * 64 + (t & 15) + 16 * (nn >> 3)) * 8 + (nn & 7)];
         }
-        __builtin_memcpy(group + 2 * Block::kKeys + (f * kRaw + p) * 1024 + lane * 16, v, 16);
+        __builtin_memcpy(group + (f * kRaw + p) * 1024 + lane * 16, v, 16);
       }
     }
   }
@@ -453,28 +483,54 @@ __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, D
 #pragma unroll
   for (int step = 0; step < 2; ++step) {
     if (step > wave >> 1) break;
-    bf16x8 u[3];
+    Parts<3> u;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int strip = 2 * step + half, j = 16 * strip + 4 * q;
       const f32x4 v = strip <= wave ? *reinterpret_cast<const f32x4*>(tm + i * kDeltaRow + j) : zero;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) split_bf16<3>(rk * v[r] * sb[j + r], u, 4 * half + r);
+      u.set(2 * half, rk * v[0] * sb[j], rk * v[1] * sb[j + 1]);
+      u.set(2 * half + 1, rk * v[2] * sb[j + 2], rk * v[3] * sb[j + 3]);
     }
 #pragma unroll
-    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(head + (delta_pair(wave, step) * 3 + p) * 1024 + lane * 16) = u[p];
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(head + (delta_pair(wave, step) * 3 + p) * 1024 + lane * 16) = u.part(p);
   }
 }
 
-// The blocks of a sequence for 16 values of a head (see above). Wave n holds the state at keys 32 kW n + 16 tile + 4 q + r
-// and value l16; of a block's tokens it takes 16 n + 4 q + r. Each operand is requested again, for the next block, when
-// this block has used it.
-template <class T, int kN>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && kN <= 128 ? 2 : 1) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
+// Where a lane's rows of a tensor lie, one block of tokens after the other: rows at(r) of the block and column `col`;
+// past the sequence's end its last row.
+template <class T, int kRows>
+struct DeltaRows {
+  const T* ptr[kRows];
+  int64_t block;  // elements of a block's rows
+  template <class At>
+  __device__ __forceinline__ DeltaRows(const T* from, int64_t stride, int len, int64_t col, At at) : block(stride * kScanBlock) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) ptr[r] = from + min(at(r), max(len - 1, 0)) * stride + col;
+  }
+  // to block b of `blocks`, from the one before it
+  template <class At>
+  __device__ __forceinline__ void to(int b, int blocks, const T* from, int64_t stride, int len, int64_t col, At at) {
+    if ((b + 1) * kScanBlock <= len) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) ptr[r] += block;
+    } else if (b < blocks) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) ptr[r] = from + static_cast<int64_t>(min(b * kScanBlock + at(r), len - 1)) * stride + col;
+    }
+  }
+};
+
+// The blocks of a sequence for 16 values of a head (see above). Wave n of the first four holds the state at keys
+// 32 (kW n + t / 2) + 8 q + 4 (t % 2) + r, tile t, and value l16, and takes a block's tokens 16 n + 4 q + r, as does wave 4 + n
+// for y. An operand is requested again, for the next block, when this block has used it.
+template <class T, int kN, bool kDirect>
+__global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
-  constexpr int kRaw = Block::kRaw, kOut = Block::kOut, kW = kN / 128;  // steps of 32 keys a wave has
-  __shared__ f32x4 parts[2][4][4][64];                                   // of K S^T and Q S^T: [wave][strip]
-  __shared__ bf16x8 rest[2][3][64], wide[2][3][64], out[2][kOut][64];    // V's rest, N' faded, N': [step][part]
+  constexpr int kRaw = Block::kRaw, kOut = Block::kOut, kW = kN / 128, kSteps = kN / 32;
+  __shared__ f32x4 ks_parts[4][4][64];           // [wave][strip]: parts of K S^T
+  __shared__ uint4 state[kSteps][kOut][64];      // S as y's operand
+  __shared__ uint4 rest[2][3][64], wide[2][3][64];  // [step][part]: V's rest, N' faded
+  __shared__ f32x4 news[4][64];                  // [strip]: N'
   const ScanArgs& s = a.s;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
 
@@ -489,217 +545,303 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && kN <= 128 ? 2 : 1) void k_de
   const ScanSeq sq = scan_seq(s, w, i);
   const int p0 = 16 * tile, np = min(16, s.P - p0), g = h / (s.H / s.G), N = s.N;
   const bool mine = l16 < np;
-  T* const y = static_cast<T*>(s.y) + sq.first * s.y_stride + static_cast<int64_t>(h) * s.P + p0 + l16;
+  T* const y = static_cast<T*>(s.y) + sq.first * s.y_stride + static_cast<int64_t>(h) * s.P + p0;
   int slot = -1, pos = 0;
   if (s.ssm_in) {
     slot = s.owned ? w.slots[i] : scan_slot(s, i);
     if (slot == -2) {
-      for (int64_t t = tid >> 4; t < sq.len; t += 16)
-        if (mine) y[t * s.y_stride] = from_float<T>(__builtin_nanf(""));
+      for (int64_t t = tid >> 4; t < sq.len; t += 32)
+        if (mine) y[t * s.y_stride + l16] = from_float<T>(__builtin_nanf(""));
       return;
     }
     if (slot >= 0 && s.positions) pos = max(s.positions[i], 0);
   }
 
-  f32x4 st[2 * kW];
-  const int64_t place = ((static_cast<int64_t>(max(slot, 0)) * s.H + h) * s.P + p0 + l16) * N + 32 * kW * wave + 4 * q;
-  const int have0 = N - 32 * kW * wave - 4 * q;
-  const bool vec = N % 4 == 0;
+  const int blocks = sq.len > 0 ? sq.blocks : 0;
+  const char* group = d.groups + (static_cast<int64_t>(sq.block0) * s.G + g) * d.group_bytes;
+  const char* head = d.heads + (static_cast<int64_t>(sq.block0) * s.H + h) * Block::kHeadBytes;
+  const int64_t group_next = s.G * d.group_bytes, head_next = static_cast<int64_t>(s.H) * Block::kHeadBytes;
+
+  if (wave < 4) {
+    __builtin_amdgcn_s_setprio(3);  // the chain, before what hangs on it
+    f32x4 st[2 * kW];
+    const int key0 = 32 * kW * wave + 8 * q;
+    const int64_t place = ((static_cast<int64_t>(max(slot, 0)) * s.H + h) * s.P + p0 + l16) * N + key0;
+    const bool vec = N % 4 == 0;
 #pragma unroll
-  for (int t = 0; t < 2 * kW; ++t) {
-    st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int have = mine ? have0 - 16 * t : 0;
-    if (slot >= 0 && pos > 0 && have > 0) {
-      const float* const from = s.ssm_in + place + 16 * t;
-      if (vec) {
-        st[t] = *reinterpret_cast<const f32x4*>(from);
-      } else {
+    for (int t = 0; t < 2 * kW; ++t) {
+      st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int more = 32 * (t >> 1) + 4 * (t & 1), have = mine ? N - key0 - more : 0;
+      if (slot >= 0 && pos > 0 && have > 0) {
+        const float* const from = s.ssm_in + place + more;
+        if (vec) {
+          st[t] = *reinterpret_cast<const f32x4*>(from);
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < have) st[t][r] = from[r];
+          for (int r = 0; r < 4; ++r)
+            if (r < have) st[t][r] = from[r];
+        }
       }
     }
-  }
 
-  const int blocks = sq.len > 0 ? sq.blocks : 0;
-  const char* const groups = d.groups + (static_cast<int64_t>(sq.block0) * s.G + g) * Block::kGroupBytes + lane * 16;
-  const char* const heads = d.heads + (static_cast<int64_t>(sq.block0) * s.H + h) * Block::kHeadBytes;
-  const int64_t group_next = static_cast<int64_t>(s.G) * Block::kGroupBytes, head_next = static_cast<int64_t>(s.H) * Block::kHeadBytes;
-  // columns past the head's last value read that one's rows, and are dropped
-  const T* const v = static_cast<const T*>(a.v) + sq.first * a.v_stride + static_cast<int64_t>(h) * s.P + p0 + min(l16, np - 1);
-  bf16x8 kf[kW][4][kRaw], qf[kW][4][kRaw], kt[2 * kW][2][kRaw], u[2][3], p[2][kOut];
-  T vv[4];
-  f32x4 fk, fq, fe;
-  float fade = 0.f;
-  auto load_keys = [&](int b) {
-    const bf16x8* const from = reinterpret_cast<const bf16x8*>(groups + b * group_next) + kW * wave * 4 * kRaw * 64;
+    const T* const k_rows = static_cast<const T*>(a.k) + sq.first * a.k_stride + static_cast<int64_t>(g) * N;
+    const T* const v_rows = static_cast<const T*>(a.v) + sq.first * a.v_stride + static_cast<int64_t>(h) * s.P + p0;
+    auto key_row = [&](int r) { return 16 * r + l16; };
+    auto value_row = [&](int r) { return 16 * wave + 4 * q + r; };
+    // columns past the head's last value read that one's rows, and are dropped
+    const int v_col = min(l16, np - 1);
+    DeltaRows<T, kDirect ? 4 : 1> keys(k_rows, a.k_stride, sq.len, key0, key_row);
+    DeltaRows<T, 4> values(v_rows, a.v_stride, sq.len, v_col, value_row);
+    // K and its turned form together would take 192 registers for float32 and wide states: there they are requested when
+    // the other one is done with
+    constexpr bool kAhead = kRaw * kW <= 3;
+    bf16x8 kf[kW][4][kRaw], kt[2 * kW][2][kRaw], u[2][3];
+    T vv[4];
+    f32x4 fk, fe;
+    float fade = 0.f;
+    auto load_keys = [&](const char* group) {
 #pragma unroll
-    for (int n = 0; n < kW; ++n)
+      for (int t = 0; t < 4; ++t) {
+        if (kDirect) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+          for (int n = 0; n < kW; ++n) __builtin_memcpy(&kf[n][t][0], keys.ptr[kDirect ? t : 0] + 32 * n, 16);
+        } else {
+          const bf16x8* const from = reinterpret_cast<const bf16x8*>(group + Block::kKeys) + (t * kSteps + kW * wave) * kRaw * 64;
 #pragma unroll
-        for (int o = 0; o < kRaw; ++o) {
-          kf[n][t][o] = from[((n * 4 + t) * kRaw + o) * 64];
-          qf[n][t][o] = from[((n * 4 + t) * kRaw + o) * 64 + Block::kKeys / 16];
+          for (int n = 0; n < kW; ++n)
+#pragma unroll
+            for (int o = 0; o < kRaw; ++o) kf[n][t][o] = from[(n * kRaw + o) * 64 + lane];
         }
-  };
-  auto load_kt = [&](int b) {
-    const bf16x8* const from = reinterpret_cast<const bf16x8*>(groups + b * group_next + 2 * Block::kKeys) + 2 * kW * wave * 2 * kRaw * 64;
+      }
+    };
+    auto load_kt = [&](const char* group, const char* head) {
+      const bf16x8* const from = reinterpret_cast<const bf16x8*>(group) + 2 * kW * wave * 2 * kRaw * 64;
 #pragma unroll
-    for (int t = 0; t < 2 * kW; ++t)
+      for (int t = 0; t < 2 * kW; ++t)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int o = 0; o < kRaw; ++o) kt[t][n][o] = from[((t * 2 + n) * kRaw + o) * 64 + lane];
+      fade = *reinterpret_cast<const float*>(head + Block::kOffFactors + 768);
+    };
+    auto load_u = [&](const char* head) {
+      const bf16x8* const from = reinterpret_cast<const bf16x8*>(head) + delta_pair(wave, 0) * 3 * 64;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int o = 0; o < kRaw; ++o) kt[t][n][o] = from[((t * 2 + n) * kRaw + o) * 64];
-  };
-  auto load_u = [&](int b) {
-    const bf16x8* const from = reinterpret_cast<const bf16x8*>(heads + b * head_next) + delta_pair(wave, 0) * 3 * 64 + lane;
+        for (int o = 0; o < 3; ++o)
+          if (n <= wave >> 1) u[n][o] = from[(n * 3 + o) * 64 + lane];
+      fe = *reinterpret_cast<const f32x4*>(head + Block::kOffFactors + 512 + (16 * wave + 4 * q) * 4);
+    };
+    auto load_values = [&](const char* head) {
+      fk = *reinterpret_cast<const f32x4*>(head + Block::kOffFactors + (16 * wave + 4 * q) * 4);
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+      for (int r = 0; r < 4; ++r) vv[r] = *values.ptr[r];
+    };
+    if (blocks > 0) {
+      if (kAhead) {
+        load_keys(group);
+        load_kt(group, head);
+      }
+      load_values(head);
+      load_u(head);
+    }
+    for (int b = 0; b < blocks; ++b) {
+      const bool more = b + 1 < blocks;
+      const char* const group_then = more ? group + group_next : group;
+      const char* const head_then = more ? head + head_next : head;
+      if (!kAhead) load_keys(group);
+      {
+        f32x4 ks[4];
 #pragma unroll
-      for (int o = 0; o < 3; ++o)
-        if (n <= wave >> 1) u[n][o] = from[(n * 3 + o) * 64];
+        for (int n = 0; n < kW; ++n) {
+          Parts<3> sp;
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) sp.set(e >> 1, st[2 * n + (e >> 2)][e & 3], st[2 * n + (e >> 2)][(e & 3) + 1]);
+#pragma unroll
+          for (int o = 0; o < kOut; ++o) __builtin_memcpy(&state[kW * wave + n][o][lane], sp.w[o], 16);
+          if (n == 0)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ks[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          mma_parts<3>(kf[n], sp, ks);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks_parts[wave][t][lane] = ks[t];
+      }
+      if (kAhead) {
+        if (kDirect) keys.to(b + 1, blocks, k_rows, a.k_stride, sq.len, key0, key_row);
+        load_keys(group_then);
+      } else {
+        load_kt(group, head);
+      }
+      __syncthreads();
+      {
+        f32x4 ks = ks_parts[0][wave][lane];
+#pragma unroll
+        for (int n = 1; n < 4; ++n) ks += ks_parts[n][wave][lane];
+        Parts<3> rp;
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) rp.set(r >> 1, to_float(vv[r]) - fk[r] * ks[r], to_float(vv[r + 1]) - fk[r + 1] * ks[r + 1]);
+#pragma unroll
+        for (int o = 0; o < 3; ++o) __builtin_memcpy(reinterpret_cast<char*>(&rest[wave >> 1][o][lane]) + 8 * (wave & 1), rp.w[o], 8);
+      }
+      values.to(b + 1, blocks, v_rows, a.v_stride, sq.len, v_col, value_row);
+      load_values(head_then);
+      __syncthreads();
+      {
+        // the three smallest products of a step, and the others
+        f32x4 sums[2][2];
+        Parts<3> rp[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          sums[n][0] = sums[n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (n > wave >> 1) break;
+#pragma unroll
+          for (int o = 0; o < 3; ++o) __builtin_memcpy(rp[n].w[o], &rest[n][o][lane], 16);
+        }
+        auto products = [&](int steps) {
+#pragma unroll
+          for (int o = 0; o < 3; ++o)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              if (n >= steps) break;
+              sums[n][0] = mma_bf16(u[n][o], rp[n].part(2 - o), sums[n][0]);
+              sums[n][1] = mma_bf16(u[n][o == 0], rp[n].part(o == 1), sums[n][1]);
+            }
+        };
+        if (wave < 2)
+          products(1);
+        else
+          products(2);
+        const f32x4 nn = (sums[0][0] + sums[1][0]) + (sums[0][1] + sums[1][1]);
+        news[wave][lane] = nn;
+        Parts<3> np3;
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) np3.set(r >> 1, fe[r] * nn[r], fe[r + 1] * nn[r + 1]);
+#pragma unroll
+        for (int o = 0; o < 3; ++o) __builtin_memcpy(reinterpret_cast<char*>(&wide[wave >> 1][o][lane]) + 8 * (wave & 1), np3.w[o], 8);
+      }
+      load_u(head_then);
+      __syncthreads();
+      {
+        Parts<3> np3[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int o = 0; o < 3; ++o) __builtin_memcpy(np3[n].w[o], &wide[n][o][lane], 16);
+#pragma unroll
+        for (int t = 0; t < 2 * kW; ++t) st[t] *= fade;
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int o = 0; o < kRaw; ++o)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int t = 0; t < 2 * kW; ++t)
+                if (p - o >= 0) st[t] = mma_bf16(kt[t][n][o], np3[n].part(p - o), st[t]);
+      }
+      if (kAhead) load_kt(group_then, head_then);
+      group = group_then;
+      head = head_then;
+    }
+
+    if (slot < 0) return;
+#pragma unroll
+    for (int t = 0; t < 2 * kW; ++t) {
+      const int more = 32 * (t >> 1) + 4 * (t & 1), have = mine ? N - key0 - more : 0;
+      if (have <= 0) continue;
+      float* const to = s.ssm_out + place + more;
+      if (vec) {
+        *reinterpret_cast<f32x4*>(to) = st[t];
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < have) to[r] = st[t][r];
+      }
+    }
+    return;
+  }
+
+  const int strip = wave - 4;
+  const T* const q_rows = static_cast<const T*>(a.q) + sq.first * a.q_stride + static_cast<int64_t>(g) * N;
+  auto query_row = [&](int) { return 16 * strip + l16; };
+  DeltaRows<T, 1> queries(q_rows, a.q_stride, sq.len, 8 * q, query_row);
+  bf16x8 qf[kSteps][1][kRaw], p[2][kOut];
+  f32x4 fq;
+  auto load_queries = [&](const char* group, const char* head) {
+    if (kDirect) {
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n) __builtin_memcpy(&qf[n][0][0], queries.ptr[0] + 32 * n, 16);
+    } else {
+      const bf16x8* const from = reinterpret_cast<const bf16x8*>(group + 2 * Block::kKeys) + strip * kSteps * kRaw * 64;
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n)
+#pragma unroll
+        for (int o = 0; o < kRaw; ++o) qf[n][0][o] = from[(n * kRaw + o) * 64 + lane];
+    }
+    fq = *reinterpret_cast<const f32x4*>(head + Block::kOffFactors + 256 + (16 * strip + 4 * q) * 4);
   };
-  auto load_p = [&](int b) {
-    const bf16x8* const from = reinterpret_cast<const bf16x8*>(heads + b * head_next + Block::kOffP) + delta_pair(wave, 0) * kOut * 64 + lane;
+  auto load_p = [&](const char* head) {
+    const bf16x8* const from = reinterpret_cast<const bf16x8*>(head + Block::kOffP) + delta_pair(strip, 0) * kOut * 64;
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int o = 0; o < kOut; ++o)
-        if (n <= wave >> 1) p[n][o] = from[(n * kOut + o) * 64];
+        if (n <= strip >> 1) p[n][o] = from[(n * kOut + o) * 64 + lane];
   };
-  auto load_rows = [&](int b) {
-    const char* const f = heads + b * head_next + Block::kOffFactors + (16 * wave + 4 * q) * 4;
-    fk = *reinterpret_cast<const f32x4*>(f);
-    fq = *reinterpret_cast<const f32x4*>(f + 256);
-    fe = *reinterpret_cast<const f32x4*>(f + 512);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t t = static_cast<int64_t>(b) * kScanBlock + 16 * wave + 4 * q + r;
-      vv[r] = v[(t < sq.len ? t : sq.len - 1) * a.v_stride];
-    }
-  };
-  auto load_fade = [&](int b) { fade = *reinterpret_cast<const float*>(heads + b * head_next + Block::kOffFactors + 768); };
   if (blocks > 0) {
-    load_keys(0);
-    load_rows(0);
-    load_u(0);
-    load_p(0);
-    load_kt(0);
-    load_fade(0);
+    load_queries(group, head);
+    load_p(head);
   }
+  T* y_row = y + (16 * strip + 4 * q) * s.y_stride + l16;
   for (int b = 0; b < blocks; ++b) {
-    const int next = min(b + 1, blocks - 1);
-    {
-      f32x4 ks[4], qs[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) ks[t] = qs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int n = 0; n < kW; ++n) {
-        bf16x8 sp[3];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split_bf16<3>(st[2 * n + (e >> 2)][e & 3], sp, e);
-        bf16x8 so[kOut];
-#pragma unroll
-        for (int o = 0; o < kOut; ++o) so[o] = sp[o];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ks[t] = mma_parts<kRaw, 3, 3>(kf[n][t], sp, ks[t]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) qs[t] = mma_parts<kRaw, kOut, kOut>(qf[n][t], so, qs[t]);
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        parts[0][wave][t][lane] = ks[t];
-        parts[1][wave][t][lane] = qs[t];
-      }
-    }
-    load_keys(next);
-    __syncthreads();
-    f32x4 yy;
-    {
-      f32x4 ks = parts[0][0][wave][lane];
-      yy = parts[1][0][wave][lane];
-#pragma unroll
-      for (int n = 1; n < 4; ++n) {
-        ks += parts[0][n][wave][lane];
-        yy += parts[1][n][wave][lane];
-      }
-      bf16x8 rp[3];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const bool ok = mine && b * kScanBlock + 16 * wave + 4 * q + r < sq.len;
-        split_bf16<3>(ok ? to_float(vv[r]) - fk[r] * ks[r] : 0.f, rp, r);
-        yy[r] *= fq[r];
-      }
-#pragma unroll
-      for (int o = 0; o < 3; ++o) __builtin_memcpy(reinterpret_cast<char*>(&rest[wave >> 1][o][lane]) + 8 * (wave & 1), &rp[o], 8);
+    if (b + 1 < blocks) {
+      group += group_next;
+      head += head_next;
     }
     __syncthreads();
-    {
-      f32x4 nn = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        if (n > wave >> 1) break;
-        bf16x8 rp[3];
-#pragma unroll
-        for (int o = 0; o < 3; ++o) rp[o] = rest[n][o][lane];
-        nn = mma_parts<3, 3, 3>(u[n], rp, nn);
-      }
-      bf16x8 np3[3], npo[kOut];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        split_bf16<3>(fe[r] * nn[r], np3, r);
-        split_bf16<kOut>(nn[r], npo, r);
-      }
-#pragma unroll
-      for (int o = 0; o < 3; ++o) __builtin_memcpy(reinterpret_cast<char*>(&wide[wave >> 1][o][lane]) + 8 * (wave & 1), &np3[o], 8);
-#pragma unroll
-      for (int o = 0; o < kOut; ++o) __builtin_memcpy(reinterpret_cast<char*>(&out[wave >> 1][o][lane]) + 8 * (wave & 1), &npo[o], 8);
-    }
-    load_u(next);
-    load_rows(next);
     __syncthreads();
+    f32x4 sums[2][1];
+    sums[0][0] = sums[1][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 2 * kW; ++t) st[t] *= fade;
+    for (int n = 0; n < kSteps; ++n) {
+      Parts<kOut> sp;
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) __builtin_memcpy(sp.w[o], &state[n][o][lane], 16);
+      mma_parts<kOut>(qf[n], sp, sums[n & 1]);
+    }
+    f32x4 yy = (sums[0][0] + sums[1][0]) * fq;
+    if (kDirect) queries.to(b + 1, blocks, q_rows, a.q_stride, sq.len, 8 * q, query_row);
+    load_queries(group, head);
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      bf16x8 np3[3];
+      if (n > strip >> 1) break;
+      const f32x4 n0 = news[2 * n][lane], n1 = news[2 * n + 1][lane];
+      Parts<kOut> np;
+      np.set(0, n0[0], n0[1]);
+      np.set(1, n0[2], n0[3]);
+      np.set(2, n1[0], n1[1]);
+      np.set(3, n1[2], n1[3]);
 #pragma unroll
-      for (int o = 0; o < 3; ++o) np3[o] = wide[n][o][lane];
+      for (int r = kOut - 1; r >= 0; --r)
 #pragma unroll
-      for (int t = 0; t < 2 * kW; ++t) st[t] = mma_parts<kRaw, 3, 3>(kt[t][n], np3, st[t]);
+        for (int o = 0; o <= r; ++o) yy = mma_bf16(p[n][o], np.part(r - o), yy);
     }
-    load_kt(next);
-    load_fade(next);
+    load_p(head);
+    const int left = sq.len - b * kScanBlock;
+    if (left >= kScanBlock) {
+      if (mine) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      if (n > wave >> 1) break;
-      bf16x8 npo[kOut];
-#pragma unroll
-      for (int o = 0; o < kOut; ++o) npo[o] = out[n][o][lane];
-      yy = mma_parts<kOut, kOut, kOut>(p[n], npo, yy);
-    }
-    load_p(next);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t t = static_cast<int64_t>(b) * kScanBlock + 16 * wave + 4 * q + r;
-      if (mine && t < sq.len) y[t * s.y_stride] = from_float<T>(yy[r]);
-    }
-  }
-
-  if (slot < 0) return;
-#pragma unroll
-  for (int t = 0; t < 2 * kW; ++t) {
-    const int have = mine ? have0 - 16 * t : 0;
-    if (have <= 0) continue;
-    float* const to = s.ssm_out + place + 16 * t;
-    if (vec) {
-      *reinterpret_cast<f32x4*>(to) = st[t];
+        for (int r = 0; r < 4; ++r) y_row[r * s.y_stride] = from_float<T>(yy[r]);
+      }
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (r < have) to[r] = st[t][r];
+        if (mine && 16 * strip + 4 * q + r < left) y_row[r * s.y_stride] = from_float<T>(yy[r]);
     }
+    y_row += s.y_stride * kScanBlock;
   }
 }
 
