@@ -48,14 +48,17 @@ def check(y, want, part, dtype, kd, what):
     assert (err <= tol).all(), f"{what}: error {float((err / tol).max()):.2f} of what it may be"
 
 
+LONG = [700, 0, 1, 129, 350, 64, 15, 16, 17]  # more than 128 tokens a sequence on average: no mixed launches
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("heads, groups, kd, vd", SHAPES)
-def test_ragged_prompts(heads, groups, kd, vd, dtype):
+@pytest.mark.parametrize("heads, groups, kd, vd, lengths", [(*s, LENGTHS) for s in SHAPES] + [(4, 2, 100, 40, LONG), (2, 1, 128, 32, LONG)])
+def test_ragged_prompts(heads, groups, kd, vd, lengths, dtype):
     g = torch.Generator().manual_seed(heads * 1000 + kd)
-    n, seqs = sum(LENGTHS) + 4, len(LENGTHS)  # four rows behind the last sequence
+    n, seqs = sum(lengths) + 4, len(lengths)  # four rows behind the last sequence
     parts, decay, bias = inputs(g, n, heads, groups, kd, vd, dtype)
     offsets = [0]
-    for x in LENGTHS:
+    for x in lengths:
         offsets.append(offsets[-1] + x)
     bounds = list(zip(offsets, offsets[1:]))
     slots = torch.tensor([4, 0, 7, 2, -1, 9, 1, 3, 10], dtype=torch.int32)  # of 11; one keeps nothing
@@ -85,7 +88,8 @@ def test_ragged_prompts(heads, groups, kd, vd, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("seqs, each, heads, groups, kd, vd", [(1, 1, 2, 1, 128, 128), (37, 10, 4, 2, 64, 64), (3, 129, 2, 2, 128, 64),
-                                                               (2, 500, 1, 1, 32, 16), (5, 16, 2, 1, 128, 32), (5, 17, 2, 1, 200, 32)])
+                                                               (2, 500, 1, 1, 32, 16), (5, 32, 2, 1, 128, 32), (5, 33, 2, 1, 128, 32), (5, 16, 2, 1, 200, 32),
+                                                               (5, 17, 2, 1, 200, 32)])
 def test_equal_prompts_without_a_state(seqs, each, heads, groups, kd, vd, dtype):
     g = torch.Generator().manual_seed(seqs * each)
     parts, decay, _ = inputs(g, seqs * each, heads, groups, kd, vd, dtype, wide=False)

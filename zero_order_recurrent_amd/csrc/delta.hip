@@ -84,7 +84,8 @@ DeltaArgs make_args(const cdrge_delta_config* c, const cdrge_delta_weights* w, c
 
 // How a prompt call is cut up and where its workspace's parts lie; by sizes alone.
 struct Plan {
-  bool tokens;  // k_delta_tokens
+  bool tokens, long_ones;  // k_delta_tokens, the kernels of blocks
+  int short_len;           // as in DeltaArgs
   int kn;       // key_dim as the kernels of blocks have it
   int max_blocks;
   bool direct;  // as in DeltaWork
@@ -92,8 +93,14 @@ struct Plan {
   size_t slots, counts, start, bounds, block_of, piece_of, groups, heads, total;
 };
 
-// Short sequences are taken token by token.
-constexpr int kShort = 16;
+// Sequences that are taken token by token. A block of 64 tokens costs the same however few it holds: 256 sequences of 32
+// heads of 128 x 128, bf16, take 29 us a token, and 1.35 ms by blocks (float32 29 us and 2.3 ms; 16 x 16 4 and 306); wider
+// keys 53 us and 1.0 ms (64 sequences of 32 heads of 256 x 256). One sequence is quicker by blocks from 24 tokens on.
+int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 ? 32 : 16; }
+
+// A ragged batch may hold both kinds, which the host does not see: below this many tokens a sequence on average either
+// path is launched and leaves the other's sequences alone.
+constexpr int kMixed = 128;
 
 template <class T>
 void block_bytes(int kn, size_t* keys, size_t* head) {
@@ -103,7 +110,11 @@ void block_bytes(int kn, size_t* keys, size_t* head) {
 
 Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bool equal) {
   Plan p{};
-  p.tokens = n_tokens <= int64_t(kShort) * n_seqs;
+  p.short_len = short_len(c);
+  const int64_t longest = equal ? n_tokens / n_seqs : n_tokens;
+  p.long_ones = longest > p.short_len;
+  p.tokens = !p.long_ones || (!equal && n_tokens <= int64_t(kMixed) * n_seqs);
+  if (!p.tokens) p.short_len = -1;
   p.kn = c->key_dim <= 128 ? 128 : 256;
   const int64_t blocks = equal ? int64_t(n_seqs) * scan_blocks_of(n_tokens / n_seqs) : n_tokens / kScanBlock + n_seqs;
   p.max_blocks = static_cast<int>(blocks);
@@ -121,7 +132,7 @@ Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bo
     p.block_of = region(sizeof(int2) * blocks);
     p.piece_of = region(sizeof(int2) * n_seqs);
   }
-  if (!p.tokens) {
+  if (p.long_ones) {
     size_t keys = 0, head = 0;
     if (c->dtype == CDRGE_F32)
       block_bytes<float>(p.kn, &keys, &head);
@@ -150,7 +161,7 @@ ScanWork make_work(const Plan& p, void* ws) {
   return w;
 }
 
-template <class T, int kLanes, int kRpt, bool kStep>
+template <class T, int kLanes, int kQuads, int kRpt, bool kStep>
 cdrge_status launch_tokens(DeltaArgs a, const ScanWork& w, hipStream_t s) {
   constexpr int kTile = 256 / kLanes * kRpt;
   a.s.ptiles = (a.s.P + kTile - 1) / kTile;
@@ -164,18 +175,25 @@ cdrge_status launch_tokens(DeltaArgs a, const ScanWork& w, hipStream_t s) {
       hipLaunchKernelGGL(k_scan_owners, dim3((a.s.n_seqs + 63) / 64), dim3(64 * kScanOwnerWaves), 0, s, a.s, w.slots);
     CDRGE_HIP(hipGetLastError());
   }
-  hipLaunchKernelGGL((k_delta_tokens<T, kLanes, kRpt, kStep>), grid_of(n, 256), dim3(256), 0, s, a, w);
+  hipLaunchKernelGGL((k_delta_tokens<T, kLanes, kQuads, kRpt, kStep>), grid_of(n, 256), dim3(256), 0, s, a, w);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
 
+// Few rows take small tiles, as the scan's steps do.
+template <class T, int kQuads, bool kStep>
+cdrge_status launch_tiles(const DeltaArgs& a, const ScanWork& w, hipStream_t s) {
+  if (int64_t(a.s.n_seqs) * a.s.H * ((a.s.P + 15) / 16) <= 1024) return launch_tokens<T, 16, kQuads, 1, kStep>(a, w, s);
+  return launch_tokens<T, 16, kQuads, 4, kStep>(a, w, s);
+}
+
 template <class T, bool kStep>
 cdrge_status enqueue_tokens(const DeltaArgs& a, const ScanWork& w, hipStream_t s) {
-  if (a.s.N <= 16) return launch_tokens<T, 4, 1, kStep>(a, w, s);
-  if (a.s.N <= 32) return launch_tokens<T, 8, 2, kStep>(a, w, s);
-  if (a.s.N <= 64) return launch_tokens<T, 16, 4, kStep>(a, w, s);
-  if (a.s.N <= 128) return launch_tokens<T, 32, 8, kStep>(a, w, s);
-  return launch_tokens<T, 64, 8, kStep>(a, w, s);
+  if (a.s.N <= 16) return launch_tokens<T, 4, 1, 1, kStep>(a, w, s);
+  if (a.s.N <= 32) return launch_tokens<T, 8, 1, 2, kStep>(a, w, s);
+  if (a.s.N <= 64) return launch_tiles<T, 1, kStep>(a, w, s);
+  if (a.s.N <= 128) return launch_tiles<T, 2, kStep>(a, w, s);
+  return launch_tiles<T, 4, kStep>(a, w, s);
 }
 
 template <class T, int kN>
@@ -210,13 +228,17 @@ cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, h
 }
 
 template <class T>
-cdrge_status enqueue_prompt(const DeltaArgs& a, const Plan& p, void* ws, hipStream_t s) {
+cdrge_status enqueue_prompt(DeltaArgs a, const Plan& p, void* ws, hipStream_t s) {
+  a.short_len = p.short_len;
   const ScanWork w = make_work(p, ws);
   if (a.s.offsets) {
     hipLaunchKernelGGL(k_scan_map, dim3(1), dim3(1024), 0, s, a.s, w);
     CDRGE_HIP(hipGetLastError());
   }
-  if (p.tokens) return enqueue_tokens<T, false>(a, w, s);
+  if (p.tokens) {
+    const cdrge_status st = enqueue_tokens<T, false>(a, w, s);
+    if (st != CDRGE_OK || !p.long_ones) return st;
+  }
   const DeltaWork d{static_cast<char*>(ws) + p.groups, static_cast<char*>(ws) + p.heads, static_cast<int64_t>(p.group_bytes), p.direct};
   return p.kn == 128 ? launch_blocks<T, 128>(a, w, d, s) : launch_blocks<T, 256>(a, w, d, s);
 }

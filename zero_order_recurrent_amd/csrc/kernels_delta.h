@@ -22,29 +22,47 @@ struct DeltaArgs {
   const void* beta;
   int64_t beta_stride;
   float q_scale, norm_eps;
+  int short_len;  // prompts: k_delta_tokens takes sequences of up to so many tokens, the kernels of blocks longer ones
 };
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
 // What brings a row of the sum of squares ss to length one; a sum past float32 makes the row NaN.
 __device__ __forceinline__ float delta_norm(float ss, float eps) {
-  return ss < __builtin_inff() ? 1.f / sqrtf(ss + eps) : __builtin_nanf("");
+  return ss < __builtin_inff() ? __builtin_amdgcn_rsqf(ss + eps) : __builtin_nanf("");  // off by 2^-23 at most
 }
 
+// Sum over kLanes (4, 8 or 16) lanes side by side, in each of them.
+template <int kControl>
+__device__ __forceinline__ float add_lane(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kControl, 0xf, 0xf, true));
+}
 template <int kLanes>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int m = kLanes / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  v = add_lane<0xb1>(v);                   // lane ^ 1
+  v = add_lane<0x4e>(v);                   // lane ^ 2
+  if (kLanes > 4) v = add_lane<0x141>(v);  // half-row mirror
+  if (kLanes > 8) v = add_lane<0x140>(v);  // row mirror
   return v;
 }
 
-// Token after token, with the state in registers: kLanes lanes side by side hold four of its columns each, a thread
-// kRpt of its rows. One token for each sequence (kStep) is bound by memory, which the state crosses twice.
+// What a thread reads of a token: four entries each of q and k from column 4 (its lane + kLanes n) on, kRpt of v.
+template <class T, int kQuads, int kRpt>
+struct DeltaToken {
+  Four<T> q[kQuads], k[kQuads];
+  T v[kRpt];
+};
+
+// Token after token, with the state in registers: kLanes lanes side by side hold 4 kQuads of its columns each, a thread
+// kRpt of its rows. One token for each sequence (kStep) is bound by memory, which the state crosses twice; all that is
+// read is requested together, the check for a repeated slot beside it. In prompts a token is requested while the one
+// before it is worked on, and 64 tokens' gates are formed at a time, a token a thread.
 // With S the state before a token, its prediction of v is a S k' and y = a S q' + (k'.q') b (v - a S k'), so that both
-// products of S run before its update.
-template <class T, int kLanes, int kRpt, bool kStep>
+// products of S run before its update, and, as the norms are factors, beside theirs.
+template <class T, int kLanes, int kQuads, int kRpt, bool kStep>
 __global__ __launch_bounds__(256) void k_delta_tokens(DeltaArgs a, ScanWork w) {
   constexpr int kTile = 256 / kLanes * kRpt;
+  __shared__ float2 gates[64];
   const ScanArgs& s = a.s;
   const int tid = threadIdx.x;
   const uint32_t id = static_cast<uint32_t>(block_number());
@@ -64,11 +82,11 @@ __global__ __launch_bounds__(256) void k_delta_tokens(DeltaArgs a, ScanWork w) {
       taken = !(to_float(y[i * s.y_stride]) == 0.f);
     else if (s.slots)
       for (int j = tid; j < i; j += 256) taken |= s.slots[j] == slot;
-    taken = __syncthreads_or(taken);
   } else {
     const ScanSeq sq = scan_seq(s, w, i);
     first = sq.first;
     len = sq.len;
+    if (len > a.short_len) return;
     if (s.ssm_in) {
       slot = s.owned ? w.slots[i] : scan_slot(s, i);
       taken = slot == -2;
@@ -76,101 +94,128 @@ __global__ __launch_bounds__(256) void k_delta_tokens(DeltaArgs a, ScanWork w) {
     }
   }
   y += first * s.y_stride;
-  if (taken) {
-    for (int t = 0; t < len; ++t)
-      if (tid < np) y[t * s.y_stride + tid] = from_float<T>(__builtin_nanf(""));
-    return;
-  }
   const int N = s.N, g = h / (s.H / s.G);
   const int ln = tid % kLanes, n0 = ln * 4, have = N - n0, r0 = tid / kLanes * kRpt;
-  const bool vec = N % 4 == 0;
-  const int64_t sbase = (static_cast<int64_t>(max(slot, 0)) * s.H + h) * s.P + p0;
-  float st[kRpt][4];
+  const bool vec = N % 4 == 0, held = slot >= 0 && !(kStep && slot >= s.n_slots);
+  const int64_t sbase = (static_cast<int64_t>(held ? slot : 0) * s.H + h) * s.P + p0;
+  f32x4 st[kRpt][kQuads];
 #pragma unroll
-  for (int r = 0; r < kRpt; ++r) {
+  for (int r = 0; r < kRpt; ++r)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) st[r][e] = 0.f;
-    if (slot >= 0 && pos > 0 && r0 + r < np && have > 0) {
-      const float* const from = s.ssm_in + (sbase + r0 + r) * N + n0;
-      if (vec) {
-        const f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(from));
+    for (int n = 0; n < kQuads; ++n) {
+      st[r][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int left = have - 4 * kLanes * n;
+      if (held && pos > 0 && r0 + r < np && left > 0) {
+        const float* const from = s.ssm_in + (sbase + r0 + r) * N + n0 + 4 * kLanes * n;
+        if (vec) {
+          st[r][n] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(from));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st[r][e] = x[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < have) st[r][e] = from[e];
+          for (int e = 0; e < 4; ++e)
+            if (e < left) st[r][n][e] = from[e];
+        }
       }
     }
-  }
   const T* const qp = static_cast<const T*>(a.q) + first * a.q_stride + static_cast<int64_t>(g) * N + n0;
   const T* const kp = static_cast<const T*>(a.k) + first * a.k_stride + static_cast<int64_t>(g) * N + n0;
   const T* const vp = static_cast<const T*>(a.v) + first * a.v_stride + static_cast<int64_t>(h) * s.P + p0 + r0;
   const T* const dp = static_cast<const T*>(s.dt) + first * s.dt_stride + h;
   const T* const bp = static_cast<const T*>(a.beta) + first * a.beta_stride + h;
   const float bias = s.dt_bias ? s.dt_bias[h] : 0.f, decay = s.decay[h];
+  auto load = [&](int64_t t) {
+    DeltaToken<T, kQuads, kRpt> x;
+#pragma unroll
+    for (int n = 0; n < kQuads; ++n) {
+      x.q[n].load(qp + t * a.q_stride + 4 * kLanes * n, have - 4 * kLanes * n);
+      x.k[n].load(kp + t * a.k_stride + 4 * kLanes * n, have - 4 * kLanes * n);
+    }
+#pragma unroll
+    for (int r = 0; r < kRpt; ++r) x.v[r] = r0 + r < np ? vp[t * a.v_stride + r] : T(0);
+    return x;
+  };
+  auto gate = [&](int64_t t) {  // the state's fade and the strength
+    return make_float2(expf(softplus(to_float(dp[t * s.dt_stride]) + bias) * decay), sigmoid(to_float(bp[t * a.beta_stride])));
+  };
+  DeltaToken<T, kQuads, kRpt> next;
+  if (len > 0) next = load(0);
+  float2 only;
+  if (kStep) {
+    only = gate(0);
+    taken = __syncthreads_or(taken);
+  }
+  if (taken) {
+    for (int64_t t = 0; t < len; ++t)
+      if (tid < np) y[t * s.y_stride + tid] = from_float<T>(__builtin_nanf(""));
+    return;
+  }
   for (int t = 0; t < len; ++t) {
-    Four<T> qv, kv;
-    qv.load(qp + t * a.q_stride, have);
-    kv.load(kp + t * a.k_stride, have);
-    float v[kRpt];
-#pragma unroll
-    for (int r = 0; r < kRpt; ++r) v[r] = r0 + r < np ? to_float(vp[t * a.v_stride + r]) : 0.f;
-    const float step = softplus(to_float(dp[t * s.dt_stride]) + bias), b = sigmoid(to_float(bp[t * a.beta_stride]));
-    const float fade = expf(step * decay);
-    float q[4], k[4], qq = 0.f, kk = 0.f, kq = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      q[e] = qv.at(e);
-      k[e] = kv.at(e);
-      qq += q[e] * q[e];
-      kk += k[e] * k[e];
+    const DeltaToken<T, kQuads, kRpt> x = next;
+    if (!kStep) {
+      if (t + 1 < len) next = load(t + 1);
+      if (t % 64 == 0) {
+        __syncthreads();
+        if (tid < min(64, len - t)) gates[tid] = gate(t + tid);
+        __syncthreads();
+      }
     }
-    const float rq = a.q_scale * delta_norm(lanes_sum<kLanes>(qq), a.norm_eps), rk = delta_norm(lanes_sum<kLanes>(kk), a.norm_eps);
+    const float2 now = kStep ? only : gates[t % 64];
+    float qq = 0.f, kk = 0.f, kq = 0.f, sk[kRpt], sq[kRpt];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      q[e] *= rq;
-      k[e] *= rk;
-      kq += k[e] * q[e];
-    }
+    for (int n = 0; n < kQuads; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float q = x.q[n].at(e), k = x.k[n].at(e);
+        qq += q * q;
+        kk += k * k;
+        kq += k * q;
+      }
+    qq = lanes_sum<kLanes>(qq);
+    kk = lanes_sum<kLanes>(kk);
     kq = lanes_sum<kLanes>(kq);
+#pragma unroll
+    for (int r = 0; r < kRpt; ++r) {
+      sk[r] = sq[r] = 0.f;
+#pragma unroll
+      for (int n = 0; n < kQuads; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          st[r][n][e] *= now.x;
+          sk[r] += st[r][n][e] * x.k[n].at(e);
+          sq[r] += st[r][n][e] * x.q[n].at(e);
+        }
+      sk[r] = lanes_sum<kLanes>(sk[r]);
+      sq[r] = lanes_sum<kLanes>(sq[r]);
+    }
+    const float rq = a.q_scale * delta_norm(qq, a.norm_eps), rk = delta_norm(kk, a.norm_eps);
     float mine = 0.f;
 #pragma unroll
     for (int r = 0; r < kRpt; ++r) {
-      float sk = 0.f, sq = 0.f;
+      const float add = now.y * (to_float(x.v[r]) - sk[r] * rk) * rk;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        st[r][e] *= fade;
-        sk += st[r][e] * k[e];
-        sq += st[r][e] * q[e];
-      }
-      sk = lanes_sum<kLanes>(sk);
-      sq = lanes_sum<kLanes>(sq);
-      const float add = b * (v[r] - sk);
+      for (int n = 0; n < kQuads; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st[r][e] += add * k[e];
-      const float out = sq + add * kq;
-      if (kRpt <= kLanes) {
-        if (ln == r) mine = out;
-      } else if (ln == 0 && r0 + r < np) {
-        y[t * s.y_stride + r0 + r] = from_float<T>(out);
-      }
+        for (int e = 0; e < 4; ++e) st[r][n][e] += add * x.k[n].at(e);
+      const float out = (sq[r] + add * kq) * rq;
+      if (ln == r) mine = out;
     }
-    if (kRpt <= kLanes && ln < kRpt && r0 + ln < np) y[t * s.y_stride + r0 + ln] = from_float<T>(mine);
+    if (ln < kRpt && r0 + ln < np) y[t * s.y_stride + r0 + ln] = from_float<T>(mine);
   }
   if (slot < 0) return;
 #pragma unroll
-  for (int r = 0; r < kRpt; ++r) {
-    if (r0 + r >= np || have <= 0) continue;
-    float* const to = s.ssm_out + (sbase + r0 + r) * N + n0;
-    if (vec) {
-      __builtin_nontemporal_store(f32x4{st[r][0], st[r][1], st[r][2], st[r][3]}, reinterpret_cast<f32x4*>(to));
-    } else {
+  for (int r = 0; r < kRpt; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < have) to[e] = st[r][e];
+    for (int n = 0; n < kQuads; ++n) {
+      const int left = have - 4 * kLanes * n;
+      if (r0 + r >= np || left <= 0) continue;
+      float* const to = s.ssm_out + (sbase + r0 + r) * N + n0 + 4 * kLanes * n;
+      if (vec) {
+        __builtin_nontemporal_store(st[r][n], reinterpret_cast<f32x4*>(to));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) to[e] = st[r][n][e];
+      }
     }
-  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -301,7 +346,7 @@ __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, D
   const ScanSeq sq = scan_seq(s, w, at.x);
   const int64_t row0 = sq.first + static_cast<int64_t>(at.y) * kScanBlock;
   const int L = min(kScanBlock, sq.len - at.y * kScanBlock);
-  if (L <= 0) return;  // a sequence without rows
+  if (sq.len <= max(a.short_len, 0)) return;
   char* const group = d.groups + (static_cast<int64_t>(block) * s.G + g) * d.group_bytes;
   char* const head = d.heads + (static_cast<int64_t>(block) * s.H + h) * Block::kHeadBytes;
   const bool first = h % rep == 0;
@@ -543,6 +588,7 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
   const int tile = id % s.ptiles, h = id / s.ptiles % s.H, i = id / (s.ptiles * s.H);
   if (i >= s.n_seqs) return;
   const ScanSeq sq = scan_seq(s, w, i);
+  if (sq.len <= a.short_len) return;
   const int p0 = 16 * tile, np = min(16, s.P - p0), g = h / (s.H / s.G), N = s.N;
   const bool mine = l16 < np;
   T* const y = static_cast<T*>(s.y) + sq.first * s.y_stride + static_cast<int64_t>(h) * s.P + p0;
