@@ -225,3 +225,15 @@ def test_classes_refuse():
         layer.project(x[:, :64], torch.zeros(4, 4, device="cuda"))
     assert layer.project(x[:0], torch.zeros(0, 4, device="cuda")).shape == (0, 4)
     assert u8 is codes.dtype
+
+
+@pytest.mark.parametrize("rows, K, O", [(1100, 300, 4100), (2049, 2112, 2050), (4097, 64, 1000)])
+def test_project_large_tiles(rows, K, O):
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn(rows, K, generator=g).bfloat16()
+    codes, scales = weights(g, O, K)
+    bias = torch.randn(O, generator=g).bfloat16()
+    y = project(x, codes, scales, bias, O, "bf16", stride=1)
+    want, size = want_of(x, codes, scales, bias)
+    err, tol = (y.double().cpu() - want).abs(), tol_of(want, size, "bf16", K)
+    assert (err <= tol).all(), float((err / tol).max())

@@ -1,6 +1,8 @@
 // Microscaled 4-bit floating point: quantisation, the values back, and the product of quantised rows with quantised
 // weights (E2M1 elements, a power of two for each 32 of them along the reduction).
 #pragma once
+#include <type_traits>
+
 #include "operators_common.h"
 
 namespace cdrge {
@@ -69,9 +71,24 @@ __device__ __forceinline__ MxPlace mx_place(int quarters, int parts) {
   return {r < each ? id * each + r : (int64_t(1) << 62), static_cast<int>(threadIdx.x) % quarters};
 }
 
-template <class T>
+// kTiled: rows of whole steps of 8 blocks (zeros past K) and scales by step, as k_mx_tiles reads them; the workgroups past
+// the rows' lay out the weights' scales in the same way, the last block's in the place of those past it (which meet zeros).
+template <class T, bool kTiled>
 __global__ __launch_bounds__(256) void k_mx_quantize(const T* __restrict__ x, int64_t stride, int64_t n_rows, int K, int quarters,
-                                                     int parts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                                                     int parts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                     int64_t groups, const uint8_t* __restrict__ w_scales, int O, int blocks,
+                                                     uint8_t* __restrict__ w_tiled) {
+  if (kTiled && block_number() >= groups) {
+    const int64_t id = (block_number() - groups) * 256 + threadIdx.x;
+    const int o = static_cast<int>(id % O), step = static_cast<int>(id / O);
+    if (8 * step >= blocks) return;
+    const uint8_t* const from = w_scales + static_cast<int64_t>(o) * blocks;
+    uint8_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = from[min(8 * step + i, blocks - 1)];
+    __builtin_memcpy(w_tiled + id * 8, v, 8);
+    return;
+  }
   const MxPlace at = mx_place(quarters, parts);
   if (at.row >= n_rows || at.quarter >= quarters) return;  // whole blocks
   float v[8];
@@ -81,7 +98,8 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const T* __restrict__ x, in
   for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
   const int e = mx_scale(quad_most(most));
   reinterpret_cast<uint32_t*>(codes)[at.row * quarters + at.quarter] = mx_codes(v, e);
-  if (at.quarter % 4 == 0) scales[(at.row * quarters + at.quarter) / 4] = static_cast<uint8_t>(e);
+  const int b = at.quarter / 4;
+  if (at.quarter % 4 == 0) scales[kTiled ? ((b / 8) * n_rows + at.row) * 8 + b % 8 : at.row * (quarters / 4) + b] = static_cast<uint8_t>(e);
 }
 
 // The value of a code with the scale byte e.
@@ -166,6 +184,163 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a, int o_tiles) {
   for (int e = 0; e < 4; ++e) {
     const int o = o0 + 4 * q + e;
     if (o < a.O) y[o] = from_float<T>(sum[e] + (a.bias ? to_float(static_cast<const T*>(a.bias)[o]) : 0.f));
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Many rows: tiles of kSide x kSide outputs, a wave 64 outputs by kSide / 2 rows of them, in products of 32 x 32 x 64. A
+// step is 256 values (128 bytes) of each row, in two buffers of LDS that are loaded without passing through registers, the
+// next step's while this one's products run. Rows lie there as eight chunks of 16 bytes, chunk c of row i at place c ^ f(i)
+// (see place_w and place_x), so that the eight rows that a read touches at a time take all eight.
+// The order along the reduction is free: lane group h of a wave takes the step's blocks 4 h .. 4 h + 3, whose scales are
+// one word. So is that of a tile's outputs: a lane holds 32 adjacent ones of a row, which leave it in whole pieces.
+// ---------------------------------------------------------------------------------------------
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+
+struct MxTileArgs {
+  const uint8_t* w_codes;  // [O][blocks][16]
+  const uint8_t* w_scales;  // [step][O][8]
+  const uint8_t* x_codes;  // [row][steps][8][16]
+  const uint8_t* x_scales;  // [step][row][8]
+  const void* bias;
+  void* y;
+  int64_t y_stride;
+  int64_t n_rows;
+  int O, blocks, steps, tiles_r, tiles_o;
+};
+
+__device__ __forceinline__ int mx_place_x(int row) { return row & 7; }
+__device__ __forceinline__ int mx_place_w(int row) { return (row & 3) | ((row >> 3) & 4); }
+
+template <class T, int kSide>
+__global__ __launch_bounds__(kSide * 2, 2) void k_mx_tiles(MxTileArgs a) {
+  constexpr int kThreads = kSide * 2, kRT = kSide / 64;  // row tiles of a wave
+  constexpr int kLoads = kSide * 8 / kThreads;           // chunks of either operand that a thread loads a step
+  constexpr int kBuf = 2 * kSide * 8;
+  extern __shared__ uint4 stage[];  // [2][kBuf]: W's rows, then x's
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, half = lane >> 5;
+  const int wo = wave >> 1, wr = wave & 1;
+
+  // Workgroups go round the eight XCDs, each of which has its own L2: XCD i gets the i-th eighth of the tiles, walked in
+  // columns of up to four row tiles.
+  const int n_tiles = a.tiles_r * a.tiles_o;
+  uint32_t id = static_cast<uint32_t>(block_number());
+  if (id >= static_cast<uint32_t>(n_tiles)) return;
+  {
+    const uint32_t per = n_tiles >> 3, left = n_tiles & 7, xcd = id & 7;
+    id = xcd * per + min(xcd, left) + (id >> 3);
+  }
+  const int band = id / (4 * a.tiles_o), in_band = id % (4 * a.tiles_o);
+  const int band_rows = min(4, a.tiles_r - 4 * band);
+  const int64_t r0 = static_cast<int64_t>(4 * band + in_band % band_rows) * kSide;
+  const int o0 = in_band / band_rows * kSide;
+  const int last_r = static_cast<int>(a.n_rows - r0 < kSide ? a.n_rows - r0 : kSide) - 1, last_o = min(kSide, a.O - o0) - 1;
+
+  // load i of a thread: place tid % 8 of row tid / 8 + i kThreads / 8; rows past the last are read from it
+  const char* const wb = reinterpret_cast<const char*>(a.w_codes) + static_cast<int64_t>(o0) * a.blocks * 16;
+  const char* const xb = reinterpret_cast<const char*>(a.x_codes) + r0 * a.steps * 128;
+  auto fetch = [&](int step, int buf) {
+    uint4* const to = stage + buf * kBuf + (tid & ~63);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (tid >> 3) + i * (kThreads / 8), c = (tid & 7) ^ mx_place_w(row);
+      // W's blocks past the last meet zeros of x: the last one is read in their place
+      load_to_lds(wb, (min(row, last_o) * a.blocks + min(8 * step + c, a.blocks - 1)) * 16, to + i * kThreads);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (tid >> 3) + i * (kThreads / 8), c = (tid & 7) ^ mx_place_x(row);
+      load_to_lds(xb + step * 128, min(row, last_r) * a.steps * 128 + c * 16, to + kSide * 8 + i * kThreads);
+    }
+  };
+  // W's rows of a wave: row m of tile t is output 32 (m / 4 % 2) + 16 t + 4 (m / 8) + m % 4 of its 64
+  int w_row[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) w_row[t] = wo * 64 + 32 * (l32 >> 2 & 1) + 16 * t + 4 * (l32 >> 3) + (l32 & 3);
+  int ew[2], ex[kRT], ew_next[2], ex_next[kRT];
+  auto fetch_scales = [&](int step) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      ew_next[t] = *reinterpret_cast<const int*>(a.w_scales + (static_cast<int64_t>(step) * a.O + o0 + min(w_row[t], last_o)) * 8 + 4 * half);
+#pragma unroll
+    for (int t = 0; t < kRT; ++t)
+      ex_next[t] = *reinterpret_cast<const int*>(a.x_scales + (step * a.n_rows + r0 + min(wr * (kSide / 2) + 32 * t + l32, last_r)) * 8 + 4 * half);
+  };
+
+  f32x16 acc[2][kRT];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < kRT; ++r)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[t][r][e] = 0.f;
+
+  fetch(0, 0);
+  fetch_scales(0);
+  for (int step = 0; step < a.steps; ++step) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) ew[t] = ew_next[t];
+#pragma unroll
+    for (int t = 0; t < kRT; ++t) ex[t] = ex_next[t];
+    const uint4* const w = stage + (step & 1) * kBuf;
+    const uint4* const x = w + kSide * 8;
+    if (step + 1 < a.steps) {
+      fetch(step + 1, ~step & 1);
+      fetch_scales(step + 1);
+    }
+    auto products = [&](auto s_) {
+      constexpr int s = decltype(s_)::value;
+      i32x8 wf[2], xf[kRT];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint4 v = w[w_row[t] * 8 + ((4 * half + s) ^ mx_place_w(w_row[t]))];
+        wf[t] = i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int t = 0; t < kRT; ++t) {
+        const int row = wr * (kSide / 2) + 32 * t + l32;
+        const uint4 v = x[row * 8 + ((4 * half + s) ^ mx_place_x(row))];
+        xf[t] = i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int r = 0; r < kRT; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[t][r] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[t], xf[r], acc[t][r], 4, 4, s, ew[t], s, ex[r]);
+    };
+    products(std::integral_constant<int, 0>{});
+    products(std::integral_constant<int, 1>{});
+    products(std::integral_constant<int, 2>{});
+    products(std::integral_constant<int, 3>{});
+  }
+
+  const int o = o0 + wo * 64 + 32 * half;  // this lane's 32 outputs
+  if (o >= a.O) return;
+  const bool whole = o + 32 <= a.O;
+#pragma unroll
+  for (int r = 0; r < kRT; ++r) {
+    const int row = wr * (kSide / 2) + 32 * r + l32;
+    if (row > last_r) continue;
+    T* const y = static_cast<T*>(a.y) + (r0 + row) * a.y_stride + o;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      T v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float sum = acc[t][r][e];
+        if (a.bias && o + 16 * t + e < a.O) sum += to_float(static_cast<const T*>(a.bias)[o + 16 * t + e]);
+        v[e] = from_float<T>(sum);
+      }
+      if (whole) {
+        __builtin_memcpy(y + 16 * t, v, sizeof(v));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (o + 16 * t + e < a.O) y[16 * t + e] = v[e];
+      }
+    }
   }
 }
 

@@ -1,6 +1,8 @@
 // Host side of cdrge_mx_quantize, cdrge_mx_dequantize and cdrge_mx_project (include/cdrge.h).
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "cdrge.h"
 #include "host_common.h"
 #include "kernels_mx.h"
@@ -40,37 +42,91 @@ int64_t quarter_groups(int64_t n_rows, int quarters, int* parts) {
 
 constexpr int64_t kMostGroups = int64_t(1) << 35;  // 2^20 by 2^15 of a grid
 
+// tiled: for k_mx_tiles, with the weights' scales (w_scales to w_tiled) in the same launch
+template <class T>
 cdrge_status quantize(const cdrge_mx_config* c, int64_t n_rows, const void* x, int64_t stride, uint8_t* codes,
-                      uint8_t* scales, hipStream_t s) {
+                      uint8_t* scales, bool tiled, const uint8_t* w_scales, uint8_t* w_tiled, hipStream_t s) {
   int parts = 1;
-  const int quarters = 4 * blocks_of(c);
+  const int blocks = blocks_of(c), steps = (blocks + 7) / 8, quarters = 4 * (tiled ? 8 * steps : blocks);
   const int64_t n = quarter_groups(n_rows, quarters, &parts);
-  if (n > kMostGroups) return CDRGE_ERR_UNSUPPORTED;
+  const int64_t more = tiled ? (int64_t(c->out_features) * steps + 255) / 256 : 0;
+  if (n + more > kMostGroups) return CDRGE_ERR_UNSUPPORTED;
   if (n == 0) return CDRGE_OK;
-  if (c->dtype == CDRGE_F32)
-    hipLaunchKernelGGL(k_mx_quantize<float>, grid_of(n, 256), dim3(256), 0, s, static_cast<const float*>(x), stride, n_rows,
-                       c->in_features, quarters, parts, codes, scales);
+  const T* const from = static_cast<const T*>(x);
+  if (tiled)
+    hipLaunchKernelGGL((k_mx_quantize<T, true>), grid_of(n + more, 256), dim3(256), 0, s, from, stride, n_rows, c->in_features,
+                       quarters, parts, codes, scales, n, w_scales, c->out_features, blocks, w_tiled);
   else
-    hipLaunchKernelGGL(k_mx_quantize<uint16_t>, grid_of(n, 256), dim3(256), 0, s, static_cast<const uint16_t*>(x), stride,
-                       n_rows, c->in_features, quarters, parts, codes, scales);
+    hipLaunchKernelGGL((k_mx_quantize<T, false>), grid_of(n, 256), dim3(256), 0, s, from, stride, n_rows, c->in_features,
+                       quarters, parts, codes, scales, n, w_scales, c->out_features, blocks, w_tiled);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
 
+// How a call is cut up and where its workspace's parts lie; by sizes alone.
 struct Plan {
-  size_t codes, scales, total;
+  int side;  // of the tiles of k_mx_tiles; 0: k_mx_rows
+  int blocks, steps, tiles_r, tiles_o;
+  size_t codes, scales, w_scales, total;
 };
 
 Plan make_plan(const cdrge_mx_config* c, int64_t n_rows) {
   Plan p{};
-  const size_t blocks = static_cast<size_t>(n_rows) * blocks_of(c);
-  p.scales = align_up(16 * blocks);
-  p.total = align_up(p.scales + blocks);
+  p.blocks = blocks_of(c);
+  p.steps = (p.blocks + 7) / 8;
+  const int64_t r128 = (n_rows + 127) / 128, o128 = (c->out_features + 127) / 128;
+  if (n_rows > 64) p.side = r128 * o128 >= 1024 ? 256 : 128;
+  if (p.side > 0) {
+    p.tiles_r = static_cast<int>((n_rows + p.side - 1) / p.side);
+    p.tiles_o = (c->out_features + p.side - 1) / p.side;
+  }
+  const size_t row_blocks = p.side > 0 ? 8 * p.steps : p.blocks;
+  p.scales = align_up(16 * row_blocks * n_rows);
+  p.w_scales = align_up(p.scales + row_blocks * n_rows);
+  p.total = p.side > 0 ? align_up(p.w_scales + size_t(8) * p.steps * c->out_features) : p.w_scales;
   return p;
 }
 
 int64_t project_groups(const cdrge_mx_config* c, int64_t n_rows) {
   return (n_rows + 63) / 64 * ((c->out_features + 15) / 16);
+}
+
+// Whether the call's sizes fit the kernels' counts.
+bool fits(const cdrge_mx_config* c, int64_t n_rows) {
+  return (n_rows + 127) / 128 * ((c->out_features + 127) / 128) < (int64_t(1) << 31);
+}
+
+template <class T, int kSide>
+cdrge_status launch_tiles(const MxTileArgs& a, hipStream_t s) {
+  constexpr size_t kLds = size_t(2) * 2 * kSide * 128;
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use this much LDS
+  int dev = 0;
+  CDRGE_HIP(hipGetDevice(&dev));
+  if (!(ready.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
+    CDRGE_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx_tiles<T, kSide>), hipFuncAttributeMaxDynamicSharedMemorySize, kLds));
+    ready.fetch_or(uint64_t(1) << (dev & 63), std::memory_order_relaxed);
+  }
+  hipLaunchKernelGGL((k_mx_tiles<T, kSide>), grid_of(int64_t(a.tiles_r) * a.tiles_o, 2 * kSide), dim3(2 * kSide), kLds, s, a);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
+}
+
+template <class T>
+cdrge_status project(const cdrge_mx_config* c, const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, int64_t n_rows,
+                     const void* x, int64_t x_stride, void* y, int64_t y_stride, const Plan& p, void* workspace, hipStream_t s) {
+  uint8_t* const codes = static_cast<uint8_t*>(workspace) + p.codes;
+  uint8_t* const scales = static_cast<uint8_t*>(workspace) + p.scales;
+  uint8_t* const w_tiled = static_cast<uint8_t*>(workspace) + p.w_scales;
+  const cdrge_status st = quantize<T>(c, n_rows, x, x_stride, codes, scales, p.side > 0, w_scales, w_tiled, s);
+  if (st != CDRGE_OK) return st;
+  if (p.side > 0) {
+    const MxTileArgs a{w_codes, w_tiled, codes, scales, bias, y, y_stride, n_rows, c->out_features, p.blocks, p.steps, p.tiles_r, p.tiles_o};
+    return p.side == 256 ? launch_tiles<T, 256>(a, s) : launch_tiles<T, 128>(a, s);
+  }
+  const MxArgs a{w_codes, w_scales, bias, codes, scales, y, y_stride, n_rows, c->out_features, p.blocks};
+  hipLaunchKernelGGL(k_mx_rows<T>, grid_of(project_groups(c, n_rows), 512), dim3(512), 0, s, a, (a.O + 15) / 16);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
 }
 
 }  // namespace
@@ -81,7 +137,9 @@ cdrge_status cdrge_mx_quantize(const cdrge_mx_config* cfg, int64_t n_rows, const
                                uint8_t* codes, uint8_t* scales, void* stream) {
   const cdrge_status st = check_rows(cfg, n_rows, x, x_stride, codes, scales);
   if (st != CDRGE_OK) return st;
-  return quantize(cfg, n_rows, x, x_stride, codes, scales, static_cast<hipStream_t>(stream));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return cfg->dtype == CDRGE_F32 ? quantize<float>(cfg, n_rows, x, x_stride, codes, scales, false, nullptr, nullptr, s)
+                                 : quantize<uint16_t>(cfg, n_rows, x, x_stride, codes, scales, false, nullptr, nullptr, s);
 }
 
 cdrge_status cdrge_mx_dequantize(const cdrge_mx_config* cfg, int64_t n_rows, const uint8_t* codes,
@@ -108,7 +166,7 @@ cdrge_status cdrge_mx_workspace_bytes(const cdrge_mx_config* cfg, int64_t n_rows
   if (!bytes_out) return CDRGE_ERR_INVALID_ARG;
   const cdrge_status st = check(cfg, n_rows);
   if (st != CDRGE_OK) return st;
-  if (project_groups(cfg, n_rows) > kMostGroups) return CDRGE_ERR_UNSUPPORTED;
+  if (!fits(cfg, n_rows)) return CDRGE_ERR_UNSUPPORTED;
   *bytes_out = make_plan(cfg, n_rows).total;
   return CDRGE_OK;
 }
@@ -127,19 +185,9 @@ cdrge_status cdrge_mx_project(const cdrge_mx_config* cfg, const uint8_t* w_codes
     return workspace_error("cdrge_mx_project", need, workspace ? workspace_bytes : 0);
   const Plan p = make_plan(cfg, n_rows);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  uint8_t* const codes = static_cast<uint8_t*>(workspace) + p.codes;
-  uint8_t* const scales = static_cast<uint8_t*>(workspace) + p.scales;
-  st = quantize(cfg, n_rows, x, x_stride, codes, scales, s);
-  if (st != CDRGE_OK) return st;
-  const MxArgs a{w_codes, w_scales, bias, codes, scales, y, y_stride, n_rows, cfg->out_features, blocks_of(cfg)};
-  const int o_tiles = (a.O + 15) / 16;
-  const dim3 grid = grid_of(project_groups(cfg, n_rows), 512);
-  if (cfg->dtype == CDRGE_F32)
-    hipLaunchKernelGGL(k_mx_rows<float>, grid, dim3(512), 0, s, a, o_tiles);
-  else
-    hipLaunchKernelGGL(k_mx_rows<uint16_t>, grid, dim3(512), 0, s, a, o_tiles);
-  CDRGE_HIP(hipGetLastError());
-  return CDRGE_OK;
+  return cfg->dtype == CDRGE_F32
+             ? project<float>(cfg, w_codes, w_scales, bias, n_rows, x, x_stride, y, y_stride, p, workspace, s)
+             : project<uint16_t>(cfg, w_codes, w_scales, bias, n_rows, x, x_stride, y, y_stride, p, workspace, s);
 }
 
 }  // extern "C"

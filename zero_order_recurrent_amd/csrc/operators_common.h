@@ -65,6 +65,23 @@ inline dim3 grid_of(int64_t blocks, int threads) {
 }
 __device__ __forceinline__ int64_t block_number() { return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; }
 
+// s_waitcnt operand: no vector memory load in flight (vmcnt 0), the other counters not waited for
+constexpr int kWaitLoads = 0x0f70;
+
+// 16 bytes a lane from base + offset into LDS, lane by lane behind `to` (base and to are the same for
+// the whole wave). The load has no register result. It is written as an instruction because the
+// compiler, which cannot tell the two buffers apart, would wait for every load of this kind before any
+// read of LDS; the wait that is needed stands before the step's barrier.
+// m0 is written, and named so that no other use of it is moved across; clang warns that it never allocates m0 itself.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, uint4* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)to)));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(at) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // Sum and maximum over a wave, in every lane. Within a row of 16 lanes the partner is reached by a lane
 // permutation of the vector unit (quads, then mirrored halves and rows), across rows by a swap.
 template <int kControl>
