@@ -100,7 +100,7 @@ def tol_of(y, size, dtype, K):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows, K, O", [(1, 1, 1), (1, 1024, 100), (2, 64, 33), (16, 130, 16), (17, 100, 50), (48, 1000, 129), (64, 32, 64),
+@pytest.mark.parametrize("rows, K, O", [(1, 1, 1), (1, 1024, 100), (2, 64, 33), (4, 3333, 70), (5, 3333, 70), (16, 130, 16), (17, 100, 50), (48, 1000, 129), (64, 32, 64),
                                         (65, 256, 70), (100, 5000, 20), (130, 515, 260), (257, 96, 300), (300, 1024, 512)])
 def test_project(rows, K, O, dtype):
     g = torch.Generator().manual_seed(rows + K)

@@ -17,19 +17,23 @@ __device__ __forceinline__ f32x4 mma_mx(i32x4 a, int ea, i32x4 b, int eb, f32x4 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, 0, ea, 0, eb);
 }
 
-// Eight elements of a row from column c on; zeros past its end.
+// Eight elements of a row from column c on; zeros past its end. kOnce: past the caches.
 template <class T>
-__device__ __forceinline__ void mx_load(float (&v)[8], const T* row, int c, int K) {
+struct MxQuarter {
   T e[8];
-  if (c + 8 <= K) {
-    __builtin_memcpy(e, row + c, sizeof(e));
-  } else {
+  template <bool kOnce>
+  __device__ __forceinline__ void load(const T* row, int c, int K) {
+    if (c + 8 <= K) {
+      if (kOnce)
+        load_once(e, row + c);
+      else
+        __builtin_memcpy(e, row + c, sizeof(e));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = c + i < K ? row[c + i] : T(0);
+      for (int i = 0; i < 8; ++i) e[i] = c + i < K ? row[c + i] : T(0);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
-}
+};
 
 // The scale byte of a block from its largest magnitude's bits, which are those of a NaN if it has one.
 __device__ __forceinline__ int mx_scale(uint32_t most) {
@@ -57,49 +61,80 @@ __device__ __forceinline__ uint32_t quad_most(uint32_t v) {
   return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4e, 0xf, 0xf, false)));
 }
 
-// Where a thread of k_mx_quantize and k_mx_dequantize works: a quarter of a block, `quarters` to a row, rows side by side
-// in a workgroup where they are short.
+// Where a thread of k_mx_quantize and k_mx_dequantize works: a quarter of a block, `quarters` to a row; `parts` groups of
+// 256 threads take a row, or rows lie side by side in a group where they are short. A workgroup takes kMxGroups of the
+// groups, so that as many loads of a thread are in flight.
+constexpr int kMxGroups = 2;
 struct MxPlace {
   int64_t row;
   int quarter;
 };
-__device__ __forceinline__ MxPlace mx_place(int quarters, int parts) {
-  const int64_t id = block_number();
-  if (parts > 1) return {id / parts, static_cast<int>(id % parts) * 256 + static_cast<int>(threadIdx.x)};
-  const int each = 256 / quarters;  // rows of a workgroup
+__device__ __forceinline__ MxPlace mx_place(int64_t group, int quarters, int parts) {
+  if (parts > 1) {
+    const int64_t row = group >> 32 ? group / parts : static_cast<uint32_t>(group) / static_cast<uint32_t>(parts);
+    return {row, static_cast<int>(group - row * parts) * 256 + static_cast<int>(threadIdx.x)};
+  }
+  const int each = 256 / quarters;  // rows of a group
   const int r = threadIdx.x / quarters;
-  return {r < each ? id * each + r : (int64_t(1) << 62), static_cast<int>(threadIdx.x) % quarters};
+  return {r < each ? group * each + r : (int64_t(1) << 62), static_cast<int>(threadIdx.x) % quarters};
 }
 
-// kTiled: rows of whole steps of 8 blocks (zeros past K) and scales by step, as k_mx_tiles reads them; the workgroups past
-// the rows' lay out the weights' scales in the same way, the last block's in the place of those past it (which meet zeros).
-template <class T, bool kTiled>
+// Where the codes and scales of a row go. kMxSteps, for k_mx_tiles: steps of 8 blocks (zeros past K), [step][row][8]; the
+// first workgroups lay out the weights' scales in the same way, the last block's in the place of those past it (which meet
+// zeros). kMxOperands, for k_mx_rows: steps of 4 blocks (zeros past K), [step][tile of 16 rows][lane], the places past the
+// last row left as they are (their products are dropped).
+enum MxLayout { kMxRows, kMxSteps, kMxOperands };
+template <int kLayout>
+__device__ __forceinline__ int64_t mx_at(int64_t row, int64_t n_rows, int block, int blocks) {  // a block's place
+  if (kLayout == kMxSteps) return ((block / 8) * n_rows + row) * 8 + block % 8;
+  if (kLayout == kMxOperands) return ((block / 4) * ((n_rows + 15) / 16) + row / 16) * 64 + row % 16 + 16 * (block % 4);
+  return row * blocks + block;
+}
+
+template <class T, int kLayout>
 __global__ __launch_bounds__(256) void k_mx_quantize(const T* __restrict__ x, int64_t stride, int64_t n_rows, int K, int quarters,
                                                      int parts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                     int64_t groups, const uint8_t* __restrict__ w_scales, int O, int blocks,
+                                                     int first, const uint8_t* __restrict__ w_scales, int O, int blocks,
                                                      uint8_t* __restrict__ w_tiled) {
-  if (kTiled && block_number() >= groups) {
-    const int64_t id = (block_number() - groups) * 256 + threadIdx.x;
-    const int o = static_cast<int>(id % O), step = static_cast<int>(id / O);
-    if (8 * step >= blocks) return;
-    const uint8_t* const from = w_scales + static_cast<int64_t>(o) * blocks;
+  const int64_t block = block_number() - first;
+  if (kLayout == kMxSteps && block < 0) {
+    const int steps = (blocks + 7) / 8;
+    const uint32_t id = static_cast<uint32_t>(block_number()) * 256 + threadIdx.x;
+    const int o = id / steps, step = id % steps;
+    if (o >= O) return;
+    const uint8_t* const from = w_scales + static_cast<int64_t>(o) * blocks + 8 * step;
     uint8_t v[8];
+    if (8 * step + 8 <= blocks) {
+      __builtin_memcpy(v, from, 8);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = from[min(8 * step + i, blocks - 1)];
-    __builtin_memcpy(w_tiled + id * 8, v, 8);
+      for (int i = 0; i < 8; ++i) v[i] = from[min(i, blocks - 1 - 8 * step)];
+    }
+    __builtin_memcpy(w_tiled + (static_cast<int64_t>(step) * O + o) * 8, v, 8);
     return;
   }
-  const MxPlace at = mx_place(quarters, parts);
-  if (at.row >= n_rows || at.quarter >= quarters) return;  // whole blocks
-  float v[8];
-  mx_load(v, x + at.row * stride, at.quarter * 8, K);
-  uint32_t most = 0;
+  MxPlace at[kMxGroups];
+  MxQuarter<T> raw[kMxGroups];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-  const int e = mx_scale(quad_most(most));
-  reinterpret_cast<uint32_t*>(codes)[at.row * quarters + at.quarter] = mx_codes(v, e);
-  const int b = at.quarter / 4;
-  if (at.quarter % 4 == 0) scales[kTiled ? ((b / 8) * n_rows + at.row) * 8 + b % 8 : at.row * (quarters / 4) + b] = static_cast<uint8_t>(e);
+  for (int n = 0; n < kMxGroups; ++n) {
+    at[n] = mx_place(block * kMxGroups + n, quarters, parts);
+    if (at[n].row < n_rows && at[n].quarter < quarters) raw[n].template load<true>(x + at[n].row * stride, at[n].quarter * 8, K);
+  }
+#pragma unroll
+  for (int n = 0; n < kMxGroups; ++n) {
+    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;  // whole blocks
+    float v[8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = to_float(raw[n].e[i]);
+      most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    const int e = mx_scale(quad_most(most));
+    const int64_t to = mx_at<kLayout>(at[n].row, n_rows, at[n].quarter / 4, quarters / 4);
+    reinterpret_cast<uint32_t*>(codes)[to * 4 + at[n].quarter % 4] = mx_codes(v, e);
+    if (at[n].quarter % 4 == 0) scales[to] = static_cast<uint8_t>(e);
+  }
 }
 
 // The value of a code with the scale byte e.
@@ -112,20 +147,31 @@ __device__ __forceinline__ float mx_value(uint32_t code, int e) {
 template <class T>
 __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                        int64_t n_rows, int K, int quarters, int parts, T* __restrict__ x, int64_t stride) {
-  const MxPlace at = mx_place(quarters, parts);
-  if (at.row >= n_rows || at.quarter >= quarters) return;
-  const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[at.row * quarters + at.quarter];
-  const int e = scales[(at.row * quarters + at.quarter) / 4], c = at.quarter * 8;
-  T v[8];
+  MxPlace at[kMxGroups];
+  uint32_t w[kMxGroups];
+  int e[kMxGroups];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = from_float<T>(mx_value(w >> (4 * i) & 15, e));
-  T* const to = x + at.row * stride + c;
-  if (c + 8 <= K) {
-    __builtin_memcpy(to, v, sizeof(v));
-  } else {
+  for (int n = 0; n < kMxGroups; ++n) {
+    at[n] = mx_place(block_number() * kMxGroups + n, quarters, parts);
+    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;
+    w[n] = reinterpret_cast<const uint32_t*>(codes)[at[n].row * quarters + at[n].quarter];
+    e[n] = scales[(at[n].row * quarters + at[n].quarter) / 4];
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < K) to[i] = v[i];
+  for (int n = 0; n < kMxGroups; ++n) {
+    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;
+    const int c = at[n].quarter * 8;
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = from_float<T>(mx_value(w[n] >> (4 * i) & 15, e[n]));
+    T* const to = x + at[n].row * stride + c;
+    if (c + 8 <= K) {
+      __builtin_memcpy(to, v, sizeof(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < K) to[i] = v[i];
+    }
   }
 }
 
@@ -133,51 +179,99 @@ struct MxArgs {
   const uint8_t* w_codes;
   const uint8_t* w_scales;
   const void* bias;
+  const void* x;  // the rows themselves, for kFused, and otherwise their codes and scales as kMxOperands
+  int64_t x_stride;
   const uint8_t* x_codes;
   const uint8_t* x_scales;
   void* y;
   int64_t y_stride;
   int64_t n_rows;
-  int O, blocks;  // blocks of 32 along the reduction
+  int K, O, blocks;  // blocks of 32 along the reduction
 };
 
-// 16 outputs of up to 64 rows by a workgroup of eight waves, which share the reduction; each wave's sums are joined in
-// their order.
-template <class T>
-__global__ __launch_bounds__(512) void k_mx_rows(MxArgs a, int o_tiles) {
-  __shared__ f32x4 sums[8][4][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
-  const int64_t id = block_number();
-  const int64_t row0 = id / o_tiles * 64;
-  const int o0 = static_cast<int>(id % o_tiles) * 16;
-  if (row0 >= a.n_rows) return;
-  const int tiles = static_cast<int>(min<int64_t>(4, (a.n_rows - row0 + 15) / 16));
-  const int steps = (a.blocks + 3) / 4, each = (steps + 7) / 8;
-  const int64_t wrow = min(o0 + l16, a.O - 1);
-  f32x4 acc[4] = {};
-  for (int s = wave * each; s < min(steps, wave * each + each); ++s) {
-    const int b = 4 * s + q;
-    const bool have = b < a.blocks;
-    const i32x4 none = {0, 0, 0, 0};
-    const i32x4 w = have ? *reinterpret_cast<const i32x4*>(a.w_codes + (wrow * a.blocks + b) * 16) : none;
-    const int we = have ? a.w_scales[wrow * a.blocks + b] : 127;
+// 16 outputs of up to 16 kTiles rows by a workgroup of eight waves, which share the reduction; each wave's sums are joined
+// in their order. Bound by reading W, so a wave requests kMxBatch steps of 128 values at a time. kFused: every workgroup
+// quantises the rows itself, into LDS, while its first weights are on their way.
+constexpr int kMxBatch = 3;
+template <class T, int kTiles, bool kFused>
+__global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
+  __shared__ f32x4 sums[8][kTiles][64];
+  extern __shared__ __align__(16) uint8_t rows[];  // kFused: codes [row][steps][4][16], then scales [row][steps][4]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, q = lane >> 4;
+  const int o0 = static_cast<int>(block_number()) * 16;
+  if (o0 >= a.O) return;
+  const int steps = (a.blocks + 3) / 4, each = (steps + 7) / 8, end = min(steps, wave * each + each), n_rows = static_cast<int>(a.n_rows);
+  const int64_t wrow = static_cast<int64_t>(min(o0 + l16, a.O - 1)) * a.blocks;
+  f32x4 acc[kTiles] = {};
+  i32x4 w[kMxBatch], x[kMxBatch][kTiles];
+  int we[kMxBatch], xe[kMxBatch][kTiles];
+  auto request_w = [&](int s0) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t >= tiles) break;
-      const int64_t row = min(row0 + 16 * t + l16, a.n_rows - 1);
-      const i32x4 x = have ? *reinterpret_cast<const i32x4*>(a.x_codes + (row * a.blocks + b) * 16) : none;
-      const int xe = have ? a.x_scales[row * a.blocks + b] : 127;
-      acc[t] = mma_mx(w, we, x, xe, acc[t]);
+    for (int u = 0; u < kMxBatch; ++u) {
+      // past the last block: the last one's weights, which meet zeros
+      const int at = min(4 * min(s0 + u, steps - 1) + q, a.blocks - 1);
+      w[u] = *reinterpret_cast<const i32x4*>(a.w_codes + (wrow + at) * 16);
+      we[u] = a.w_scales[wrow + at];
     }
+  };
+  auto request_x = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      const int s = min(s0 + u, steps - 1);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        if (kFused) {
+          const int from = (min(l16, n_rows - 1) * steps + s) * 4 + q;
+          x[u][t] = reinterpret_cast<const i32x4*>(rows)[from];
+          xe[u][t] = rows[n_rows * steps * 64 + from];
+        } else {
+          const uint32_t from = (s * static_cast<uint32_t>((n_rows + 15) / 16) + t) * 64 + lane;
+          x[u][t] = reinterpret_cast<const i32x4*>(a.x_codes)[from];
+          xe[u][t] = a.x_scales[from];
+        }
+      }
+    }
+  };
+  int s0 = wave * each;
+  request_w(s0);
+  if (kFused) {
+    const int quarters = 16 * steps;
+    for (int i = tid; i < n_rows * quarters; i += 512) {
+      const int row = i / quarters;
+      MxQuarter<T> raw;
+      raw.template load<false>(static_cast<const T*>(a.x) + row * a.x_stride, (i - row * quarters) * 8, a.K);
+      float v[8];
+      uint32_t most = 0;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        v[n] = to_float(raw.e[n]);
+        most = max(most, __float_as_uint(v[n]) & 0x7fffffffu);
+      }
+      const int e = mx_scale(quad_most(most));
+      reinterpret_cast<uint32_t*>(rows)[i] = mx_codes(v, e);
+      if (i % 4 == 0) rows[n_rows * steps * 64 + i / 4] = static_cast<uint8_t>(e);
+    }
+    __syncthreads();
+  }
+  for (; s0 < end; s0 += kMxBatch) {
+    request_x(s0);
+    __builtin_amdgcn_sched_barrier(0);  // all of a batch on its way before the first product
+#pragma unroll
+    for (int u = 0; u < kMxBatch; ++u) {
+      if (s0 + u >= end) break;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) acc[t] = mma_mx(w[u], we[u], x[u][t], xe[u][t], acc[t]);
+    }
+    if (s0 + kMxBatch < end) request_w(s0 + kMxBatch);
   }
 #pragma unroll
-  for (int t = 0; t < 4; ++t) sums[wave][t][lane] = acc[t];
+  for (int t = 0; t < kTiles; ++t) sums[wave][t][lane] = acc[t];
   __syncthreads();
-  if (wave >= tiles) return;
+  if (wave >= kTiles) return;
   f32x4 sum = sums[0][wave][lane];
 #pragma unroll
   for (int v = 1; v < 8; ++v) sum += sums[v][wave][lane];
-  const int64_t row = row0 + 16 * wave + l16;
+  const int row = 16 * wave + l16;
   if (row >= a.n_rows) return;
   T* const y = static_cast<T*>(a.y) + row * a.y_stride;
 #pragma unroll
@@ -191,16 +285,17 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a, int o_tiles) {
 // Many rows: tiles of kSide x kSide outputs, a wave 64 outputs by kSide / 2 rows of them, in products of 32 x 32 x 64. A
 // step is 256 values (128 bytes) of each row, in two buffers of LDS that are loaded without passing through registers, the
 // next step's while this one's products run. Rows lie there as eight chunks of 16 bytes, chunk c of row i at place c ^ f(i)
-// (see place_w and place_x), so that the eight rows that a read touches at a time take all eight.
+// (mx_place_of), so that the eight rows that a read touches at a time take all eight.
 // The order along the reduction is free: lane group h of a wave takes the step's blocks 4 h .. 4 h + 3, whose scales are
-// one word. So is that of a tile's outputs: a lane holds 32 adjacent ones of a row, which leave it in whole pieces.
+// one word. Outputs lie along the lanes, so that a store fills 64 bytes of a row (bf16); with rows along the lanes and 16
+// bytes of each a store the call below took 48 us for them.
 // ---------------------------------------------------------------------------------------------
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 struct MxTileArgs {
   const uint8_t* w_codes;  // [O][blocks][16]
   const uint8_t* w_scales;  // [step][O][8]
-  const uint8_t* x_codes;  // [row][steps][8][16]
+  const uint8_t* x_codes;  // [step][row][8][16]
   const uint8_t* x_scales;  // [step][row][8]
   const void* bias;
   void* y;
@@ -209,8 +304,7 @@ struct MxTileArgs {
   int O, blocks, steps, tiles_r, tiles_o;
 };
 
-__device__ __forceinline__ int mx_place_x(int row) { return row & 7; }
-__device__ __forceinline__ int mx_place_w(int row) { return (row & 3) | ((row >> 3) & 4); }
+__device__ __forceinline__ int mx_place_of(int row) { return row & 7; }
 
 template <class T, int kSide>
 __global__ __launch_bounds__(kSide * 2, 2) void k_mx_tiles(MxTileArgs a) {
@@ -238,33 +332,42 @@ __global__ __launch_bounds__(kSide * 2, 2) void k_mx_tiles(MxTileArgs a) {
 
   // load i of a thread: place tid % 8 of row tid / 8 + i kThreads / 8; rows past the last are read from it
   const char* const wb = reinterpret_cast<const char*>(a.w_codes) + static_cast<int64_t>(o0) * a.blocks * 16;
-  const char* const xb = reinterpret_cast<const char*>(a.x_codes) + r0 * a.steps * 128;
+  const char* const xb = reinterpret_cast<const char*>(a.x_codes) + r0 * 128;
+  const int c = (tid & 7) ^ mx_place_of(tid >> 3);
+  uint32_t w_at[kLoads], x_at[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = (tid >> 3) + i * (kThreads / 8);
+    w_at[i] = (min(row, last_o) * a.blocks + c) * 16;
+    x_at[i] = min(row, last_r) * 128 + c * 16;
+  }
   auto fetch = [&](int step, int buf) {
-    uint4* const to = stage + buf * kBuf + (tid & ~63);
+    uint4* const to = stage + buf * kBuf + wave * 64;
+    if (8 * step + 8 <= a.blocks) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = (tid >> 3) + i * (kThreads / 8), c = (tid & 7) ^ mx_place_w(row);
+      for (int i = 0; i < kLoads; ++i) load_to_lds(wb + step * 128, w_at[i], to + i * kThreads);
+    } else {
       // W's blocks past the last meet zeros of x: the last one is read in their place
-      load_to_lds(wb, (min(row, last_o) * a.blocks + min(8 * step + c, a.blocks - 1)) * 16, to + i * kThreads);
+      const int more = (min(8 * step + c, a.blocks - 1) - c) * 16;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_to_lds(wb, w_at[i] + more, to + i * kThreads);
     }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = (tid >> 3) + i * (kThreads / 8), c = (tid & 7) ^ mx_place_x(row);
-      load_to_lds(xb + step * 128, min(row, last_r) * a.steps * 128 + c * 16, to + kSide * 8 + i * kThreads);
-    }
+    for (int i = 0; i < kLoads; ++i) load_to_lds(xb + step * a.n_rows * 128, x_at[i], to + kSide * 8 + i * kThreads);
   };
-  // W's rows of a wave: row m of tile t is output 32 (m / 4 % 2) + 16 t + 4 (m / 8) + m % 4 of its 64
-  int w_row[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) w_row[t] = wo * 64 + 32 * (l32 >> 2 & 1) + 16 * t + 4 * (l32 >> 3) + (l32 & 3);
   int ew[2], ex[kRT], ew_next[2], ex_next[kRT];
+  uint32_t ew_at[2], ex_at[kRT];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) ew_at[t] = min(wo * 64 + 32 * t + l32, last_o) * 8 + 4 * half;
+#pragma unroll
+  for (int t = 0; t < kRT; ++t) ex_at[t] = min(wr * (kSide / 2) + 32 * t + l32, last_r) * 8 + 4 * half;
   auto fetch_scales = [&](int step) {
+    const uint8_t* const w = a.w_scales + (static_cast<int64_t>(step) * a.O + o0) * 8;
+    const uint8_t* const x = a.x_scales + (step * a.n_rows + r0) * 8;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      ew_next[t] = *reinterpret_cast<const int*>(a.w_scales + (static_cast<int64_t>(step) * a.O + o0 + min(w_row[t], last_o)) * 8 + 4 * half);
+    for (int t = 0; t < 2; ++t) ew_next[t] = *reinterpret_cast<const int*>(w + ew_at[t]);
 #pragma unroll
-    for (int t = 0; t < kRT; ++t)
-      ex_next[t] = *reinterpret_cast<const int*>(a.x_scales + (step * a.n_rows + r0 + min(wr * (kSide / 2) + 32 * t + l32, last_r)) * 8 + 4 * half);
+    for (int t = 0; t < kRT; ++t) ex_next[t] = *reinterpret_cast<const int*>(x + ex_at[t]);
   };
 
   f32x16 acc[2][kRT];
@@ -286,61 +389,61 @@ __global__ __launch_bounds__(kSide * 2, 2) void k_mx_tiles(MxTileArgs a) {
     for (int t = 0; t < kRT; ++t) ex[t] = ex_next[t];
     const uint4* const w = stage + (step & 1) * kBuf;
     const uint4* const x = w + kSide * 8;
-    if (step + 1 < a.steps) {
-      fetch(step + 1, ~step & 1);
-      fetch_scales(step + 1);
-    }
-    auto products = [&](auto s_) {
-      constexpr int s = decltype(s_)::value;
-      i32x8 wf[2], xf[kRT];
+    // operands of blocks s and 4 + s, requested while the products of the ones before them run
+    uint4 wf[2][2], xf[2][kRT];
+    auto request = [&](int s) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint4 v = w[w_row[t] * 8 + ((4 * half + s) ^ mx_place_w(w_row[t]))];
-        wf[t] = i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+        const int row = wo * 64 + 32 * t + l32;
+        wf[s & 1][t] = w[row * 8 + ((4 * half + s) ^ mx_place_of(row))];
       }
 #pragma unroll
       for (int t = 0; t < kRT; ++t) {
         const int row = wr * (kSide / 2) + 32 * t + l32;
-        const uint4 v = x[row * 8 + ((4 * half + s) ^ mx_place_x(row))];
-        xf[t] = i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+        xf[s & 1][t] = x[row * 8 + ((4 * half + s) ^ mx_place_of(row))];
       }
+    };
+    auto operand = [](uint4 v) {
+      return i32x8{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
+    };
+    auto products = [&](auto s_) {
+      constexpr int s = decltype(s_)::value;
+      if (s < 3) request(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int r = 0; r < kRT; ++r)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          acc[t][r] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[t], xf[r], acc[t][r], 4, 4, s, ew[t], s, ex[r]);
+          acc[t][r] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(xf[s & 1][r]), operand(wf[s & 1][t]), acc[t][r], 4, 4, s, ex[r], s, ew[t]);
+      __builtin_amdgcn_sched_barrier(0);
     };
+    request(0);
+    if (step + 1 < a.steps) {
+      fetch(step + 1, ~step & 1);
+      fetch_scales(step + 1);
+    }
     products(std::integral_constant<int, 0>{});
     products(std::integral_constant<int, 1>{});
     products(std::integral_constant<int, 2>{});
     products(std::integral_constant<int, 3>{});
   }
 
-  const int o = o0 + wo * 64 + 32 * half;  // this lane's 32 outputs
-  if (o >= a.O) return;
-  const bool whole = o + 32 <= a.O;
+  // lane: an output, and rows 8 (e / 4) + 4 half + e % 4 of each tile
+  const bool whole = last_r == kSide - 1;
 #pragma unroll
-  for (int r = 0; r < kRT; ++r) {
-    const int row = wr * (kSide / 2) + 32 * r + l32;
-    if (row > last_r) continue;
-    T* const y = static_cast<T*>(a.y) + (r0 + row) * a.y_stride + o;
+  for (int t = 0; t < 2; ++t) {
+    const int o = o0 + wo * 64 + 32 * t + l32;
+    if (o >= a.O) continue;
+    const float bias = a.bias ? to_float(static_cast<const T*>(a.bias)[o]) : 0.f;
+    const int first = wr * (kSide / 2) + 4 * half;
+    T* const y = static_cast<T*>(a.y) + (r0 + first) * a.y_stride + o;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      T v[16];
+    for (int r = 0; r < kRT; ++r)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        float sum = acc[t][r][e];
-        if (a.bias && o + 16 * t + e < a.O) sum += to_float(static_cast<const T*>(a.bias)[o + 16 * t + e]);
-        v[e] = from_float<T>(sum);
+        const int row = 32 * r + 8 * (e >> 2) + (e & 3);
+        if (whole || first + row <= last_r) __builtin_nontemporal_store(from_float<T>(acc[t][r][e] + bias), y + row * a.y_stride);
       }
-      if (whole) {
-        __builtin_memcpy(y + 16 * t, v, sizeof(v));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (o + 16 * t + e < a.O) y[16 * t + e] = v[e];
-      }
-    }
   }
 }
 

@@ -32,63 +32,61 @@ cdrge_status check_rows(const cdrge_mx_config* c, int64_t n_rows, const void* x,
   return CDRGE_OK;
 }
 
-// Workgroups of the kernels that take a quarter of a block a thread; parts: workgroups of a row.
+// Workgroups of the kernels that take a quarter of a block a thread; parts: as in mx_place.
 int64_t quarter_groups(int64_t n_rows, int quarters, int* parts) {
   *parts = (quarters + 255) / 256;
-  if (*parts > 1) return n_rows * *parts;
-  const int each = 256 / quarters;
-  return (n_rows + each - 1) / each;
+  const int each = *parts > 1 ? 1 : 256 / quarters;
+  return ((n_rows + each - 1) / each * *parts + kMxGroups - 1) / kMxGroups;
 }
 
 constexpr int64_t kMostGroups = int64_t(1) << 35;  // 2^20 by 2^15 of a grid
 
-// tiled: for k_mx_tiles, with the weights' scales (w_scales to w_tiled) in the same launch
-template <class T>
+// kMxSteps: with the weights' scales (w_scales to w_tiled) in the same launch
+template <class T, int kLayout>
 cdrge_status quantize(const cdrge_mx_config* c, int64_t n_rows, const void* x, int64_t stride, uint8_t* codes,
-                      uint8_t* scales, bool tiled, const uint8_t* w_scales, uint8_t* w_tiled, hipStream_t s) {
+                      uint8_t* scales, const uint8_t* w_scales, uint8_t* w_tiled, hipStream_t s) {
+  constexpr int kStep = kLayout == kMxSteps ? 8 : kLayout == kMxOperands ? 4 : 1;  // blocks
   int parts = 1;
-  const int blocks = blocks_of(c), steps = (blocks + 7) / 8, quarters = 4 * (tiled ? 8 * steps : blocks);
+  const int blocks = blocks_of(c), steps = (blocks + kStep - 1) / kStep, quarters = 4 * kStep * steps;
   const int64_t n = quarter_groups(n_rows, quarters, &parts);
-  const int64_t more = tiled ? (int64_t(c->out_features) * steps + 255) / 256 : 0;
-  if (n + more > kMostGroups) return CDRGE_ERR_UNSUPPORTED;
+  const int64_t first = kLayout == kMxSteps ? (int64_t(c->out_features) * steps + 255) / 256 : 0;
+  if (n + first > kMostGroups) return CDRGE_ERR_UNSUPPORTED;
   if (n == 0) return CDRGE_OK;
-  const T* const from = static_cast<const T*>(x);
-  if (tiled)
-    hipLaunchKernelGGL((k_mx_quantize<T, true>), grid_of(n + more, 256), dim3(256), 0, s, from, stride, n_rows, c->in_features,
-                       quarters, parts, codes, scales, n, w_scales, c->out_features, blocks, w_tiled);
-  else
-    hipLaunchKernelGGL((k_mx_quantize<T, false>), grid_of(n, 256), dim3(256), 0, s, from, stride, n_rows, c->in_features,
-                       quarters, parts, codes, scales, n, w_scales, c->out_features, blocks, w_tiled);
+  hipLaunchKernelGGL((k_mx_quantize<T, kLayout>), grid_of(n + first, 256), dim3(256), 0, s, static_cast<const T*>(x), stride, n_rows,
+                     c->in_features, quarters, parts, codes, scales, static_cast<int>(first), w_scales, c->out_features, blocks,
+                     w_tiled);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
 
 // How a call is cut up and where its workspace's parts lie; by sizes alone.
 struct Plan {
-  int side;  // of the tiles of k_mx_tiles; 0: k_mx_rows
+  int side;    // of the tiles of k_mx_tiles; 0: k_mx_rows
+  bool fused;  // which quantises the rows itself, without a workspace
   int blocks, steps, tiles_r, tiles_o;
   size_t codes, scales, w_scales, total;
 };
+
+// Up to four rows are quantised by every workgroup of k_mx_rows, which saves a launch, where their codes fit in 32 KB.
+constexpr int kFusedBlocks = 2000;
 
 Plan make_plan(const cdrge_mx_config* c, int64_t n_rows) {
   Plan p{};
   p.blocks = blocks_of(c);
   p.steps = (p.blocks + 7) / 8;
   const int64_t r128 = (n_rows + 127) / 128, o128 = (c->out_features + 127) / 128;
+  p.fused = n_rows <= 4 && n_rows * p.blocks <= kFusedBlocks;
   if (n_rows > 64) p.side = r128 * o128 >= 1024 ? 256 : 128;
   if (p.side > 0) {
     p.tiles_r = static_cast<int>((n_rows + p.side - 1) / p.side);
     p.tiles_o = (c->out_features + p.side - 1) / p.side;
   }
-  const size_t row_blocks = p.side > 0 ? 8 * p.steps : p.blocks;
-  p.scales = align_up(16 * row_blocks * n_rows);
-  p.w_scales = align_up(p.scales + row_blocks * n_rows);
-  p.total = p.side > 0 ? align_up(p.w_scales + size_t(8) * p.steps * c->out_features) : p.w_scales;
+  // blocks of the rows: k_mx_tiles has whole steps of 8, k_mx_rows of 4 and tiles of 16 rows
+  const size_t blocks = p.side > 0 ? size_t(8) * p.steps * n_rows : size_t((p.blocks + 3) / 4 * 4) * ((n_rows + 15) / 16 * 16);
+  p.scales = align_up(16 * blocks);
+  p.w_scales = align_up(p.scales + blocks);
+  p.total = p.fused ? 0 : p.side > 0 ? align_up(p.w_scales + size_t(8) * p.steps * c->out_features) : p.w_scales;
   return p;
-}
-
-int64_t project_groups(const cdrge_mx_config* c, int64_t n_rows) {
-  return (n_rows + 63) / 64 * ((c->out_features + 15) / 16);
 }
 
 // Whether the call's sizes fit the kernels' counts.
@@ -111,22 +109,33 @@ cdrge_status launch_tiles(const MxTileArgs& a, hipStream_t s) {
   return CDRGE_OK;
 }
 
+template <class T, int kTiles, bool kFused>
+cdrge_status launch_rows(const MxArgs& a, hipStream_t s) {
+  const size_t lds = kFused ? size_t(68) * a.n_rows * ((a.blocks + 3) / 4) : 0;
+  hipLaunchKernelGGL((k_mx_rows<T, kTiles, kFused>), grid_of((a.O + 15) / 16, 512), dim3(512), lds, s, a);
+  CDRGE_HIP(hipGetLastError());
+  return CDRGE_OK;
+}
+
 template <class T>
 cdrge_status project(const cdrge_mx_config* c, const uint8_t* w_codes, const uint8_t* w_scales, const void* bias, int64_t n_rows,
                      const void* x, int64_t x_stride, void* y, int64_t y_stride, const Plan& p, void* workspace, hipStream_t s) {
   uint8_t* const codes = static_cast<uint8_t*>(workspace) + p.codes;
   uint8_t* const scales = static_cast<uint8_t*>(workspace) + p.scales;
   uint8_t* const w_tiled = static_cast<uint8_t*>(workspace) + p.w_scales;
-  const cdrge_status st = quantize<T>(c, n_rows, x, x_stride, codes, scales, p.side > 0, w_scales, w_tiled, s);
-  if (st != CDRGE_OK) return st;
+  const MxArgs a{w_codes, w_scales, bias, x, x_stride, codes, scales, y, y_stride, n_rows, c->in_features, c->out_features, p.blocks};
+  if (p.fused) return launch_rows<T, 1, true>(a, s);
   if (p.side > 0) {
-    const MxTileArgs a{w_codes, w_tiled, codes, scales, bias, y, y_stride, n_rows, c->out_features, p.blocks, p.steps, p.tiles_r, p.tiles_o};
-    return p.side == 256 ? launch_tiles<T, 256>(a, s) : launch_tiles<T, 128>(a, s);
+    const cdrge_status st = quantize<T, kMxSteps>(c, n_rows, x, x_stride, codes, scales, w_scales, w_tiled, s);
+    if (st != CDRGE_OK) return st;
+    const MxTileArgs t{w_codes, w_tiled, codes, scales, bias, y, y_stride, n_rows, c->out_features, p.blocks, p.steps, p.tiles_r, p.tiles_o};
+    return p.side == 256 ? launch_tiles<T, 256>(t, s) : launch_tiles<T, 128>(t, s);
   }
-  const MxArgs a{w_codes, w_scales, bias, codes, scales, y, y_stride, n_rows, c->out_features, p.blocks};
-  hipLaunchKernelGGL(k_mx_rows<T>, grid_of(project_groups(c, n_rows), 512), dim3(512), 0, s, a, (a.O + 15) / 16);
-  CDRGE_HIP(hipGetLastError());
-  return CDRGE_OK;
+  const cdrge_status st = quantize<T, kMxOperands>(c, n_rows, x, x_stride, codes, scales, nullptr, nullptr, s);
+  if (st != CDRGE_OK) return st;
+  if (n_rows <= 16) return launch_rows<T, 1, false>(a, s);
+  if (n_rows <= 32) return launch_rows<T, 2, false>(a, s);
+  return n_rows <= 48 ? launch_rows<T, 3, false>(a, s) : launch_rows<T, 4, false>(a, s);
 }
 
 }  // namespace
@@ -138,8 +147,8 @@ cdrge_status cdrge_mx_quantize(const cdrge_mx_config* cfg, int64_t n_rows, const
   const cdrge_status st = check_rows(cfg, n_rows, x, x_stride, codes, scales);
   if (st != CDRGE_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return cfg->dtype == CDRGE_F32 ? quantize<float>(cfg, n_rows, x, x_stride, codes, scales, false, nullptr, nullptr, s)
-                                 : quantize<uint16_t>(cfg, n_rows, x, x_stride, codes, scales, false, nullptr, nullptr, s);
+  return cfg->dtype == CDRGE_F32 ? quantize<float, kMxRows>(cfg, n_rows, x, x_stride, codes, scales, nullptr, nullptr, s)
+                                 : quantize<uint16_t, kMxRows>(cfg, n_rows, x, x_stride, codes, scales, nullptr, nullptr, s);
 }
 
 cdrge_status cdrge_mx_dequantize(const cdrge_mx_config* cfg, int64_t n_rows, const uint8_t* codes,
@@ -181,7 +190,7 @@ cdrge_status cdrge_mx_project(const cdrge_mx_config* cfg, const uint8_t* w_codes
   if (x_stride < cfg->in_features || y_stride < cfg->out_features) return CDRGE_ERR_INVALID_ARG;
   if (n_rows == 0) return CDRGE_OK;
   if (!x || !y) return CDRGE_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < need || !aligned(workspace, kAlign))
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, kAlign)))
     return workspace_error("cdrge_mx_project", need, workspace ? workspace_bytes : 0);
   const Plan p = make_plan(cfg, n_rows);
   const hipStream_t s = static_cast<hipStream_t>(stream);
