@@ -24,11 +24,11 @@ cdrge_status check(const cdrge_score_config* c, int64_t n_rows, const void* logi
   return CDRGE_OK;
 }
 
-template <class T, bool kGrad, int kTeam, int kPieces>
+template <class T, int kMode, int kTeam, int kPieces>
 cdrge_status launch(const ScoreArgs& a, hipStream_t s) {
   constexpr int kThreads = distill_threads(kTeam), kRows = kThreads / kTeam;
-  const size_t lds = a.top_k > 0 ? score_lds(a.cap, kTeam) * kRows : 0;
-  hipLaunchKernelGGL((k_scores<T, kGrad, kTeam, kPieces>), grid_of((a.n_rows + kRows - 1) / kRows, kThreads), dim3(kThreads),
+  const size_t lds = kMode == kScoreTop ? score_lds(a.cap, kTeam) * kRows : 0;
+  hipLaunchKernelGGL((k_scores<T, kMode, kTeam, kPieces>), grid_of((a.n_rows + kRows - 1) / kRows, kThreads), dim3(kThreads),
                      lds, s, a);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
@@ -36,28 +36,35 @@ cdrge_status launch(const ScoreArgs& a, hipStream_t s) {
 
 // Threads of a row and pieces a thread: as for the distillation loss the fewest threads that hold the row in at most 8
 // pieces each, but where alternatives are asked for no fewer than there are of them, as far as the row has pieces.
-template <class T, bool kGrad>
+template <class T, int kMode>
 cdrge_status launch_team(const ScoreArgs& a, hipStream_t s) {
   const int pieces = (a.vocab + DistillRow<T>::kPer - 1) / DistillRow<T>::kPer, least = std::min(a.top_k, pieces);
   if (least <= 16 && pieces <= 16 * 4 && a.top_k <= 64)
-    return pieces <= 16 ? launch<T, kGrad, 16, 1>(a, s) : launch<T, kGrad, 16, 4>(a, s);
-  if (least <= 64 && pieces <= 64 * 2) return launch<T, kGrad, 64, 2>(a, s);
-  if (least <= 64 && pieces <= 64 * 8) return launch<T, kGrad, 64, 8>(a, s);
-  if (least <= 256 && pieces <= 256 * 4) return launch<T, kGrad, 256, 4>(a, s);
-  if (least <= 256 && pieces <= 256 * 8) return launch<T, kGrad, 256, 8>(a, s);
-  if (least <= 512 && pieces <= 512 * 8) return launch<T, kGrad, 512, 8>(a, s);
-  if (pieces <= 1024 * 8) return launch<T, kGrad, 1024, 8>(a, s);
-  return launch<T, kGrad, 1024, 0>(a, s);
+    return pieces <= 16 ? launch<T, kMode, 16, 1>(a, s) : launch<T, kMode, 16, 4>(a, s);
+  if (least <= 64 && pieces <= 64 * 2) return launch<T, kMode, 64, 2>(a, s);
+  if (least <= 64 && pieces <= 64 * 8) return launch<T, kMode, 64, 8>(a, s);
+  if (least <= 256 && pieces <= 256 * 4) return launch<T, kMode, 256, 4>(a, s);
+  if (least <= 256 && pieces <= 256 * 8) return launch<T, kMode, 256, 8>(a, s);
+  if (least <= 512 && pieces <= 512 * 8) return launch<T, kMode, 512, 8>(a, s);
+  if (pieces <= 1024 * 8) return launch<T, kMode, 1024, 8>(a, s);
+  if (pieces <= 1024 * 16) return launch<T, kMode, 1024, 16>(a, s);
+  return launch<T, kMode, 1024, 0>(a, s);
 }
 
-template <bool kGrad>
+template <int kMode>
 cdrge_status enqueue(const cdrge_score_config* c, ScoreArgs& a, hipStream_t s) {
   if (a.n_rows == 0) return CDRGE_OK;
   a.vocab = c->vocab;
   a.tau = c->temperature;
-  a.top_k = kGrad ? 0 : c->top_k;
+  a.top_k = kMode == kScoreTop ? c->top_k : 0;
   a.cap = std::min(c->vocab, std::max(4 * a.top_k, 128));
-  return c->dtype == CDRGE_F32 ? launch_team<float, kGrad>(a, s) : launch_team<uint16_t, kGrad>(a, s);
+  if (a.cap > 512)  // sorted as a power of two
+    for (int n = 1024;; n *= 2)
+      if (n >= a.cap) {
+        a.cap = n;
+        break;
+      }
+  return c->dtype == CDRGE_F32 ? launch_team<float, kMode>(a, s) : launch_team<uint16_t, kMode>(a, s);
 }
 
 }  // namespace
@@ -80,7 +87,8 @@ cdrge_status cdrge_token_scores(const cdrge_score_config* cfg, int64_t n_rows, c
   a.top_ids = top_ids;
   a.top_logprobs = top_logprobs;
   a.n_rows = n_rows;
-  return enqueue<false>(cfg, a, static_cast<hipStream_t>(stream));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return cfg->top_k > 0 ? enqueue<kScoreTop>(cfg, a, s) : enqueue<kScoreOnly>(cfg, a, s);
 }
 
 cdrge_status cdrge_token_scores_grad(const cdrge_score_config* cfg, int64_t n_rows, const void* logits,
@@ -99,7 +107,7 @@ cdrge_status cdrge_token_scores_grad(const cdrge_score_config* cfg, int64_t n_ro
   a.dlogits = dlogits;
   a.dlogits_stride = dlogits_stride;
   a.n_rows = n_rows;
-  return enqueue<true>(cfg, a, static_cast<hipStream_t>(stream));
+  return enqueue<kScoreGrad>(cfg, a, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"
