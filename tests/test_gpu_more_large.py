@@ -129,10 +129,10 @@ def test_four_bit_rows_far_apart():
     assert torch.equal(x, back)
 
 
-@pytest.mark.parametrize("rows, O", [(550_000, 4100), (60, 1 << 20)])
-def test_project_many_outputs(rows, O):
+@pytest.mark.parametrize("rows, O, K", [(550_000, 4100, 40), (60, 1 << 20, 40), (16, 1 << 20, 40), (17, 32_650, 1000), (33, 32_640, 700),
+                                        (17, 32_641, 1)])
+def test_project_many_outputs(rows, O, K):
     g = torch.Generator().manual_seed(4)
-    K = 40
     f = b.MxFormat(b.make_mx_config(K, 1, "bf16"))
     w = f.quantize(torch.randn(O, K, generator=g).bfloat16().cuda(), *f.empty(O))
     x = torch.randn(rows, K, generator=g).bfloat16().cuda()

@@ -62,9 +62,7 @@ __device__ __forceinline__ uint32_t quad_most(uint32_t v) {
 }
 
 // Where a thread of k_mx_quantize and k_mx_dequantize works: a quarter of a block, `quarters` to a row; `parts` groups of
-// 256 threads take a row, or rows lie side by side in a group where they are short. A workgroup takes kMxGroups of the
-// groups, so that as many loads of a thread are in flight.
-constexpr int kMxGroups = 2;
+// 256 threads take a row, or rows lie side by side in a group where they are short.
 struct MxPlace {
   int64_t row;
   int quarter;
@@ -91,6 +89,8 @@ __device__ __forceinline__ int64_t mx_at(int64_t row, int64_t n_rows, int block,
   return row * blocks + block;
 }
 
+// A quarter of a block a thread, the block's largest magnitude by two lane permutations. Bound by reading x: 8192 x 4096 bf16
+// with back again 40 us, 4.2 TB/s; the rows of a product in the layout of kMxSteps 23 us. Two quarters a thread: the same.
 template <class T, int kLayout>
 __global__ __launch_bounds__(256) void k_mx_quantize(const T* __restrict__ x, int64_t stride, int64_t n_rows, int K, int quarters,
                                                      int parts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -113,28 +113,21 @@ __global__ __launch_bounds__(256) void k_mx_quantize(const T* __restrict__ x, in
     __builtin_memcpy(w_tiled + (static_cast<int64_t>(step) * O + o) * 8, v, 8);
     return;
   }
-  MxPlace at[kMxGroups];
-  MxQuarter<T> raw[kMxGroups];
+  const MxPlace at = mx_place(block, quarters, parts);
+  if (at.row >= n_rows || at.quarter >= quarters) return;  // whole blocks
+  MxQuarter<T> raw;
+  raw.template load<true>(x + at.row * stride, at.quarter * 8, K);
+  float v[8];
+  uint32_t most = 0;
 #pragma unroll
-  for (int n = 0; n < kMxGroups; ++n) {
-    at[n] = mx_place(block * kMxGroups + n, quarters, parts);
-    if (at[n].row < n_rows && at[n].quarter < quarters) raw[n].template load<true>(x + at[n].row * stride, at[n].quarter * 8, K);
+  for (int i = 0; i < 8; ++i) {
+    v[i] = to_float(raw.e[i]);
+    most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
   }
-#pragma unroll
-  for (int n = 0; n < kMxGroups; ++n) {
-    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;  // whole blocks
-    float v[8];
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = to_float(raw[n].e[i]);
-      most = max(most, __float_as_uint(v[i]) & 0x7fffffffu);
-    }
-    const int e = mx_scale(quad_most(most));
-    const int64_t to = mx_at<kLayout>(at[n].row, n_rows, at[n].quarter / 4, quarters / 4);
-    reinterpret_cast<uint32_t*>(codes)[to * 4 + at[n].quarter % 4] = mx_codes(v, e);
-    if (at[n].quarter % 4 == 0) scales[to] = static_cast<uint8_t>(e);
-  }
+  const int e = mx_scale(quad_most(most));
+  const int64_t to = mx_at<kLayout>(at.row, n_rows, at.quarter / 4, quarters / 4);
+  reinterpret_cast<uint32_t*>(codes)[to * 4 + at.quarter % 4] = mx_codes(v, e);
+  if (at.quarter % 4 == 0) scales[to] = static_cast<uint8_t>(e);
 }
 
 // The value of a code with the scale byte e.
@@ -147,31 +140,20 @@ __device__ __forceinline__ float mx_value(uint32_t code, int e) {
 template <class T>
 __global__ __launch_bounds__(256) void k_mx_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                        int64_t n_rows, int K, int quarters, int parts, T* __restrict__ x, int64_t stride) {
-  MxPlace at[kMxGroups];
-  uint32_t w[kMxGroups];
-  int e[kMxGroups];
+  const MxPlace at = mx_place(block_number(), quarters, parts);
+  if (at.row >= n_rows || at.quarter >= quarters) return;
+  const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[at.row * quarters + at.quarter];
+  const int e = scales[(at.row * quarters + at.quarter) / 4], c = at.quarter * 8;
+  T v[8];
 #pragma unroll
-  for (int n = 0; n < kMxGroups; ++n) {
-    at[n] = mx_place(block_number() * kMxGroups + n, quarters, parts);
-    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;
-    w[n] = reinterpret_cast<const uint32_t*>(codes)[at[n].row * quarters + at[n].quarter];
-    e[n] = scales[(at[n].row * quarters + at[n].quarter) / 4];
-  }
+  for (int i = 0; i < 8; ++i) v[i] = from_float<T>(mx_value(w >> (4 * i) & 15, e));
+  T* const to = x + at.row * stride + c;
+  if (c + 8 <= K) {
+    __builtin_memcpy(to, v, sizeof(v));
+  } else {
 #pragma unroll
-  for (int n = 0; n < kMxGroups; ++n) {
-    if (at[n].row >= n_rows || at[n].quarter >= quarters) continue;
-    const int c = at[n].quarter * 8;
-    T v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = from_float<T>(mx_value(w[n] >> (4 * i) & 15, e[n]));
-    T* const to = x + at[n].row * stride + c;
-    if (c + 8 <= K) {
-      __builtin_memcpy(to, v, sizeof(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < K) to[i] = v[i];
-    }
+    for (int i = 0; i < 8; ++i)
+      if (c + i < K) to[i] = v[i];
   }
 }
 
@@ -190,9 +172,10 @@ struct MxArgs {
 };
 
 // 16 outputs of up to 16 kTiles rows by a workgroup of eight waves, which share the reduction; each wave's sums are joined
-// in their order. Bound by reading W, so a wave requests kMxBatch steps of 128 values at a time. kFused: every workgroup
-// quantises the rows itself, into LDS, while its first weights are on their way.
-constexpr int kMxBatch = 3;
+// in their order. Bound by reading W, with a request a wave in flight: 32768 x 4096, one row 20.5 us (3.5 TB/s), 16 rows 25;
+// with few outputs by the launches and the loads' latency: 4096 x 4096, one row 7.0 us, 64 rows 11. Requests of two or three
+// steps at a time: one row 7.6, 64 rows 12.9. kFused: every workgroup quantises the rows itself, into LDS, while its first
+// weights are on their way.
 template <class T, int kTiles, bool kFused>
 __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
   __shared__ f32x4 sums[8][kTiles][64];
@@ -203,37 +186,30 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
   const int steps = (a.blocks + 3) / 4, each = (steps + 7) / 8, end = min(steps, wave * each + each), n_rows = static_cast<int>(a.n_rows);
   const int64_t wrow = static_cast<int64_t>(min(o0 + l16, a.O - 1)) * a.blocks;
   f32x4 acc[kTiles] = {};
-  i32x4 w[kMxBatch], x[kMxBatch][kTiles];
-  int we[kMxBatch], xe[kMxBatch][kTiles];
-  auto request_w = [&](int s0) {
-#pragma unroll
-    for (int u = 0; u < kMxBatch; ++u) {
-      // past the last block: the last one's weights, which meet zeros
-      const int at = min(4 * min(s0 + u, steps - 1) + q, a.blocks - 1);
-      w[u] = *reinterpret_cast<const i32x4*>(a.w_codes + (wrow + at) * 16);
-      we[u] = a.w_scales[wrow + at];
-    }
+  i32x4 w, x[kTiles];
+  int we, xe[kTiles];
+  auto request_w = [&](int s) {
+    // past the last block: the last one's weights, which meet zeros
+    const int at = min(4 * min(s, steps - 1) + q, a.blocks - 1);
+    w = *reinterpret_cast<const i32x4*>(a.w_codes + (wrow + at) * 16);
+    we = a.w_scales[wrow + at];
   };
-  auto request_x = [&](int s0) {
+  auto request_x = [&](int s) {
 #pragma unroll
-    for (int u = 0; u < kMxBatch; ++u) {
-      const int s = min(s0 + u, steps - 1);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        if (kFused) {
-          const int from = (min(l16, n_rows - 1) * steps + s) * 4 + q;
-          x[u][t] = reinterpret_cast<const i32x4*>(rows)[from];
-          xe[u][t] = rows[n_rows * steps * 64 + from];
-        } else {
-          const uint32_t from = (s * static_cast<uint32_t>((n_rows + 15) / 16) + t) * 64 + lane;
-          x[u][t] = reinterpret_cast<const i32x4*>(a.x_codes)[from];
-          xe[u][t] = a.x_scales[from];
-        }
+    for (int t = 0; t < kTiles; ++t) {
+      if (kFused) {
+        const int from = (min(l16, n_rows - 1) * steps + s) * 4 + q;
+        x[t] = reinterpret_cast<const i32x4*>(rows)[from];
+        xe[t] = rows[n_rows * steps * 64 + from];
+      } else {
+        const uint32_t from = (s * static_cast<uint32_t>((n_rows + 15) / 16) + t) * 64 + lane;
+        x[t] = reinterpret_cast<const i32x4*>(a.x_codes)[from];
+        xe[t] = a.x_scales[from];
       }
     }
   };
-  int s0 = wave * each;
-  request_w(s0);
+  int s = wave * each;
+  request_w(s);
   if (kFused) {
     const int quarters = 16 * steps;
     for (int i = tid; i < n_rows * quarters; i += 512) {
@@ -253,16 +229,11 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
     }
     __syncthreads();
   }
-  for (; s0 < end; s0 += kMxBatch) {
-    request_x(s0);
-    __builtin_amdgcn_sched_barrier(0);  // all of a batch on its way before the first product
+  for (; s < end; ++s) {
+    request_x(s);
 #pragma unroll
-    for (int u = 0; u < kMxBatch; ++u) {
-      if (s0 + u >= end) break;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) acc[t] = mma_mx(w[u], we[u], x[u][t], xe[u][t], acc[t]);
-    }
-    if (s0 + kMxBatch < end) request_w(s0 + kMxBatch);
+    for (int t = 0; t < kTiles; ++t) acc[t] = mma_mx(w, we, x[t], xe[t], acc[t]);
+    if (s + 1 < end) request_w(s + 1);
   }
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) sums[wave][t][lane] = acc[t];
@@ -288,7 +259,10 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
 // (mx_place_of), so that the eight rows that a read touches at a time take all eight.
 // The order along the reduction is free: lane group h of a wave takes the step's blocks 4 h .. 4 h + 3, whose scales are
 // one word. Outputs lie along the lanes, so that a store fills 64 bytes of a row (bf16); with rows along the lanes and 16
-// bytes of each a store the call below took 48 us for them.
+// bytes of each a store the products below took 48 us more.
+// 8192 x 4096 -> 4096, bf16: 75 us, 3.7 PFLOP/s, where 4-bit products with nothing else reach 6.5 to 7.5. What
+// is left is the start and end of each of two rounds of
+// tiles, in which no products run, and the stores (67 MB, 14 us at the memory's rate).
 // ---------------------------------------------------------------------------------------------
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 

@@ -36,7 +36,7 @@ cdrge_status check_rows(const cdrge_mx_config* c, int64_t n_rows, const void* x,
 int64_t quarter_groups(int64_t n_rows, int quarters, int* parts) {
   *parts = (quarters + 255) / 256;
   const int each = *parts > 1 ? 1 : 256 / quarters;
-  return ((n_rows + each - 1) / each * *parts + kMxGroups - 1) / kMxGroups;
+  return (n_rows + each - 1) / each * *parts;
 }
 
 constexpr int64_t kMostGroups = int64_t(1) << 35;  // 2^20 by 2^15 of a grid
@@ -67,7 +67,9 @@ struct Plan {
   size_t codes, scales, w_scales, total;
 };
 
-// Up to four rows are quantised by every workgroup of k_mx_rows, which saves a launch, where their codes fit in 32 KB.
+// Up to four rows are quantised by every workgroup of k_mx_rows, which saves a launch, where their codes fit in 34 KB:
+// 4096 -> 4096, one row 7.1 us and 10.2 with a launch for it, four 8.5 and 10.2, eight 10.3 both; 16384 -> 4096, one row
+// 14.8 and 17.6, four (2,048 blocks) 21.3 and 17.6.
 constexpr int kFusedBlocks = 2000;
 
 Plan make_plan(const cdrge_mx_config* c, int64_t n_rows) {
@@ -75,8 +77,12 @@ Plan make_plan(const cdrge_mx_config* c, int64_t n_rows) {
   p.blocks = blocks_of(c);
   p.steps = (p.blocks + 7) / 8;
   const int64_t r128 = (n_rows + 127) / 128, o128 = (c->out_features + 127) / 128;
+  // k_mx_rows takes up to 64 rows, whose codes every one of its workgroups reads, for 16 outputs: 64 rows, 4096 -> 4096, 11 us,
+  // and 21 by tiles, which are too few to fill the chip. With outputs for 256 tiles these are quicker: 4096 -> 32768, 17 rows
+  // 25 us by tiles and 28 by rows, 64 rows 26 and 37; -> 16384, 64 rows 23 both. Large tiles read half as much, but leave
+  // CUs idle below 256 of them: 8192 rows, 4096 -> 4096, 101 us and 112 with small ones, 2048 rows 45 and 34.
   p.fused = n_rows <= 4 && n_rows * p.blocks <= kFusedBlocks;
-  if (n_rows > 64) p.side = r128 * o128 >= 1024 ? 256 : 128;
+  if (n_rows > 64 || (n_rows > 16 && o128 >= 256)) p.side = r128 * o128 >= 1024 ? 256 : 128;
   if (p.side > 0) {
     p.tiles_r = static_cast<int>((n_rows + p.side - 1) / p.side);
     p.tiles_o = (c->out_features + p.side - 1) / p.side;
