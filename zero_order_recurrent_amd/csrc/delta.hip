@@ -98,8 +98,10 @@ struct Plan {
 // keys 53 us and 1.0 ms (64 sequences of 32 heads of 256 x 256). One sequence is quicker by blocks from 24 tokens on.
 int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 ? 32 : 16; }
 
-// A ragged batch may hold both kinds, which the host does not see: below this many tokens a sequence on average either
-// path is launched and leaves the other's sequences alone.
+// A ragged batch may hold both kinds, which the host does not see: up to this many tokens a sequence on average either
+// path is launched and leaves the other's sequences alone. 255 single tokens beside a prompt of 4,096 (32 heads of 128 x
+// 128, bf16) take 1.1 ms so and 2.3 by blocks alone; where most sequences are long the launch costs up to a tenth: 64
+// sequences of 8 heads, 7,000 tokens together, 200 and 178 us, 12,000 tokens 255 and 231.
 constexpr int kMixed = 128;
 
 template <class T>
@@ -180,10 +182,12 @@ cdrge_status launch_tokens(DeltaArgs a, const ScanWork& w, hipStream_t s) {
   return CDRGE_OK;
 }
 
-// Few rows take small tiles, as the scan's steps do.
+// Few rows take tiles of 16 rows of the state, more of them tiles of 64, by how many columns of 64 the small tiles hold.
+// Single tokens, 32 heads of 128 x 128: one row 6.9 us with small tiles and 7.1 with large ones, 4 rows 8.7 and 7.9, 16 rows
+// 19.3 and 14.4; of 256 x 256 2 rows 10.8 and 11.8; of 64 x 64 8 rows 8.1 and 6.8.
 template <class T, int kQuads, bool kStep>
 cdrge_status launch_tiles(const DeltaArgs& a, const ScanWork& w, hipStream_t s) {
-  if (int64_t(a.s.n_seqs) * a.s.H * ((a.s.P + 15) / 16) <= 1024) return launch_tokens<T, 16, kQuads, 1, kStep>(a, w, s);
+  if (int64_t(a.s.n_seqs) * a.s.H * ((a.s.P + 15) / 16) <= 256 * kQuads) return launch_tokens<T, 16, kQuads, 1, kStep>(a, w, s);
   return launch_tokens<T, 16, kQuads, 4, kStep>(a, w, s);
 }
 
