@@ -449,7 +449,10 @@ cdrge_status cdrge_delta_workspace_bytes(const cdrge_delta_config* cfg, int64_t 
 
 /* Whole prompts, or continued ones. Offsets, slots that are negative, out of range or named twice, and
  * rows outside every sequence: as for cdrge_scan_prompt. A token that is not finite may spoil outputs of
- * its own sequence from up to 63 tokens before it; other sequences are not affected. */
+ * its own sequence from up to 63 tokens before it; other sequences are not affected. Magnitudes past
+ * 2^100, of v, of the state or of its product with a row of k as it comes, count as not finite. Short
+ * sequences go token by token, others in blocks, by the call's sizes: the sums, in float32, have another
+ * order then. In bf16 what y is formed of is rounded to 16 bits, the state never is. */
 cdrge_status cdrge_delta_prompt(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
                                 const cdrge_delta_io* io, void* workspace, size_t workspace_bytes, void* stream);
 
@@ -519,12 +522,14 @@ cdrge_status cdrge_mx_quantize(const cdrge_mx_config* cfg, int64_t n_rows, const
 cdrge_status cdrge_mx_dequantize(const cdrge_mx_config* cfg, int64_t n_rows, const uint8_t* codes,
                                  const uint8_t* scales, void* x, int64_t x_stride, void* stream);
 
-/* Workspace, in bytes, of cdrge_mx_project for n_rows rows (256-byte aligned base required). */
+/* Workspace, in bytes, of cdrge_mx_project for n_rows rows (256-byte aligned base required); the
+ * largest of the calls' serves all of them on a stream. */
 cdrge_status cdrge_mx_workspace_bytes(const cdrge_mx_config* cfg, int64_t n_rows, size_t* bytes_out);
 
 /* y_r = W Q(x_r) + bias, with W the values of w_codes and w_scales [O][K] and Q(x_r) those of the row
  * quantised as by cdrge_mx_quantize. bias: T [O], or NULL; y: T [n_rows][O]. Products of codes are
- * exact and summed in float32. A row with a NaN or an infinity gives NaN; other rows are not affected. */
+ * exact and summed in float32. A row with a NaN or an infinity gives NaN; other rows are not affected.
+ * y must not overlap x. The workspace may be NULL where cdrge_mx_workspace_bytes says 0 (few rows). */
 cdrge_status cdrge_mx_project(const cdrge_mx_config* cfg, const uint8_t* w_codes, const uint8_t* w_scales,
                               const void* bias, int64_t n_rows, const void* x, int64_t x_stride, void* y,
                               int64_t y_stride, void* workspace, size_t workspace_bytes, void* stream);

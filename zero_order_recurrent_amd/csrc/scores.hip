@@ -35,7 +35,8 @@ cdrge_status launch(const ScoreArgs& a, hipStream_t s) {
 }
 
 // Threads of a row and pieces a thread: as for the distillation loss the fewest threads that hold the row in at most 8
-// pieces each, but where alternatives are asked for no fewer than there are of them, as far as the row has pieces.
+// pieces each, but where alternatives are asked for no fewer than there are of them, as far as the row has pieces, so that
+// the threads' largest logits bound them.
 template <class T, int kMode>
 cdrge_status launch_team(const ScoreArgs& a, hipStream_t s) {
   const int pieces = (a.vocab + DistillRow<T>::kPer - 1) / DistillRow<T>::kPer, least = std::min(a.top_k, pieces);
