@@ -89,6 +89,7 @@ struct Plan {
   int kn;       // key_dim as the kernels of blocks have it
   int max_blocks;
   bool direct;  // as in DeltaWork
+  bool pair;    // kPair of k_delta_heads
   size_t group_bytes;
   size_t slots, counts, start, bounds, block_of, piece_of, groups, heads, total;
 };
@@ -103,6 +104,8 @@ int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 ? 32 : 16;
 // 128, bf16) take 1.1 ms so and 2.3 by blocks alone; where most sequences are long the launch costs up to a tenth: 64
 // sequences of 8 heads, 7,000 tokens together, 200 and 178 us, 12,000 tokens 255 and 231.
 constexpr int kMixed = 128;
+
+constexpr int kCus = 256;
 
 template <class T>
 void block_bytes(int kn, size_t* keys, size_t* head) {
@@ -140,7 +143,8 @@ Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bo
       block_bytes<float>(p.kn, &keys, &head);
     else
       block_bytes<uint16_t>(p.kn, &keys, &head);
-    p.direct = c->dtype == CDRGE_BF16 && c->key_dim == p.kn;
+    p.pair = c->dtype == CDRGE_BF16 && p.kn == 128 && int64_t(n_seqs) * c->n_heads * ((c->value_dim + 15) / 16) > kCus;
+    p.direct = c->dtype == CDRGE_BF16 && c->key_dim == p.kn && !p.pair;
     p.group_bytes = (p.direct ? 1 : 3) * keys;
     p.groups = region(p.group_bytes * c->n_groups * blocks);
     p.heads = region(head * c->n_heads * blocks);
@@ -201,7 +205,7 @@ cdrge_status enqueue_tokens(const DeltaArgs& a, const ScanWork& w, hipStream_t s
 }
 
 template <class T, int kN>
-cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, hipStream_t s) {
+cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, bool pair, hipStream_t s) {
   using Block = DeltaBlock<T, kN>;
   a.s.ptiles = (a.s.P + 15) / 16;
   const int64_t n = int64_t(a.s.n_seqs) * a.s.H * a.s.ptiles;
@@ -223,10 +227,13 @@ cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, h
   }
   hipLaunchKernelGGL((k_delta_blocks<T, kN>), grid_of(int64_t(w.max_blocks) * a.s.H, 256), dim3(256), kLds, s, a, w, d);
   CDRGE_HIP(hipGetLastError());
-  if (sizeof(T) == 2 && d.direct)
-    hipLaunchKernelGGL((k_delta_heads<T, kN, sizeof(T) == 2>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
+  constexpr bool kRaw = sizeof(T) == 2;
+  if (kRaw && kN == 128 && pair)
+    hipLaunchKernelGGL((k_delta_heads<T, kN, false, kRaw && kN == 128>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
+  else if (kRaw && d.direct)
+    hipLaunchKernelGGL((k_delta_heads<T, kN, kRaw, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
   else
-    hipLaunchKernelGGL((k_delta_heads<T, kN, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
+    hipLaunchKernelGGL((k_delta_heads<T, kN, false, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
   CDRGE_HIP(hipGetLastError());
   return CDRGE_OK;
 }
@@ -244,7 +251,7 @@ cdrge_status enqueue_prompt(DeltaArgs a, const Plan& p, void* ws, hipStream_t s)
     if (st != CDRGE_OK || !p.long_ones) return st;
   }
   const DeltaWork d{static_cast<char*>(ws) + p.groups, static_cast<char*>(ws) + p.heads, static_cast<int64_t>(p.group_bytes), p.direct};
-  return p.kn == 128 ? launch_blocks<T, 128>(a, w, d, s) : launch_blocks<T, 256>(a, w, d, s);
+  return p.kn == 128 ? launch_blocks<T, 128>(a, w, d, p.pair, s) : launch_blocks<T, 256>(a, w, d, p.pair, s);
 }
 
 // Whether the call's sizes fit the kernels' 32-bit counts.

@@ -581,8 +581,13 @@ struct DeltaRows {
 // One sequence of 8,192 tokens, 32 heads of 128 x 128, bf16: 250 us, 1.95 us a block. That is the chain: of its 4,500
 // clocks one wave's instructions, the trips through LDS and three barriers take 3,300, waits for the next operands the rest
 // (0.2 GB of them by way of L2); its products alone would take 600.
-template <class T, int kN, bool kDirect>
-__global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
+// kPair, where there are more workgroups than CUs: two of them share a CU, in 128 registers each, so that one's steps hide
+// the other's waits. Operands are requested within the block then, and Q and K come by way of the workspace, whose addresses
+// are fewer. 32 sequences of 512 tokens, 32 heads of 128 x 128: 631 us and 793 without, 2 of 4,096 307 and 345; but one of
+// 8,192 more than 400 and 344, and in float32 or with 256 keys, which do not fit, 32 of 512 2,135 and 1,482, 32 of 256 1,012
+// and 709.
+template <class T, int kN, bool kDirect, bool kPair>
+__global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
   constexpr int kRaw = Block::kRaw, kOut = Block::kOut, kW = kN / 128, kSteps = kN / 32;
   __shared__ f32x4 ks_parts[4][4][64];           // [wave][strip]: parts of K S^T
@@ -622,7 +627,6 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
   const int64_t group_next = s.G * d.group_bytes, head_next = static_cast<int64_t>(s.H) * Block::kHeadBytes;
 
   if (wave < 4) {
-    __builtin_amdgcn_s_setprio(3);  // the chain, before what hangs on it
     f32x4 st[2 * kW];
     const int key0 = 32 * kW * wave + 8 * q;
     const int64_t place = ((static_cast<int64_t>(max(slot, 0)) * s.H + h) * s.P + p0 + l16) * N + key0;
@@ -653,7 +657,7 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
     DeltaRows<T, 4> values(v_rows, a.v_stride, sq.len, v_col, value_row);
     // K and its turned form together would take 192 registers for float32 and wide states: there they are requested when
     // the other one is done with
-    constexpr bool kAhead = kRaw * kW <= 3;
+    constexpr bool kAhead = kRaw * kW <= 3 && !kPair;
     bf16x8 kf[kW][4][kRaw], kt[2 * kW][2][kRaw], u[2][3];
     T vv[4];
     f32x4 fk, fe;
@@ -703,7 +707,7 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
         load_kt(group, head);
       }
       load_values(head);
-      load_u(head);
+      if (!kPair) load_u(head);
     }
     for (int b = 0; b < blocks; ++b) {
       const bool more = b + 1 < blocks;
@@ -730,9 +734,10 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
       if (kAhead) {
         if (kDirect) keys.to(b + 1, blocks, k_rows, a.k_stride, sq.len, key0, key_row);
         load_keys(group_then);
-      } else {
+      } else if (!kPair) {
         load_kt(group, head);
       }
+      if (kPair) load_u(head);
       __syncthreads();
       {
         f32x4 ks = ks_parts[0][wave][lane];
@@ -780,7 +785,8 @@ __global__ __launch_bounds__(512) void k_delta_heads(DeltaArgs a, ScanWork w, De
 #pragma unroll
         for (int o = 0; o < 3; ++o) __builtin_memcpy(reinterpret_cast<char*>(&wide[wave >> 1][o][lane]) + 8 * (wave & 1), np3.w[o], 8);
       }
-      load_u(head_then);
+      if (!kPair) load_u(head_then);
+      if (kPair) load_kt(group, head);
       __syncthreads();
       {
         Parts<3> np3[2];

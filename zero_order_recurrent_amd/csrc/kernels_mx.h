@@ -260,9 +260,8 @@ __global__ __launch_bounds__(512) void k_mx_rows(MxArgs a) {
 // The order along the reduction is free: lane group h of a wave takes the step's blocks 4 h .. 4 h + 3, whose scales are
 // one word. Outputs lie along the lanes, so that a store fills 64 bytes of a row (bf16); with rows along the lanes and 16
 // bytes of each a store the products below took 48 us more.
-// 8192 x 4096 -> 4096, bf16: 75 us, 3.7 PFLOP/s, where 4-bit products with nothing else reach 6.5 to 7.5. What
-// is left is the start and end of each of two rounds of
-// tiles, in which no products run, and the stores (67 MB, 14 us at the memory's rate).
+// 8192 x 4096 -> 4096, bf16: 75 us, 3.7 PFLOP/s, where 4-bit products with nothing else reach 6.5 to 7.5. What is left is the
+// start and end of each of two rounds of tiles, in which no products run, and the stores (67 MB, 14 us at the memory's rate).
 // ---------------------------------------------------------------------------------------------
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
