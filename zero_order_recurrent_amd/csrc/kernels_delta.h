@@ -335,7 +335,7 @@ __device__ __forceinline__ void store_lds(float* to, f32x4 d, float sign) {
 
 // One block of a head: a wave takes 16 tokens. The first head of a group writes the group's operands. The inverse goes from
 // blocks of 16, by substitution in registers, to 32 and 64 by products in float32, as its entries grow with the block where
-// keys are alike. 128 blocks of 32 heads of 128 x 128, bf16: 84 us; float32, 160 blocks of 14 heads of 40 x 100: 125 us,
+// keys are alike. 128 blocks of 32 heads of 128 x 128, bf16: 87 us; float32, 160 blocks of 14 heads of 40 x 100: 125 us,
 // with six products for one. Bound by its dependent steps and nine barriers, with two workgroups a CU, not by memory.
 template <class T, int kN>
 __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, DeltaWork d) {
@@ -578,7 +578,7 @@ struct DeltaRows {
 // 32 (kW n + t / 2) + 8 q + 4 (t % 2) + r, tile t, and value l16, and takes a block's tokens 16 n + 4 q + r, as does wave 4 + n
 // for y. An operand is requested again, for the next block, when this block has used it. 16 values of a head are a
 // workgroup, since the rows of S do not wait for each other: 32 heads of 128 values fill the 256 CUs with one sequence.
-// One sequence of 8,192 tokens, 32 heads of 128 x 128, bf16: 250 us, 1.95 us a block. That is the chain: of its 4,500
+// One sequence of 8,192 tokens, 32 heads of 128 x 128, bf16: 248 us, 1.95 us a block. That is the chain: of its 4,500
 // clocks one wave's instructions, the trips through LDS and three barriers take 3,300, waits for the next operands the rest
 // (0.2 GB of them by way of L2); its products alone would take 600.
 // kPair, where there are more workgroups than CUs: two of them share a CU, in 128 registers each, so that one's steps hide
