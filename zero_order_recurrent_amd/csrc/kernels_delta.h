@@ -583,9 +583,9 @@ struct DeltaRows {
 // (0.2 GB of them by way of L2); its products alone would take 600.
 // kPair, where there are more workgroups than CUs: two of them share a CU, in 128 registers each, so that one's steps hide
 // the other's waits. Operands are requested within the block then, and Q and K come by way of the workspace, whose addresses
-// are fewer. 32 sequences of 512 tokens, 32 heads of 128 x 128: 631 us and 793 without, 2 of 4,096 307 and 345; but one of
-// 8,192 more than 400 and 344, and in float32 or with 256 keys, which do not fit, 32 of 512 2,135 and 1,482, 32 of 256 1,012
-// and 709.
+// are fewer. 32 heads of 128 x 128, bf16: 32 sequences of 512 tokens 631 us and 793 without (698 with Q and K as they lie), 2
+// of 4,096 307 and 345, but one of 8,192 more than 400 and 344; with 256 keys 8 of 1,024 482 and 574; in float32 32 of 512
+// 1,347 and 1,482, but with 256 keys, whose operands do not fit, 32 of 256 2,237 and 1,311.
 template <class T, int kN, bool kDirect, bool kPair>
 __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
