@@ -452,7 +452,7 @@ cdrge_status cdrge_delta_workspace_bytes(const cdrge_delta_config* cfg, int64_t 
  * its own sequence from up to 63 tokens before it; other sequences are not affected. Magnitudes past
  * 2^100, of v, of the state or of its product with a row of k as it comes, count as not finite. Short
  * sequences go token by token, others in blocks, by the call's sizes: the sums, in float32, have another
- * order then. In bf16 what y is formed of is rounded to 16 bits, the state never is. */
+ * order then. */
 cdrge_status cdrge_delta_prompt(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
                                 const cdrge_delta_io* io, void* workspace, size_t workspace_bytes, void* stream);
 

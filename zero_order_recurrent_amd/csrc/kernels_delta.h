@@ -237,11 +237,11 @@ __global__ __launch_bounds__(256) void k_delta_tokens(DeltaArgs a, ScanWork w) {
 // rest, and N'. Four further waves form y from S and N', beside that chain.
 //
 // Operands of the matrix cores are bf16 (K, Q of bf16 tensors as they are), others the sum of three bf16 parts, which
-// hold 24 bits whatever the magnitude; of two such operands the six products that reach 2^-24 are taken. The state and what
-// tokens write always have three. For y in bf16 its operands have two (16 bits): y's distance from the formula, in the
-// 2-norm, is that of its own rounding, 0.0017, with two parts and with three, which take 367 us instead of 340 for one
-// sequence of 8,192 tokens (below) and 830 instead of 793 for 32 of 512. Parts end where float32 does: magnitudes past
-// 2^100 may come out infinite, and below 2^-100 some bits are lost.
+// hold 24 bits whatever the magnitude; of two such operands the six products that reach 2^-24 are taken. So is y in bf16,
+// which comes out as a neighbour of the value nearest to the exact one in 0.014 % of its elements, 2.4e-5 of y in the 2-norm,
+// as for single tokens. With two parts for what y is formed of that was 0.33 % and 1.2e-4, and one sequence of 8,192 tokens
+// (below) took 343 us instead of 368, 32 of 512 632 instead of 649. Parts end where float32 does: magnitudes past 2^100 may
+// come out infinite, and below 2^-100 some bits are lost.
 //
 // Along a reduction the order is free if both operands have it, and so is that of a result's rows. Keys: entry e of lane
 // group q is key 8 q + e of 32, and row m of a state's tile t is key 8 (m / 4) + 4 t + m % 4. Tokens: entry e of lane
@@ -269,29 +269,18 @@ struct Parts {
   }
 };
 
-// c[m] + a[m] b for kM operands a, the products of parts that reach 2^(-8 kReach), small ones first. Products with sums of
-// their own stand next to each other.
-template <int kReach, int kM, int kA, int kB>
-__device__ __forceinline__ void mma_parts(const bf16x8 (&a)[kM][kA], const Parts<kB>& b, f32x4 (&c)[kM]) {
+// c[m] + a[m] b for kM operands a, the products of parts that reach 2^-24, small ones first. Products with sums of their own
+// stand next to each other.
+template <int kM, int kA>
+__device__ __forceinline__ void mma_parts(const bf16x8 (&a)[kM][kA], const Parts<3>& b, f32x4 (&c)[kM]) {
 #pragma unroll
-  for (int s = kReach - 1; s >= 0; --s)
+  for (int s = 2; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < kA; ++i)
 #pragma unroll
       for (int m = 0; m < kM; ++m)
-        if (s - i >= 0 && s - i < kB) c[m] = mma_bf16(a[m][i], b.part(s - i), c[m]);
+        if (s - i >= 0) c[m] = mma_bf16(a[m][i], b.part(s - i), c[m]);
 }
-
-template <class T>
-struct DeltaParts;  // parts of K and Q, of y's operands
-template <>
-struct DeltaParts<float> {
-  static constexpr int kRaw = 3, kOut = 3;
-};
-template <>
-struct DeltaParts<uint16_t> {
-  static constexpr int kRaw = 1, kOut = 2;
-};
 
 // What k_delta_blocks leaves, as operands of 1 KB (16 bytes a lane).
 //   for a block and group  kt     [tile kN / 16][step 2][part]: keys of a state's tile, tokens of the step
@@ -301,9 +290,9 @@ struct DeltaParts<uint16_t> {
 //                          factors: e^G r, e^G s and e^(G_last - G) of 64 tokens each, e^G_last
 template <class T, int kN>
 struct DeltaBlock {
-  static constexpr int kRaw = DeltaParts<T>::kRaw, kOut = DeltaParts<T>::kOut;
+  static constexpr int kRaw = sizeof(T) == 2 ? 1 : 3;         // parts of K and Q; all other operands have three
   static constexpr int kKeys = 1024 * (kN / 32) * 4 * kRaw;  // of kt, of k and of q
-  static constexpr int kOffP = 6 * 3 * 1024, kOffFactors = kOffP + 6 * kOut * 1024, kHeadBytes = kOffFactors + 1024;
+  static constexpr int kOffP = 6 * 3 * 1024, kOffFactors = 2 * kOffP, kHeadBytes = kOffFactors + 1024;
 };
 __host__ __device__ constexpr int delta_pair(int strip, int step) { return strip + (strip > 2) + step; }
 
@@ -340,7 +329,7 @@ __device__ __forceinline__ void store_lds(float* to, f32x4 d, float sign) {
 template <class T, int kN>
 __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
-  constexpr int kRaw = Block::kRaw, kOut = Block::kOut, kSteps = kN / 32;
+  constexpr int kRaw = Block::kRaw, kSteps = kN / 32;
   extern __shared__ __align__(16) char lds[];
   bf16x8* const kl = reinterpret_cast<bf16x8*>(lds);  // [strip][step][part][lane]
   float* const lm = reinterpret_cast<float*>(lds + 4 * kSteps * kRaw * 1024);
@@ -469,12 +458,12 @@ __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, D
         p[r] = j <= i ? rq * qkt[r] * fall : 0.f;
       }
       if (strip <= wave) *reinterpret_cast<f32x4*>(lm + i * kDeltaRow + 16 * strip + 4 * q) = low;
-      Parts<kOut> pp;
+      Parts<3> pp;
       pp.set(0, p[0], p[1]);
       pp.set(1, p[2], p[3]);
 #pragma unroll
-      for (int o = 0; o < kOut; ++o)
-        __builtin_memcpy(head + Block::kOffP + (delta_pair(wave, strip >> 1) * kOut + o) * 1024 + lane * 16 + 8 * (strip & 1), pp.w[o], 8);
+      for (int o = 0; o < 3; ++o)
+        __builtin_memcpy(head + Block::kOffP + (delta_pair(wave, strip >> 1) * 3 + o) * 1024 + lane * 16 + 8 * (strip & 1), pp.w[o], 8);
     }
   }
   if (first) {  // K on its side
@@ -589,9 +578,9 @@ struct DeltaRows {
 template <class T, int kN, bool kDirect, bool kPair>
 __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
-  constexpr int kRaw = Block::kRaw, kOut = Block::kOut, kW = kN / 128, kSteps = kN / 32;
+  constexpr int kRaw = Block::kRaw, kW = kN / 128, kSteps = kN / 32;
   __shared__ f32x4 ks_parts[4][4][64];           // [wave][strip]: parts of K S^T
-  __shared__ uint4 state[kSteps][kOut][64];      // S as y's operand
+  __shared__ uint4 state[kSteps][3][64];      // S as y's operand
   __shared__ uint4 rest[2][3][64], wide[2][3][64];  // [step][part]: V's rest, N' faded
   __shared__ f32x4 news[4][64];                  // [strip]: N'
   const ScanArgs& s = a.s;
@@ -722,11 +711,11 @@ __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a,
 #pragma unroll
           for (int e = 0; e < 8; e += 2) sp.set(e >> 1, st[2 * n + (e >> 2)][e & 3], st[2 * n + (e >> 2)][(e & 3) + 1]);
 #pragma unroll
-          for (int o = 0; o < kOut; ++o) __builtin_memcpy(&state[kW * wave + n][o][lane], sp.w[o], 16);
+          for (int o = 0; o < 3; ++o) __builtin_memcpy(&state[kW * wave + n][o][lane], sp.w[o], 16);
           if (n == 0)
 #pragma unroll
             for (int t = 0; t < 4; ++t) ks[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-          mma_parts<3>(kf[n], sp, ks);
+          mma_parts(kf[n], sp, ks);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) ks_parts[wave][t][lane] = ks[t];
@@ -832,7 +821,7 @@ __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a,
   const T* const q_rows = static_cast<const T*>(a.q) + sq.first * a.q_stride + static_cast<int64_t>(g) * N;
   auto query_row = [&](int) { return 16 * strip + l16; };
   DeltaRows<T, 1> queries(q_rows, a.q_stride, sq.len, 8 * q, query_row);
-  bf16x8 qf[kSteps][1][kRaw], p[2][kOut];
+  bf16x8 qf[kSteps][1][kRaw], p[2][3];
   f32x4 fq;
   auto load_queries = [&](const char* group, const char* head) {
     if (kDirect) {
@@ -848,12 +837,12 @@ __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a,
     fq = *reinterpret_cast<const f32x4*>(head + Block::kOffFactors + 256 + (16 * strip + 4 * q) * 4);
   };
   auto load_p = [&](const char* head) {
-    const bf16x8* const from = reinterpret_cast<const bf16x8*>(head + Block::kOffP) + delta_pair(strip, 0) * kOut * 64;
+    const bf16x8* const from = reinterpret_cast<const bf16x8*>(head + Block::kOffP) + delta_pair(strip, 0) * 3 * 64;
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int o = 0; o < kOut; ++o)
-        if (n <= strip >> 1) p[n][o] = from[(n * kOut + o) * 64 + lane];
+      for (int o = 0; o < 3; ++o)
+        if (n <= strip >> 1) p[n][o] = from[(n * 3 + o) * 64 + lane];
   };
   if (blocks > 0) {
     load_queries(group, head);
@@ -871,10 +860,10 @@ __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a,
     sums[0][0] = sums[1][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
-      Parts<kOut> sp;
+      Parts<3> sp;
 #pragma unroll
-      for (int o = 0; o < kOut; ++o) __builtin_memcpy(sp.w[o], &state[n][o][lane], 16);
-      mma_parts<kOut>(qf[n], sp, sums[n & 1]);
+      for (int o = 0; o < 3; ++o) __builtin_memcpy(sp.w[o], &state[n][o][lane], 16);
+      mma_parts(qf[n], sp, sums[n & 1]);
     }
     f32x4 yy = (sums[0][0] + sums[1][0]) * fq;
     if (kDirect) queries.to(b + 1, blocks, q_rows, a.q_stride, sq.len, 8 * q, query_row);
@@ -884,13 +873,13 @@ __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a,
     for (int n = 0; n < 2; ++n) {
       if (n > strip >> 1) break;
       const f32x4 n0 = news[2 * n][lane], n1 = news[2 * n + 1][lane];
-      Parts<kOut> np;
+      Parts<3> np;
       np.set(0, n0[0], n0[1]);
       np.set(1, n0[2], n0[3]);
       np.set(2, n1[0], n1[1]);
       np.set(3, n1[2], n1[3]);
 #pragma unroll
-      for (int r = kOut - 1; r >= 0; --r)
+      for (int r = 2; r >= 0; --r)
 #pragma unroll
         for (int o = 0; o <= r; ++o) yy = mma_bf16(p[n][o], np.part(r - o), yy);
     }
