@@ -169,13 +169,14 @@ __global__ __launch_bounds__(distill_threads(kTeam), score_waves(kTeam, kPieces)
   constexpr float kLn2 = 0.693147180559945309417f;
   const float rest = sums[0] + (sums[2] - 1.f), total = 1.f + rest, log_total = log1pf(rest);
   const bool bad = !(fabsf(top) < __builtin_inff()) || !(rest < __builtin_inff());
-  const float entropy = bad ? nan : log_total - kLn2 * (sums[1] / total);
+  const float apart = -kLn2 * (sums[1] / total);  // the mean distance from the largest: log p_v + entropy = d_v + apart
+  const float entropy = bad ? nan : log_total + apart;
   const float logprob = token < 0 ? 0.f : (bad || !inside ? nan : (chosen - top) * inv_tau - log_total);
 
   if (kGrad) {
     const bool spoilt = bad || (up_l != 0.f && !inside);
-    // -p (up_l + up_h (log p + entropy)) / tau, with log p = d ln 2 - log_total
-    const float c0 = spoilt ? nan : -inv_tau / total * (up_l + up_h * (entropy - log_total)), c1 = -inv_tau / total * up_h * kLn2;
+    // -p (up_l + up_h (log p + entropy)) / tau, without log_total, in which the distances of a flat row would be lost
+    const float c0 = spoilt ? nan : -inv_tau / total * (up_l + up_h * apart), c1 = -inv_tau / total * up_h * kLn2;
     each([&](uint4 r, int b) {
       T v[kPer];
       __builtin_memcpy(v, &r, 16);
@@ -189,7 +190,7 @@ __global__ __launch_bounds__(distill_threads(kTeam), score_waves(kTeam, kPieces)
     });
     // the given token's, by the thread that has just written its piece: 1 - p is not formed by subtraction
     if (inside && !spoilt && up_l != 0.f && lane == token / kPer % kTeam)
-      dx[token] = from_float<T>(-inv_tau * (up_l * expm1f(logprob) + up_h * expf(logprob) * (logprob == ninf ? 0.f : logprob + entropy)));
+      dx[token] = from_float<T>(-inv_tau * (up_l * expm1f(logprob) + up_h * expf(logprob) * (logprob == ninf ? 0.f : (chosen - top) * inv_tau + apart)));
     return;
   }
   if (lane == 0) {
