@@ -1,6 +1,6 @@
 """The gated delta rule's prompts by the 2-norm of their errors, by each of their kernels.
 
-Which kernels a call takes goes by its type, its keys (up to 128, or more; exactly 128 or 256 in bf16 read where they lie),
+Which kernels a call takes goes by its type, its keys (up to 128, or more; exactly 128 in bf16 read where they lie),
 and its workgroups, one for each sequence, head and 16 values: up to 256 of them or more.
 """
 import pytest

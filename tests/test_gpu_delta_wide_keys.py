@@ -1,4 +1,4 @@
-"""Prompts with more than 128 keys in calls of few workgroups, where bf16 keys of exactly 256 are read where they lie."""
+"""Prompts with more than 128 keys in calls of few workgroups, one on a CU."""
 import pytest
 
 import test_gpu_delta as delta

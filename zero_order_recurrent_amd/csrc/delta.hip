@@ -144,7 +144,7 @@ Plan make_plan(const cdrge_delta_config* c, int64_t n_tokens, int32_t n_seqs, bo
     else
       block_bytes<uint16_t>(p.kn, &keys, &head);
     p.pair = (c->dtype == CDRGE_BF16 || p.kn == 128) && int64_t(n_seqs) * c->n_heads * ((c->value_dim + 15) / 16) > kCus;
-    p.direct = c->dtype == CDRGE_BF16 && c->key_dim == p.kn && !p.pair;
+    p.direct = c->dtype == CDRGE_BF16 && c->key_dim == 128 && !p.pair;
     p.group_bytes = (p.direct ? 1 : 3) * keys;
     p.groups = region(p.group_bytes * c->n_groups * blocks);
     p.heads = region(head * c->n_heads * blocks);
@@ -227,11 +227,11 @@ cdrge_status launch_blocks(DeltaArgs a, const ScanWork& w, const DeltaWork& d, b
   }
   hipLaunchKernelGGL((k_delta_blocks<T, kN>), grid_of(int64_t(w.max_blocks) * a.s.H, 256), dim3(256), kLds, s, a, w, d);
   CDRGE_HIP(hipGetLastError());
-  constexpr bool kRaw = sizeof(T) == 2, kPair = kRaw || kN == 128;
+  constexpr bool kPair = sizeof(T) == 2 || kN == 128, kDirect = sizeof(T) == 2 && kN == 128;
   if (kPair && pair)
     hipLaunchKernelGGL((k_delta_heads<T, kN, false, kPair>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
-  else if (kRaw && d.direct)
-    hipLaunchKernelGGL((k_delta_heads<T, kN, kRaw, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
+  else if (kDirect && d.direct)
+    hipLaunchKernelGGL((k_delta_heads<T, kN, kDirect, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
   else
     hipLaunchKernelGGL((k_delta_heads<T, kN, false, false>), grid_of(n, 512), dim3(512), 0, s, a, w, d);
   CDRGE_HIP(hipGetLastError());

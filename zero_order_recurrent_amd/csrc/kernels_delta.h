@@ -300,8 +300,9 @@ struct DeltaWork {
   char* groups;  // [block][group]
   char* heads;   // [block][head]
   int64_t group_bytes;
-  // K and Q in bf16 with rows of kN keys are operands as they lie: k_delta_heads reads the tensors (one sequence of 8,192
-  // tokens, 32 heads of 128 x 128: 342 us, and 364 by way of the workspace)
+  // K and Q in bf16 with rows of 128 keys are operands as they lie: k_delta_heads reads the tensors (one sequence of 8,192
+  // tokens, 32 heads of 128 x 128: 368 us, and 399 by way of the workspace). Rows of 256 keys, which are twice the addresses,
+  // go by way of it (one of 4,096, 16 heads of 256 x 256: 196 us, and 220 as they lie; one of 8,192, 8 heads: 323 and 388)
   bool direct;
 };
 
