@@ -94,10 +94,14 @@ struct Plan {
   size_t slots, counts, start, bounds, block_of, piece_of, groups, heads, total;
 };
 
-// Sequences that are taken token by token. A block of 64 tokens costs the same however few it holds: 256 sequences of 32
-// heads of 128 x 128, bf16, take 29 us a token, and 1.35 ms by blocks (float32 29 us and 2.3 ms; 16 x 16 4 and 306); wider
-// keys 53 us and 1.0 ms (64 sequences of 32 heads of 256 x 256). One sequence is quicker by blocks from 24 tokens on.
-int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 ? 32 : 16; }
+// Sequences that are taken token by token. A block of 64 tokens costs the same however few it holds. 32 heads of 128 x 128,
+// bf16, 32 tokens: one sequence 24 us and 19 by blocks, 8 of them 45 and 43, 64 244 and 253, 256 916 and 1,038; 40 tokens: 8
+// 53 and 43, 64 297 and 262. In float32, where blocks take twice as long, with 256 keys too (32 heads of 128 values): 32 tokens,
+// one sequence 32 us and 33, 8 68 and 96, 64 436 and 871. In bf16 with 256 keys 16 tokens: one 30 and 23, 8 48 and 55, 64 362 and
+// 413; 24 tokens: 8 68 and 55, 64 507 and 417. The border does not go by the number of sequences: one would be 5 us quicker by
+// blocks at it, and many narrow or float32 ones of 33 to 64 tokens token by token (256 sequences of 16 heads of 64 x 64, float32,
+// 40 tokens: 211 us so and 635 by blocks; bf16 214 and 326).
+int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 || c->dtype == CDRGE_F32 ? 32 : 16; }
 
 // A ragged batch may hold both kinds, which the host does not see: up to this many tokens a sequence on average either
 // path is launched and leaves the other's sequences alone. 255 single tokens beside a prompt of 4,096 (32 heads of 128 x
