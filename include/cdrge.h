@@ -509,7 +509,7 @@ typedef struct {
   uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
   int32_t dtype;        /* type T of rows that are not quantised: CDRGE_F32 or CDRGE_BF16 */
   int32_t in_features;  /* K, 1 .. 2^20 */
-  int32_t out_features; /* O, 1 .. 2^20 (cdrge_mx_project only) */
+  int32_t out_features; /* O, 1 .. 2^20 (used by cdrge_mx_project alone, checked by every call) */
 } cdrge_mx_config;
 
 /* x: T [n_rows][K]; codes: uint8 [n_rows][16 * ceil(K / 32)], 16-byte aligned; scales: uint8 [n_rows]

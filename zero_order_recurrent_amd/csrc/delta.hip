@@ -104,9 +104,10 @@ struct Plan {
 int short_len(const cdrge_delta_config* c) { return c->key_dim <= 128 || c->dtype == CDRGE_F32 ? 32 : 16; }
 
 // A ragged batch may hold both kinds, which the host does not see: up to this many tokens a sequence on average either
-// path is launched and leaves the other's sequences alone. 255 single tokens beside a prompt of 4,096 (32 heads of 128 x
-// 128, bf16) take 1.1 ms so and 2.3 by blocks alone; where most sequences are long the launch costs up to a tenth: 64
-// sequences of 8 heads, 7,000 tokens together, 200 and 178 us, 12,000 tokens 255 and 231.
+// path is launched and leaves the other's sequences alone. 255 single tokens beside a prompt of 512 (32 heads of 128 x 128,
+// bf16) take 375 us so and 1,044 by blocks alone, beside one of 4,096 888 and 1,734. Lengths that differ less lose by the second
+// launch: 64 sequences of 8 heads, 2,000 tokens together, 107 and 78 us, 7,000 168 and 145, 256 with 20,000 429 and 411; 64 with
+// 12,000, past the border, 214 and 190.
 constexpr int kMixed = 128;
 
 constexpr int kCus = 256;

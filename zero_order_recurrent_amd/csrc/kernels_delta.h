@@ -325,8 +325,9 @@ __device__ __forceinline__ void store_lds(float* to, f32x4 d, float sign) {
 
 // One block of a head: a wave takes 16 tokens. The first head of a group writes the group's operands. The inverse goes from
 // blocks of 16, by substitution in registers, to 32 and 64 by products in float32, as its entries grow with the block where
-// keys are alike. 128 blocks of 32 heads of 128 x 128, bf16: 87 us; float32, 160 blocks of 14 heads of 40 x 100: 125 us,
-// with six products for one. Bound by its dependent steps and nine barriers, with two workgroups a CU, not by memory.
+// keys are alike. 128 blocks of 32 heads of 128 x 128, bf16: 88 us; float32, 160 blocks of 14 heads of 40 x 100: 125 us,
+// with six products for one. Bound by its dependent steps and nine barriers, not by memory: LDS holds three workgroups a CU in
+// bf16 (two with more than 128 keys) and one in float32.
 template <class T, int kN>
 __global__ __launch_bounds__(256) void k_delta_blocks(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;
@@ -568,14 +569,20 @@ struct DeltaRows {
 // 32 (kW n + t / 2) + 8 q + 4 (t % 2) + r, tile t, and value l16, and takes a block's tokens 16 n + 4 q + r, as does wave 4 + n
 // for y. An operand is requested again, for the next block, when this block has used it. 16 values of a head are a
 // workgroup, since the rows of S do not wait for each other: 32 heads of 128 values fill the 256 CUs with one sequence.
-// One sequence of 8,192 tokens, 32 heads of 128 x 128, bf16: 248 us, 1.95 us a block. That is the chain: of its 4,500
-// clocks one wave's instructions, the trips through LDS and three barriers take 3,300, waits for the next operands the rest
-// (0.2 GB of them by way of L2); its products alone would take 600.
+// One sequence of 8,192 tokens, 32 heads of 128 x 128, bf16: 272 us, 2.1 us a block. That is the chain: with y of two parts,
+// whose waves hold it up less, it took 4,500 clocks a block, of which one wave's instructions, the trips through LDS and three
+// barriers took 3,300 and waits for the next operands the rest (0.2 GB of them by way of L2); its products alone would take
+// 600. With sequences enough to hide the chain it is the operands, 84 KB of a block in bf16 and 180 in float32, which every
+// workgroup of 16 values reads again.
+// A sequence's workgroups follow each other in the order that fills an XCD after the other, so that one long sequence among
+// short ones has 32 CUs: 4,096 tokens beside 255 single ones, 32 heads of 128 x 128, bf16, take 888 us, alone 176.
 // kPair, where there are more workgroups than CUs: two of them share a CU, in 128 registers each, so that one's steps hide
 // the other's waits. Operands are requested within the block then, and Q and K come by way of the workspace, whose addresses
-// are fewer. 32 heads of 128 x 128, bf16: 32 sequences of 512 tokens 631 us and 793 without (698 with Q and K as they lie), 2
-// of 4,096 307 and 345, but one of 8,192 more than 400 and 344; with 256 keys 8 of 1,024 482 and 574; in float32 32 of 512
-// 1,347 and 1,482, but with 256 keys, whose operands do not fit, 32 of 256 2,237 and 1,311.
+// are fewer; 4 registers go to scratch in float32, 6 with 256 keys. 32 heads of 128 x 128, bf16: 32 sequences of 512 tokens
+// 649 us, without 832 and with Q and K by way of the workspace 863; 2 of 4,096 320 and 366, but one of 8,192 400 and 368; with
+// 256 keys 8 of 1,024 475 and 548; in float32 32 of 512 1,348 and 1,482, but with 256 keys, whose operands do not fit, 32 of
+// 256 2,237 and 1,311. It goes by the call's sequences, though not all of a ragged batch need have blocks: the 4,096 tokens
+// beside 255 single ones take 1,222 us without, one of 8,192 beside a single one 517 and 607.
 template <class T, int kN, bool kDirect, bool kPair>
 __global__ __launch_bounds__(512, kPair ? 4 : 2) void k_delta_heads(DeltaArgs a, ScanWork w, DeltaWork d) {
   using Block = DeltaBlock<T, kN>;

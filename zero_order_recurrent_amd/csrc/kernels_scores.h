@@ -55,8 +55,11 @@ enum ScoreMode { kScoreOnly, kScoreTop, kScoreGrad };  // what a launch writes: 
 
 // One row by kTeam threads, in registers or, with kPieces = 0, read again for each pass (as in k_distill). 4,096 rows of
 // 32,768 bf16 logits: 70 us (3.8 TB/s), of which the exponentials' instructions overlap the reading; with 64 alternatives 104;
-// gradient 114 (4.7 TB/s). 10,240 rows of 50 float32 logits: 7.0 us with five alternatives; 48 rows of 32,768 with 20: 14 us,
-// a row's latency.
+// gradient 112 (4.8 TB/s); in float32 98, 209 and 193. 10,240 rows of 50 float32 logits: 7.0 us with five alternatives; 48 rows
+// of 32,768 with 20: 14 us, a row's latency. Rows of more than 16 pieces for each of 1,024 threads are read up to three times, by
+// one CU each: 64 rows of 300,007 bf16 logits with 20 alternatives 71 us, 0.5 TB/s. With alternatives, 1,024 threads with 8
+// pieces each (32,769 to 65,536 bf16 logits, half as many in float32, or more than 512 alternatives) keep 14 to 16 registers in
+// scratch, 256 and 512 threads of a bf16 row 2.
 //
 // Alternatives: the k-th largest of the threads' largest logits, or one a little below it, bounds the k largest of all from
 // below. What lies above the bound, 1.1 to 1.6 k logits of a row without order, goes into LDS and takes its place by

@@ -1,5 +1,5 @@
-// What the kernels of the scan, the adapters and the distillation loss share: element types,
-// conversions, matrix-core fragments in 32-bit and split 16-bit precision, reductions over a wave.
+// What the operators' kernels share (scan, adapters, distillation loss, delta rule, token scores, 4-bit projections): element
+// types, conversions, matrix-core fragments, loads past the caches and into LDS, grids, reductions over a wave.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
