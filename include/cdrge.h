@@ -397,7 +397,9 @@ cdrge_status cdrge_distill_grad(const cdrge_distill_config* cfg, int64_t n_rows,
  *   y_t = S_t q'_t
  *
  * The squares of a row of q or k must sum to less than 2^127 (magnitudes up to 2^59 always do); a row
- * past that counts as not finite. */
+ * past that counts as not finite, and so do magnitudes past 2^100 of v, of the state or of its product
+ * with a row of q (for y alone) or of k as it comes. Of v, of the state and of v over the length of its
+ * row of k, what is below 2^-100 may lose bits. */
 typedef struct {
   uint32_t abi_version; /* must be CDRGE_ABI_VERSION */
   int32_t dtype;        /* CDRGE_F32 or CDRGE_BF16 */
@@ -449,10 +451,8 @@ cdrge_status cdrge_delta_workspace_bytes(const cdrge_delta_config* cfg, int64_t 
 
 /* Whole prompts, or continued ones. Offsets, slots that are negative, out of range or named twice, and
  * rows outside every sequence: as for cdrge_scan_prompt. A token that is not finite may spoil outputs of
- * its own sequence from up to 63 tokens before it; other sequences are not affected. Magnitudes past
- * 2^100, of v, of the state or of its product with a row of k as it comes, count as not finite. Short
- * sequences go token by token, others in blocks, by the call's sizes: the sums, in float32, have another
- * order then. */
+ * its own sequence from up to 63 tokens before it; other sequences are not affected. Short sequences go
+ * token by token, others in blocks, by the call's sizes: the sums, in float32, have another order then. */
 cdrge_status cdrge_delta_prompt(const cdrge_delta_config* cfg, const cdrge_delta_weights* weights,
                                 const cdrge_delta_io* io, void* workspace, size_t workspace_bytes, void* stream);
 
