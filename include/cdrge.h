@@ -492,7 +492,8 @@ cdrge_status cdrge_token_scores(const cdrge_score_config* cfg, int64_t n_rows, c
  * d_logprob, d_entropy: float32 [n_rows], either may be NULL (0; tokens may be NULL where d_logprob
  * is); d_logprob counts as zero where the token is padding. Where both are zero the row's gradient is
  * zero whatever it holds; otherwise a row that has NaN above, or a token of vocab or more with a
- * d_logprob that is not zero, gives NaN. dlogits may be logits itself (same pointer and stride). */
+ * d_logprob that is not zero, gives NaN. Factors past 2^100 times the temperature count as not finite.
+ * dlogits may be logits itself (same pointer and stride). */
 cdrge_status cdrge_token_scores_grad(const cdrge_score_config* cfg, int64_t n_rows, const void* logits,
                                      int64_t logits_stride, const int32_t* tokens, const float* d_logprob,
                                      const float* d_entropy, void* dlogits, int64_t dlogits_stride, void* stream);
